@@ -405,6 +405,97 @@ int pgemm_diag_parts(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
                      int tile_k, int stages, int parts, int64_t* clock, int64_t clock_len,
                      void* stream);
 
+/* ---- Feed-forward operators --------------------------------------------------
+ *
+ * A matrix product with a fused epilogue, the gated feed-forward block, and
+ * their backward passes, on row-major activations X[M][K] (one row per
+ * token).  fp32, fp16 and bf16 operands (PGEMM_I8 returns
+ * PGEMM_ERR_UNSUPPORTED_DTYPE), fp32 accumulation; every output is rounded
+ * once, to nearest even, from fp32.
+ *
+ *   linear         Z = X W + b            Y = act(Z) + R
+ *   gated          G = X Wg + bg          U = X Wu + bu          H = act(G) * U
+ *   linear backward   dZ = dY * act'(Z)   dX = dZ W^T   dW = X^T dZ
+ *                     db = column sums of dZ   (the residual's gradient is dY)
+ *   gated backward    dG = dH * U * act'(G)   dU = dH * act(G)
+ *                     dX = dG Wg^T + dU Wu^T   dWg = X^T dG   dWu = X^T dU
+ *                     dbg, dbu = column sums of dG, dU
+ *
+ * Weights W are K x N in either storage order (pgemm_order): PGEMM_KN is
+ * W[K][N] with ldw >= N, PGEMM_NK is W[N][K] with ldw >= K, the usual storage
+ * of an (out, in) parameter.  Leading dimensions are in elements; pointers
+ * and leading dimensions need only element alignment.  bias, R, Z, G and U
+ * may be null where noted; X, W, bias, Z, G, U and dY have the operand type,
+ * Y and R the output type: the operand type or PGEMM_F32.
+ *
+ * Activations: none, relu, silu z/(1 + exp(-z)), gelu z Phi(z), gelu_tanh
+ * (z/2)(1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))).  relu'(0) = 0; a NaN passes
+ * through every activation.
+ *
+ * In the backward passes dZ (dG, dU) is rounded to the operand type before it
+ * is multiplied (not where act is none: dZ is dY); the bias gradients sum
+ * the unrounded values in fp32.  Nothing depends on the order in which
+ * workgroups run: repeated calls give the same bits.
+ *
+ * Each call takes a workspace: device memory, 16-byte aligned, of at least
+ * the bytes that its _workspace function returns for the same sizes (0: the
+ * pointer may be null).  It holds nothing between calls and needs no
+ * initialisation; two calls that may run at the same time need one each.
+ * Calls enqueue one or more kernels on `stream`, allocate nothing and can be
+ * captured in a graph.  Outputs may not overlap inputs, the workspace or each
+ * other.  Empty sizes are served: M or N zero computes nothing forward, and
+ * gradients over no rows or columns are zeros.
+ *
+ * Errors: UNSUPPORTED_DTYPE; INVALID_ARG (a negative size, a leading dimension
+ * too small, a missing or misaligned pointer, an unknown order, activation or
+ * output type, a workspace too small); TOO_LARGE (a size above 2^31 - 256 or a
+ * leading dimension of 2^21 or more); HIP for a rejected launch. */
+enum pgemm_act {
+    PGEMM_ACT_NONE = 0,
+    PGEMM_ACT_RELU = 1,
+    PGEMM_ACT_SILU = 2,
+    PGEMM_ACT_GELU = 3,
+    PGEMM_ACT_GELU_TANH = 4
+};
+enum pgemm_order { PGEMM_KN = 0, PGEMM_NK = 1 };
+
+/* Bytes of workspace, or a negative pgemm_status.  `act` as in the call:
+ * without an activation the backward pass keeps no dZ. */
+int64_t pgemm_linear_workspace(int64_t M, int64_t N, int64_t K, int dtype);
+int64_t pgemm_gated_workspace(int64_t M, int64_t N, int64_t K, int dtype);
+int64_t pgemm_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int act, int dtype);
+int64_t pgemm_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int dtype);
+
+/* Y[M][N] = act(X W + bias) + R.  bias[N], R[M][N] and Z[M][N] (receives the
+ * pre-activation, for the backward pass) may be null. */
+int pgemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                 int w_order, const void* bias, const void* R, int64_t ldr, int act, void* Z, int64_t ldz, void* Y,
+                 int64_t ldy, int out_dtype, int dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* H[M][N] = act(X Wg + bias_g) * (X Wu + bias_u).  Wg and Wu share ldw and
+ * order.  Biases, G and U (receive the two projections) may be null. */
+int pgemm_gated(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* Wg, const void* Wu,
+                int64_t ldw, int w_order, const void* bias_g, const void* bias_u, int act, void* G, int64_t ldg,
+                void* U, int64_t ldu, void* H, int64_t ldh, int out_dtype, int dtype, void* workspace,
+                int64_t workspace_bytes, void* stream);
+
+/* Gradients of linear.  dX[M][K] (operand type), dW (order dw_order) and
+ * dbias[N] (both of grad_dtype: the operand type or PGEMM_F32) may be null:
+ * what is null is not computed.  Z may be null when act is none; X when dW is
+ * null, W when dX is null. */
+int pgemm_linear_backward(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                          const void* W, int64_t ldw, int w_order, const void* Z, int64_t ldz, int act, void* dX,
+                          int64_t lddx, void* dW, int64_t lddw, int dw_order, void* dbias, int grad_dtype, int dtype,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Gradients of gated.  dX, dWg and dWu (both or neither) and the bias
+ * gradients may be null. */
+int pgemm_gated_backward(int64_t M, int64_t N, int64_t K, const void* dH, int64_t lddh, const void* X, int64_t ldx,
+                         const void* Wg, const void* Wu, int64_t ldw, int w_order, const void* G, int64_t ldg,
+                         const void* U, int64_t ldu, int act, void* dX, int64_t lddx, void* dWg, void* dWu,
+                         int64_t lddw, int dw_order, void* dbias_g, void* dbias_u, int grad_dtype, int dtype,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
 /* ABI version: major*10000 + minor*100 + patch (a library convention, not
  * from the pages). */
 int pgemm_version(void);

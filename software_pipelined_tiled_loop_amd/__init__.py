@@ -13,14 +13,15 @@ from __future__ import annotations
 import importlib
 
 __all__ = ["binding", "inputs", "build", "pgemm_gemm", "pgemm_gemm_ex", "pgemm_plan",
-           "pgemm_strerror", "gemm"]
+           "pgemm_strerror", "gemm", "linear", "linear_backward", "gated", "gated_backward"]
 
 
 def __getattr__(name):
     if name in ("binding", "inputs", "build"):
         return importlib.import_module("." + name, __name__)
     if name in ("pgemm_gemm", "pgemm_gemm_ex", "pgemm_plan", "pgemm_strerror", "gemm",
-                "pgemm_num_variants", "pgemm_variant_info", "PgemmError"):
+                "pgemm_num_variants", "pgemm_variant_info", "PgemmError", "linear", "linear_backward", "gated",
+                "gated_backward"):
         mod = importlib.import_module(".binding", __name__)
         return getattr(mod, name)
     raise AttributeError(name)

@@ -12,6 +12,7 @@ library has not been built: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -101,6 +102,26 @@ _lib.pgemm_diag_wait_profile.restype = _int
 _lib.pgemm_diag_parts.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _int, _int, _int, _int,
                                   _int, _vp, _i64, _vp]
 _lib.pgemm_diag_parts.restype = _int
+for _f, _n in (("pgemm_linear_workspace", 3), ("pgemm_gated_workspace", 3), ("pgemm_linear_backward_workspace", 3),
+               ("pgemm_gated_backward_workspace", 3)):
+    getattr(_lib, _f).argtypes = [_i64] * _n + [_int] * (2 if _f == "pgemm_linear_backward_workspace" else 1)
+    getattr(_lib, _f).restype = _i64
+_lib.pgemm_linear.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _vp, _i64, _int, _vp, _i64, _vp, _i64,
+                              _int, _int, _vp, _i64, _vp]
+_lib.pgemm_linear.restype = _int
+_lib.pgemm_gated.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _int, _vp, _vp, _int, _vp, _i64, _vp, _i64,
+                             _vp, _i64, _int, _int, _vp, _i64, _vp]
+_lib.pgemm_gated.restype = _int
+_lib.pgemm_linear_backward.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _int, _vp,
+                                       _i64, _vp, _i64, _int, _vp, _int, _int, _vp, _i64, _vp]
+_lib.pgemm_linear_backward.restype = _int
+_lib.pgemm_gated_backward.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _int, _vp, _i64, _vp,
+                                      _i64, _int, _vp, _i64, _vp, _vp, _i64, _int, _vp, _vp, _int, _int, _vp, _i64,
+                                      _vp]
+_lib.pgemm_gated_backward.restype = _int
+
+ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+ORDER_KN, ORDER_NK = 0, 1
 
 # Steady-state parts of a parts-ladder build (enum pgemm_part).
 PART_DMA, PART_BARRIER, PART_AREADS, PART_BREADS, PART_ALL = 1, 2, 4, 8, 15
@@ -108,7 +129,9 @@ PART_DMA, PART_BARRIER, PART_AREADS, PART_BREADS, PART_ALL = 1, 2, 4, 8, 15
 EXPORTED = ("pgemm_gemm", "pgemm_gemm_ex", "pgemm_plan", "pgemm_strerror", "pgemm_num_variants",
             "pgemm_variant_info", "pgemm_version", "pgemm_model_uncovered_cycles", "pgemm_model_lds_bytes",
             "pgemm_model_global_loads_per_output", "pgemm_model_compute_load_ratio", "pgemm_hazard_copy_reduce",
-            "pgemm_diag_mfma_ceiling", "pgemm_diag_lds_stream", "pgemm_diag_wait_profile", "pgemm_diag_parts")
+            "pgemm_diag_mfma_ceiling", "pgemm_diag_lds_stream", "pgemm_diag_wait_profile", "pgemm_diag_parts",
+            "pgemm_linear", "pgemm_gated", "pgemm_linear_backward", "pgemm_gated_backward", "pgemm_linear_workspace",
+            "pgemm_gated_workspace", "pgemm_linear_backward_workspace", "pgemm_gated_backward_workspace")
 
 
 class PgemmError(RuntimeError):
@@ -281,6 +304,335 @@ def gemm(A, B, C, alpha=1.0, beta=0.0, stages=0, producer=None, tile=None, M=Non
     if r != 0:
         raise PgemmError(r)
     return C
+
+
+# ---- feed-forward operators ------------------------------------------------------------
+
+# The C entry points, with their names and argument order; every pointer is a
+# device address (or None) and the stream a hipStream_t.
+pgemm_linear = _lib.pgemm_linear
+pgemm_gated = _lib.pgemm_gated
+pgemm_linear_backward = _lib.pgemm_linear_backward
+pgemm_gated_backward = _lib.pgemm_gated_backward
+pgemm_linear_workspace = _lib.pgemm_linear_workspace
+pgemm_gated_workspace = _lib.pgemm_gated_workspace
+pgemm_linear_backward_workspace = _lib.pgemm_linear_backward_workspace
+pgemm_gated_backward_workspace = _lib.pgemm_gated_backward_workspace
+
+
+class _Call:
+    """The checks that the four operators share.  Collects the tensors of one
+    call; `go` launches it on their GPU once every check has passed."""
+
+    __slots__ = ("dtype", "device", "ins", "outs")
+
+    def __init__(self, X, name="X"):
+        code = _FLOAT_CODE.get(X.dtype)
+        if code is None:
+            raise ValueError("%s has unsupported dtype %s: float32, float16 or bfloat16 is needed" % (name, X.dtype))
+        self.dtype = code
+        self.device = X.device
+        self.ins, self.outs = [], []
+
+    def _place(self, name, t, dtypes, out):
+        if t.dtype not in dtypes:
+            raise ValueError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+        if t.device != self.device:
+            raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, self.device))
+        (self.outs if out else self.ins).append((name, t))
+
+    def rows(self, name, t, shape, dtypes, out=False):
+        """(address, leading dimension) of a row-major matrix with unit column stride."""
+        if t is None:
+            return None, 0
+        if t.dim() != 2 or tuple(t.shape) != shape:
+            raise ValueError("%s is %s, the call needs %s" % (name, tuple(t.shape), shape))
+        self._place(name, t, dtypes, out)
+        r, c = shape
+        s0, s1 = t.stride()
+        if (s1 != 1 and c > 1) or (s0 < c and r > 1):
+            raise ValueError("%s must be row-major with unit column stride, got strides %s" % (name, (s0, s1)))
+        return t.data_ptr(), (s0 if r > 1 else c) or 1
+
+    def weight(self, name, t, shape, dtypes, out=False):
+        """(address, leading dimension, order) of a K x N weight stored either way."""
+        if t is None:
+            return None, 0, ORDER_KN
+        if t.dim() != 2 or tuple(t.shape) != shape:
+            raise ValueError("%s is %s, the call needs %s" % (name, tuple(t.shape), shape))
+        self._place(name, t, dtypes, out)
+        k, n = shape
+        s0, s1 = t.stride()
+        if (s1 == 1 or n <= 1) and (s0 >= n or k <= 1):
+            return t.data_ptr(), (s0 if k > 1 else n) or 1, ORDER_KN
+        if (s0 == 1 or k <= 1) and (s1 >= k or n <= 1):
+            return t.data_ptr(), (s1 if n > 1 else k) or 1, ORDER_NK
+        raise ValueError("%s must have unit stride along one axis and whole rows along the other, got strides %s"
+                         % (name, (s0, s1)))
+
+    def vector(self, name, t, n, dtypes, out=False):
+        if t is None:
+            return None
+        if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+            raise ValueError("%s must be a contiguous vector of %d, got %s" % (name, n, tuple(t.shape)))
+        self._place(name, t, dtypes, out)
+        return t.data_ptr()
+
+    def check_overlap(self, same=None):
+        """No output may share memory with an input or another output; `same` is
+        an (input, output) pair that may be one and the same matrix."""
+        spans = []
+        for kind, group in ((0, self.ins), (1, self.outs)):
+            for name, t in group:
+                if t.numel():
+                    p = t.data_ptr()
+                    last = sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
+                    spans.append((p, p + (last + 1) * t.element_size(), kind, name, t))
+        spans.sort(key=_first)
+        top, i = 0, 0
+        for i, a in enumerate(spans):
+            if a[0] < top:
+                break
+            top = max(top, a[1])
+        else:
+            return
+        for i, a in enumerate(spans):
+            for b in spans[i + 1:]:
+                if b[0] >= a[1] or not (a[2] or b[2]):
+                    continue
+                x, y = a[4], b[4]
+                if same is not None and {id(x), id(y)} == {id(same[0]), id(same[1])}:
+                    if x.data_ptr() == y.data_ptr() and x.stride() == y.stride() and x.dtype == y.dtype:
+                        continue
+                if x.dim() == 2 and y.dim() == 2:  # stored rows: the axis of larger stride
+                    x, y = _stored_rows(x), _stored_rows(y)
+                    if not _regions_overlap(x, x.shape[0], x.shape[1], y, y.shape[0], y.shape[1]):
+                        continue
+                raise ValueError("%s and %s overlap: outputs must not share memory with inputs or each other"
+                                 % (a[3], b[3]))
+
+    def go(self, need, workspace, stream, call):
+        """Runs call(workspace address, bytes, stream) on the tensors' GPU."""
+        import torch
+        if self.device.type != "cuda":
+            raise ValueError("the tensors must be on a GPU, got %s" % self.device)
+        index = self.device.index
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return self.go(need, workspace, stream, call)
+        if need < 0:
+            raise PgemmError(need)
+        if workspace is not None:
+            if workspace.device != self.device or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on %s" % self.device)
+            p = workspace.data_ptr()
+            n = workspace.numel() * workspace.element_size()
+            if n < need or p % 16:
+                raise ValueError("workspace must be 16-byte aligned and hold %d bytes, got %d" % (need, n))
+            if n:
+                for name, t in self.ins + self.outs:
+                    if t.numel():
+                        q = t.data_ptr()
+                        last = sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
+                        if q < p + n and p < q + (last + 1) * t.element_size():
+                            raise ValueError("workspace overlaps %s" % name)
+        elif need == 0:
+            p, n = None, 0
+        elif stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            p, n = workspace.data_ptr(), need
+        else:
+            # from the pool of the stream that the kernels run on: freed with
+            # this call, it can only be handed out again behind them
+            with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
+                                   torch.cuda.ExternalStream(stream, device=self.device)):
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            p, n = workspace.data_ptr(), need
+        r = call(p, n, torch.cuda.current_stream(index).cuda_stream if stream is None else _stream(stream))
+        if r != 0:
+            raise PgemmError(r)
+
+
+def _first(span):
+    return span[0]
+
+
+def _stored_rows(t):
+    return t if t.stride(0) >= t.stride(1) else t.t()
+
+
+try:
+    _FLOAT_CODE = {torch.float32: PGEMM_F32, torch.float16: PGEMM_F16, torch.bfloat16: PGEMM_BF16}
+    _BY_CODE = {c: t for t, c in _FLOAT_CODE.items()}
+    _OUT_TYPES = {c: (t,) if c == PGEMM_F32 else (t, torch.float32) for c, t in _BY_CODE.items()}
+    _OWN_TYPE = {c: (t,) for c, t in _BY_CODE.items()}
+except NameError:  # without torch only the C entry points above are used
+    pass
+
+
+def _act_code(act):
+    try:
+        return ACT[act]
+    except (KeyError, TypeError):
+        raise ValueError("unknown activation %r: one of %s" % (act, ", ".join(ACT))) from None
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(function, *args):
+    return getattr(_lib, function)(*args)
+
+
+def _sizes(X, W, name="W"):
+    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[0]:
+        raise ValueError("X is %s and %s is %s: M x K and K x N are needed" % (tuple(X.shape), name, tuple(W.shape)))
+    return X.shape[0], W.shape[1], X.shape[1]
+
+
+def linear(X, W, Y, bias=None, residual=None, act="none", Z=None, workspace=None, stream=None):
+    """Y = act(X @ W + bias) + residual on torch tensors.
+
+    X is M x K, row-major with unit column stride; W is K x N in either storage
+    order (a contiguous K x N tensor, or the transposed view of an N x K
+    parameter), bias N.  float32, float16 or bfloat16, all of one type; Y (and
+    residual) may be float32 instead.  Y and residual are M x N; residual may
+    be Y itself.  Z, when given, receives the pre-activation X @ W + bias in
+    X's type, which linear_backward reads.  act: "none", "relu", "silu",
+    "gelu", "gelu_tanh".  Accumulation, bias, activation and residual are in
+    fp32; Y and Z are each rounded once.
+
+    The call runs on the tensors' GPU, on torch's current stream there unless
+    `stream` is given, and does not synchronise.  A workspace of
+    pgemm_linear_workspace bytes is taken from torch's allocator for the call
+    unless one is passed.  Bad arguments raise ValueError before anything is
+    launched; a status the library returns raises PgemmError.  Returns Y.
+    """
+    M, N, K = _sizes(X, W)
+    c = _Call(X)
+    own, out = _OWN_TYPE[c.dtype], _OUT_TYPES[c.dtype]
+    a = _act_code(act)
+    px, ldx = c.rows("X", X, (M, K), own)
+    pw, ldw, order = c.weight("W", W, (K, N), own)
+    pb = c.vector("bias", bias, N, own)
+    py, ldy = c.rows("Y", Y, (M, N), out, True)
+    pr, ldr = c.rows("residual", residual, (M, N), (Y.dtype,))
+    pz, ldz = c.rows("Z", Z, (M, N), own, True)
+    c.check_overlap((residual, Y))
+    c.go(_workspace_bytes("pgemm_linear_workspace", M, N, K, c.dtype), workspace, stream,
+         lambda p, n, s: pgemm_linear(M, N, K, px, ldx, pw, ldw, order, pb, pr, ldr, a, pz, ldz, py, ldy,
+                                      _FLOAT_CODE[Y.dtype], c.dtype, p, n, s))
+    return Y
+
+
+def gated(X, Wg, Wu, H, bias_g=None, bias_u=None, act="silu", G=None, U=None, workspace=None, stream=None):
+    """H = act(X @ Wg + bias_g) * (X @ Wu + bias_u) on torch tensors, in one product kernel.
+
+    As linear, with two weights of the same strides.  G and U, when given,
+    receive the two projections (with bias, before the activation) in X's type,
+    which gated_backward reads.  Returns H.
+    """
+    M, N, K = _sizes(X, Wg, "Wg")
+    c = _Call(X)
+    own, out = _OWN_TYPE[c.dtype], _OUT_TYPES[c.dtype]
+    a = _act_code(act)
+    px, ldx = c.rows("X", X, (M, K), own)
+    pg, pu, ldw, order = _two_weights(c, "Wg", Wg, "Wu", Wu, (K, N), own, False)
+    pbg, pbu = c.vector("bias_g", bias_g, N, own), c.vector("bias_u", bias_u, N, own)
+    ph, ldh = c.rows("H", H, (M, N), out, True)
+    pG, ldg = c.rows("G", G, (M, N), own, True)
+    pU, ldu = c.rows("U", U, (M, N), own, True)
+    c.check_overlap()
+    c.go(_workspace_bytes("pgemm_gated_workspace", M, N, K, c.dtype), workspace, stream,
+         lambda p, n, s: pgemm_gated(M, N, K, px, ldx, pg, pu, ldw, order, pbg, pbu, a, pG, ldg, pU, ldu, ph, ldh,
+                                     _FLOAT_CODE[H.dtype], c.dtype, p, n, s))
+    return H
+
+
+def _two_weights(c, name0, w0, name1, w1, shape, dtypes, out):
+    p0, ld0, order0 = c.weight(name0, w0, shape, dtypes, out)
+    p1, ld1, order1 = c.weight(name1, w1, shape, dtypes, out)
+    if (w0 is None) != (w1 is None):
+        raise ValueError("%s and %s must be given together" % (name0, name1))
+    if w0 is not None and (ld0 != ld1 or order0 != order1):
+        raise ValueError("%s and %s must have the same strides, got %s and %s"
+                         % (name0, name1, tuple(w0.stride()), tuple(w1.stride())))
+    return p0, p1, ld0, order0
+
+
+def _grad_type(c, outs):
+    """The one type of the weight and bias gradients: X's, or float32."""
+    types = {t.dtype for t in outs if t is not None}
+    if len(types) > 1:
+        raise ValueError("weight and bias gradients must share one type, got %s" % sorted(str(t) for t in types))
+    t = types.pop() if types else _BY_CODE[c.dtype]
+    if t not in _OUT_TYPES[c.dtype]:
+        raise ValueError("weight and bias gradients must be %s, got %s"
+                         % (" or ".join(str(d) for d in _OUT_TYPES[c.dtype]), t))
+    return t
+
+
+def linear_backward(dY, X, W, Z=None, act="none", dX=None, dW=None, dbias=None, workspace=None, stream=None):
+    """Gradients of linear for dY, the gradient at Y, into the tensors given.
+
+    With dZ = dY * act'(Z): dX = dZ @ W.T (M x K, X's type), dW = X.T @ dZ
+    (K x N in either storage order) and dbias = dZ summed over rows; dW and
+    dbias have X's type or float32.  What is None is not computed.  Z is the
+    pre-activation that linear wrote (not needed for act "none"); the
+    residual's gradient is dY itself.  dZ is rounded to X's type before the two
+    products; dbias sums it unrounded.  Streams, workspace
+    (pgemm_linear_backward_workspace) and errors as for linear.
+    Returns (dX, dW, dbias).
+    """
+    M, N, K = _sizes(X, W)
+    c = _Call(X)
+    own = _OWN_TYPE[c.dtype]
+    a = _act_code(act)
+    if a != 0 and Z is None:
+        raise ValueError("Z, the pre-activation, is needed for act %r" % act)
+    gt = _grad_type(c, (dW, dbias))
+    pdy, lddy = c.rows("dY", dY, (M, N), own)
+    px, ldx = c.rows("X", X, (M, K), own)
+    pw, ldw, order = c.weight("W", W, (K, N), own)
+    pz, ldz = c.rows("Z", Z, (M, N), own)
+    pdx, lddx = c.rows("dX", dX, (M, K), own, True)
+    pdw, lddw, dorder = c.weight("dW", dW, (K, N), (gt,), True)
+    pdb = c.vector("dbias", dbias, N, (gt,), True)
+    c.check_overlap()
+    c.go(_workspace_bytes("pgemm_linear_backward_workspace", M, N, K, a, c.dtype), workspace, stream,
+         lambda p, n, s: pgemm_linear_backward(M, N, K, pdy, lddy, px, ldx, pw, ldw, order, pz, ldz, a, pdx, lddx,
+                                               pdw, lddw, dorder, pdb, _FLOAT_CODE[gt], c.dtype, p, n, s))
+    return dX, dW, dbias
+
+
+def gated_backward(dH, X, Wg, Wu, G, U, act="silu", dX=None, dWg=None, dWu=None, dbias_g=None, dbias_u=None,
+                   workspace=None, stream=None):
+    """Gradients of gated for dH, the gradient at H, into the tensors given.
+
+    G and U are the projections that gated wrote.  With dG = dH * U * act'(G)
+    and dU = dH * act(G): dX = dG @ Wg.T + dU @ Wu.T, dWg = X.T @ dG,
+    dWu = X.T @ dU (both or neither, of the same strides), dbias_g and dbias_u
+    the sums of dG and dU over rows.  Types, streams, workspace
+    (pgemm_gated_backward_workspace) and errors as for linear_backward.
+    Returns (dX, dWg, dWu, dbias_g, dbias_u).
+    """
+    M, N, K = _sizes(X, Wg, "Wg")
+    c = _Call(X)
+    own = _OWN_TYPE[c.dtype]
+    a = _act_code(act)
+    gt = _grad_type(c, (dWg, dWu, dbias_g, dbias_u))
+    pdh, lddh = c.rows("dH", dH, (M, N), own)
+    px, ldx = c.rows("X", X, (M, K), own)
+    pg, pu, ldw, order = _two_weights(c, "Wg", Wg, "Wu", Wu, (K, N), own, False)
+    pG, ldg = c.rows("G", G, (M, N), own)
+    pU, ldu = c.rows("U", U, (M, N), own)
+    pdx, lddx = c.rows("dX", dX, (M, K), own, True)
+    pdg, pdu, lddw, dorder = _two_weights(c, "dWg", dWg, "dWu", dWu, (K, N), (gt,), True)
+    pbg, pbu = c.vector("dbias_g", dbias_g, N, (gt,), True), c.vector("dbias_u", dbias_u, N, (gt,), True)
+    c.check_overlap()
+    c.go(_workspace_bytes("pgemm_gated_backward_workspace", M, N, K, c.dtype), workspace, stream,
+         lambda p, n, s: pgemm_gated_backward(M, N, K, pdh, lddh, px, ldx, pg, pu, ldw, order, pG, ldg, pU, ldu, a,
+                                              pdx, lddx, pdg, pdu, lddw, dorder, pbg, pbu, _FLOAT_CODE[gt], c.dtype,
+                                              p, n, s))
+    return dX, dWg, dWu, dbias_g, dbias_u
 
 
 def pgemm_hazard_copy_reduce(X, rows, cols, ldx, row_sums, reuse_wait, delay_wave=-1, delay_cycles=0, trace=None,

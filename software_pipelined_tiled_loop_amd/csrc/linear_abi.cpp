@@ -1,0 +1,472 @@
+// linear_abi.cpp -- the feed-forward operators' C entry points: argument
+// checks, the choice of tile and splits, workspaces and launches.
+//
+// Every operator is a few products of one of three operand layouts
+// (linear_variants.hpp); the backward passes begin with one elementwise kernel
+// that forms the gradients at the pre-activations and their column sums.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+
+#include "linear_variants.hpp"
+#include "pgemm.h"
+
+using namespace pgemm;
+
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffff00;
+constexpr int64_t kMaxLd = (int64_t)1 << 21;  // 256 rows of 4-byte elements stay below 2^31 bytes
+constexpr int kNumCU = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+int64_t elem_size(int dtype) { return dtype == PGEMM_F32 ? 4 : 2; }
+bool float_type(int dtype) { return dtype == PGEMM_F32 || dtype == PGEMM_F16 || dtype == PGEMM_BF16; }
+
+LinKernels kernels_for(int dtype) {
+    return dtype == PGEMM_F32 ? linear_kernels_f32() : dtype == PGEMM_F16 ? linear_kernels_f16()
+                                                                        : linear_kernels_bf16();
+}
+
+ActArgs act_args(int act) {
+    // -log2(e) * P(t); see ActArgs
+    constexpr double kLog2e = 1.4426950408889634;
+    static const double gelu[7] = {1.5957684317138,     0.07266856844868,    -6.6261136489796e-05, -1.1047993311290e-04,
+                                   7.9381600098274e-06, -2.6688873955814e-07, 3.6111307428585e-09};
+    ActArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.kind = act;
+    if (act == PGEMM_ACT_SILU) {
+        a.c[0] = (float)-kLog2e;
+    } else if (act == PGEMM_ACT_GELU) {
+        for (int d = 0; d < 7; ++d) a.c[d] = (float)(-kLog2e * gelu[d]);
+    } else if (act == PGEMM_ACT_GELU_TANH) {
+        const double c = 1.5957691216057308;  // sqrt(8 / pi)
+        a.c[0] = (float)(-kLog2e * c);
+        a.c[1] = (float)(-kLog2e * c * 0.044715);
+    }
+    return a;
+}
+
+// A rows x cols product over K (per contraction half), with `outs` outputs
+// side by side.
+struct Shape {
+    int64_t rows, cols, K;
+    int lay, gated, halves, outs;
+};
+
+struct Plan {
+    const LinVariant* v;
+    int64_t tiles_m, tiles_n, splits, part_bytes;
+    int np4;
+};
+
+// The tile and the splits of a product, from its sizes and type alone (so the
+// workspace functions and the calls agree).
+Plan plan_product(const Shape& p, int dtype) {
+    const LinKernels k = kernels_for(dtype);
+    Plan best{};
+    for (int i = 0; i < k.n; ++i) {
+        const LinVariant& v = k.v[i];
+        if (v.lay != p.lay || v.gated != p.gated) continue;
+        best.v = &v;
+        break;
+    }
+    const LinVariant& v = *best.v;
+    best.tiles_m = ceil_div(p.rows, v.bm);
+    best.tiles_n = ceil_div(p.cols, v.bn);
+    const int64_t tiles = best.tiles_m * best.tiles_n * p.outs;
+    const int64_t kt = ceil_div(p.K, v.bk) * p.halves;
+    int64_t s = 1;
+    if (tiles > 0 && tiles < kNumCU) {
+        s = kNumCU / tiles;
+        if (s > kt / 4) s = kt / 4;
+        if (s > 32) s = 32;
+        if (s < 1) s = 1;
+    }
+    best.splits = s;
+    best.np4 = (int)round_up(p.cols, 4);
+    best.part_bytes = s > 1 ? s * (p.gated ? 2 : p.outs) * p.rows * best.np4 * 4 : 0;
+    return best;
+}
+
+int64_t part_bytes(const Shape& p, int dtype) {
+    if (p.rows == 0 || p.cols == 0) return 0;
+    return round_up(plan_product(p, dtype).part_bytes, 256);
+}
+
+int hip_failed(const char* what, hipError_t e) {
+    std::fprintf(stderr, "pgemm: launch of %s failed: %s (%d)\n", what, hipGetErrorString(e), (int)e);
+    return PGEMM_ERR_HIP;
+}
+
+// Runs a product whose operands, outputs and epilogue `a` already holds.
+int run_product(const Shape& p, LinArgs& a, int dtype, void* part, hipStream_t stream) {
+    if (p.rows == 0 || p.cols == 0) return PGEMM_OK;
+    const LinKernels k = kernels_for(dtype);
+    const Plan pl = plan_product(p, dtype);
+    const LinVariant& v = *pl.v;
+    a.K = (int)p.K;
+    a.halves = p.halves;
+    a.outs = p.outs;
+    a.tiles_m = (int)pl.tiles_m;
+    a.tiles_n = (int)pl.tiles_n;
+    a.group_m = 4;
+    a.splits = (int)pl.splits;
+    a.part = pl.splits > 1 ? (float*)part : nullptr;
+    a.np4 = pl.np4;
+    a.e.M = (int)p.rows;
+    a.e.N = (int)p.cols;
+    a.nfull = v.ring_tiles(p.K, p.rows, a.lda, p.cols, a.ldb);
+    const int64_t grid = round_up(pl.tiles_m * pl.tiles_n * p.outs * pl.splits, 8);
+    hipError_t e = v.launch(a, (int)grid, stream);
+    if (e != hipSuccess) return hip_failed("linear_kernel", e);
+    if (pl.splits > 1) {
+        const int64_t g2 = ceil_div(pl.np4, 1024) * p.rows * p.outs;
+        e = (p.gated ? k.join_gated : k.join)(a, (int)g2, stream);
+        if (e != hipSuccess) return hip_failed("linear_join", e);
+    }
+    return PGEMM_OK;
+}
+
+bool in_range(int64_t M, int64_t N, int64_t K) { return M <= kMaxDim && N <= kMaxDim && K <= kMaxDim; }
+// Work items of the largest grids (tiles, rows x strips) fit an int.
+bool grids_fit(int64_t a, int64_t b) { return ceil_div(a, 64) * ceil_div(b, 64) < 0x3fffff00 && a * ceil_div(b, 1024) < 0x3fffff00; }
+
+int check_sizes(int64_t M, int64_t N, int64_t K, int dtype) {
+    if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
+    if (M < 0 || N < 0 || K < 0) return PGEMM_ERR_INVALID_ARG;
+    if (!in_range(M, N, K) || !grids_fit(M, N) || !grids_fit(M, K) || !grids_fit(K, N) || !grids_fit(N, K))
+        return PGEMM_ERR_TOO_LARGE;
+    return PGEMM_OK;
+}
+
+// A matrix of `rows` rows of `cols` elements: 0, or the error.
+int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t es, bool needed) {
+    if (!p) return needed && rows > 0 && cols > 0 ? PGEMM_ERR_INVALID_ARG : PGEMM_OK;
+    if (ld < (cols > 1 ? cols : 1) || (uintptr_t)p % es) return PGEMM_ERR_INVALID_ARG;
+    return ld >= kMaxLd ? PGEMM_ERR_TOO_LARGE : PGEMM_OK;
+}
+int check_vector(const void* p, int64_t es) { return (uintptr_t)p % es ? PGEMM_ERR_INVALID_ARG : PGEMM_OK; }
+int check_workspace(const void* p, int64_t bytes, int64_t need) {
+    return need > 0 && (!p || (uintptr_t)p % 16 || bytes < need) ? PGEMM_ERR_INVALID_ARG : PGEMM_OK;
+}
+bool known(int order, int act, int out, int dtype) {
+    return (order == PGEMM_KN || order == PGEMM_NK) && act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_GELU_TANH &&
+           (out == dtype || out == PGEMM_F32);
+}
+#define PGEMM_TRY(x)                     \
+    do {                                 \
+        const int r_ = (x);              \
+        if (r_ != PGEMM_OK) return r_;   \
+    } while (0)
+
+Shape forward_shape(int64_t M, int64_t N, int64_t K, int order, int gated) {
+    return Shape{M, N, K, order == PGEMM_KN ? LIN_KX : LIN_KK, gated, 1, 1};
+}
+// dX: the contraction runs over N, along W[K][N]'s rows or W[N][K]'s columns.
+Shape dx_shape(int64_t M, int64_t N, int64_t K, int order, int halves) {
+    return Shape{M, K, N, order == PGEMM_KN ? LIN_KK : LIN_KX, 0, halves, 1};
+}
+// dW in its own storage order: K x N, or N x K.
+Shape dw_shape(int64_t M, int64_t N, int64_t K, int order, int outs) {
+    return order == PGEMM_KN ? Shape{K, N, M, LIN_XX, 0, 1, outs} : Shape{N, K, M, LIN_XX, 0, 1, outs};
+}
+int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
+
+// Workspace of a backward pass: gradients at the pre-activations, the row
+// blocks' column sums, the splits' sums (of dX, then of dW).
+struct Backward {
+    int64_t ldd, np4, blocks, dz_bytes, sum_bytes, split_bytes;
+    int64_t total(int planes, bool keeps) const { return (keeps ? planes * dz_bytes : 0) + sum_bytes + split_bytes; }
+};
+Backward backward_layout(int64_t M, int64_t N, int64_t K, int dtype, int planes) {
+    Backward b;
+    b.ldd = round_up(N, 64);
+    b.np4 = round_up(N, 4);
+    b.blocks = ceil_div(M, kSlopeRows);
+    b.dz_bytes = M * b.ldd * elem_size(dtype);  // a multiple of 128
+    b.sum_bytes = round_up(b.blocks * planes * b.np4 * 4, 256);
+    b.split_bytes = 0;
+    for (int order = 0; order < 2; ++order) {
+        b.split_bytes = larger(b.split_bytes, part_bytes(dx_shape(M, N, K, order, planes), dtype));
+        b.split_bytes = larger(b.split_bytes, part_bytes(dw_shape(M, N, K, order, planes), dtype));
+    }
+    return b;
+}
+
+struct Grad {
+    const void *dY, *X, *W[2], *Z, *U;
+    int64_t lddy, ldx, ldw, ldz, ldu;
+    void *dX, *dW[2], *db[2];
+    int64_t lddx, lddw;
+};
+
+// The backward pass of both operators (planes: 1, or 2 for gated).
+int run_backward(int64_t M, int64_t N, int64_t K, const Grad& q, int w_order, int dw_order, int act, int grad_dtype,
+                 int dtype, int planes, void* workspace, hipStream_t stream) {
+    const LinKernels k = kernels_for(dtype);
+    const Backward b = backward_layout(M, N, K, dtype, planes);
+    const bool gated = planes == 2, keeps = gated || act != PGEMM_ACT_NONE;
+    char* ws = (char*)workspace;
+    void* dz[2] = {ws, ws ? ws + b.dz_bytes : nullptr};
+    char* rest = ws ? ws + (keeps ? planes * b.dz_bytes : 0) : nullptr;
+    float* sums = (float*)rest;
+    void* part = rest ? rest + b.sum_bytes : nullptr;
+    const bool products = q.dX || q.dW[0], bias = q.db[0] || q.db[1];
+    if (N == 0) {
+        // no column: dX is all zeros (a product over nothing), the rest is empty
+    } else if (M > 0 && ((keeps && products) || bias)) {
+        SlopeArgs s;
+        std::memset(&s, 0, sizeof(s));
+        s.dY = q.dY;
+        s.ldy = q.lddy;
+        s.Z = q.Z;
+        s.ldz = q.ldz;
+        s.U = q.U;
+        s.ldu = q.ldu;
+        s.dZ = keeps && products ? dz[0] : nullptr;
+        s.dU = gated && products ? dz[1] : nullptr;
+        s.ldd = b.ldd;
+        s.sums = bias ? sums : nullptr;
+        s.np4 = (int)b.np4;
+        s.M = (int)M;
+        s.N = (int)N;
+        s.act = act_args(act);
+        const hipError_t e = k.slope(s, gated, (int)(ceil_div(N, kSlopeCols) * b.blocks), stream);
+        if (e != hipSuccess) return hip_failed("linear_slope", e);
+    }
+    if (bias && N > 0) {
+        SumArgs s;
+        std::memset(&s, 0, sizeof(s));
+        s.sums = sums;
+        s.out[0] = q.db[0];
+        s.out[1] = q.db[1];
+        s.blocks = (int)b.blocks;
+        s.planes = planes;
+        s.np4 = (int)b.np4;
+        s.N = (int)N;
+        s.out_f32 = grad_dtype == PGEMM_F32;
+        const hipError_t e = k.colsum(s, (int)ceil_div(N, 64), stream);
+        if (e != hipSuccess) return hip_failed("linear_colsum", e);
+    }
+    const void* d[2] = {keeps ? dz[0] : q.dY, gated ? dz[1] : keeps ? dz[0] : q.dY};
+    const int64_t ldd = keeps ? b.ldd : q.lddy;
+    if (q.dX) {
+        LinArgs a;
+        std::memset(&a, 0, sizeof(a));
+        for (int h = 0; h < 2; ++h) {
+            a.A[h] = d[h];
+            a.B[h] = q.W[h];
+        }
+        a.lda = ldd;
+        a.ldb = q.ldw;
+        a.e.Y[0] = a.e.Y[1] = q.dX;
+        a.e.ldy = q.lddx;
+        a.e.out_f32 = dtype == PGEMM_F32;
+        PGEMM_TRY(run_product(dx_shape(M, N, K, w_order, planes), a, dtype, part, stream));
+    }
+    if (q.dW[0]) {
+        LinArgs a;
+        std::memset(&a, 0, sizeof(a));
+        for (int h = 0; h < 2; ++h) {
+            a.A[h] = dw_order == PGEMM_KN ? q.X : d[h];
+            a.B[h] = dw_order == PGEMM_KN ? d[h] : q.X;
+            a.e.Y[h] = q.dW[h];
+        }
+        a.lda = dw_order == PGEMM_KN ? q.ldx : ldd;
+        a.ldb = dw_order == PGEMM_KN ? ldd : q.ldx;
+        a.e.ldy = q.lddw;
+        a.e.out_f32 = grad_dtype == PGEMM_F32;
+        PGEMM_TRY(run_product(dw_shape(M, N, K, dw_order, planes), a, dtype, part, stream));
+    }
+    return PGEMM_OK;
+}
+
+int check_weight(const void* W, int64_t N, int64_t K, int64_t ldw, int order, int64_t es, bool needed) {
+    return order == PGEMM_KN ? check_matrix(W, K, N, ldw, es, needed) : check_matrix(W, N, K, ldw, es, needed);
+}
+
+int64_t forward_workspace(int64_t M, int64_t N, int64_t K, int dtype, int gated) {
+    PGEMM_TRY(check_sizes(M, N, K, dtype));
+    return larger(part_bytes(forward_shape(M, N, K, PGEMM_KN, gated), dtype),
+                  part_bytes(forward_shape(M, N, K, PGEMM_NK, gated), dtype));
+}
+
+int64_t backward_workspace(int64_t M, int64_t N, int64_t K, int act, int dtype, int planes) {
+    PGEMM_TRY(check_sizes(M, N, K, dtype));
+    if (act < PGEMM_ACT_NONE || act > PGEMM_ACT_GELU_TANH) return PGEMM_ERR_INVALID_ARG;
+    return backward_layout(M, N, K, dtype, planes).total(planes, planes == 2 || act != PGEMM_ACT_NONE);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t pgemm_linear_workspace(int64_t M, int64_t N, int64_t K, int dtype) {
+    return forward_workspace(M, N, K, dtype, 0);
+}
+int64_t pgemm_gated_workspace(int64_t M, int64_t N, int64_t K, int dtype) {
+    return forward_workspace(M, N, K, dtype, 1);
+}
+int64_t pgemm_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int act, int dtype) {
+    return backward_workspace(M, N, K, act, dtype, 1);
+}
+int64_t pgemm_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int dtype) {
+    return backward_workspace(M, N, K, PGEMM_ACT_SILU, dtype, 2);
+}
+
+int pgemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                 int w_order, const void* bias, const void* R, int64_t ldr, int act, void* Z, int64_t ldz, void* Y,
+                 int64_t ldy, int out_dtype, int dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+    PGEMM_TRY(check_sizes(M, N, K, dtype));
+    if (!known(w_order, act, out_dtype, dtype)) return PGEMM_ERR_INVALID_ARG;
+    const int64_t es = elem_size(dtype), os = elem_size(out_dtype);
+    PGEMM_TRY(check_matrix(X, M, K, ldx, es, N > 0));
+    PGEMM_TRY(check_weight(W, N, K, ldw, w_order, es, M > 0));
+    PGEMM_TRY(check_vector(bias, es));
+    PGEMM_TRY(check_matrix(R, M, N, ldr, os, false));
+    PGEMM_TRY(check_matrix(Z, M, N, ldz, es, false));
+    PGEMM_TRY(check_matrix(Y, M, N, ldy, os, true));
+    if (M == 0 || N == 0) return PGEMM_OK;
+    const Shape p = forward_shape(M, N, K, w_order, 0);
+    PGEMM_TRY(check_workspace(workspace, workspace_bytes, forward_workspace(M, N, K, dtype, 0)));
+    LinArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.A[0] = a.A[1] = X;
+    a.B[0] = a.B[1] = W;
+    a.lda = ldx;
+    a.ldb = ldw;
+    a.e.Y[0] = a.e.Y[1] = Y;
+    a.e.ldy = ldy;
+    a.e.R = R;
+    a.e.ldr = ldr;
+    a.e.Z = Z;
+    a.e.ldz = ldz;
+    a.e.bias[0] = bias;
+    a.e.act = act_args(act);
+    a.e.out_f32 = out_dtype == PGEMM_F32;
+    return run_product(p, a, dtype, workspace, (hipStream_t)stream);
+}
+
+int pgemm_gated(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* Wg, const void* Wu,
+                int64_t ldw, int w_order, const void* bias_g, const void* bias_u, int act, void* G, int64_t ldg,
+                void* U, int64_t ldu, void* H, int64_t ldh, int out_dtype, int dtype, void* workspace,
+                int64_t workspace_bytes, void* stream) {
+    PGEMM_TRY(check_sizes(M, N, K, dtype));
+    if (!known(w_order, act, out_dtype, dtype)) return PGEMM_ERR_INVALID_ARG;
+    const int64_t es = elem_size(dtype), os = elem_size(out_dtype);
+    PGEMM_TRY(check_matrix(X, M, K, ldx, es, N > 0));
+    PGEMM_TRY(check_weight(Wg, N, K, ldw, w_order, es, M > 0));
+    PGEMM_TRY(check_weight(Wu, N, K, ldw, w_order, es, M > 0));
+    PGEMM_TRY(check_vector(bias_g, es));
+    PGEMM_TRY(check_vector(bias_u, es));
+    PGEMM_TRY(check_matrix(G, M, N, ldg, es, false));
+    PGEMM_TRY(check_matrix(U, M, N, ldu, es, false));
+    PGEMM_TRY(check_matrix(H, M, N, ldh, os, true));
+    if (M == 0 || N == 0) return PGEMM_OK;
+    const Shape p = forward_shape(M, N, K, w_order, 1);
+    PGEMM_TRY(check_workspace(workspace, workspace_bytes, forward_workspace(M, N, K, dtype, 1)));
+    LinArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.A[0] = a.A[1] = X;
+    a.B[0] = Wg;
+    a.B[1] = Wu;
+    a.lda = ldx;
+    a.ldb = ldw;
+    a.e.Y[0] = a.e.Y[1] = H;
+    a.e.ldy = ldh;
+    a.e.Z = G;
+    a.e.ldz = ldg;
+    a.e.U = U;
+    a.e.ldu = ldu;
+    a.e.bias[0] = bias_g;
+    a.e.bias[1] = bias_u;
+    a.e.act = act_args(act);
+    a.e.out_f32 = out_dtype == PGEMM_F32;
+    return run_product(p, a, dtype, workspace, (hipStream_t)stream);
+}
+
+int pgemm_linear_backward(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                          const void* W, int64_t ldw, int w_order, const void* Z, int64_t ldz, int act, void* dX,
+                          int64_t lddx, void* dW, int64_t lddw, int dw_order, void* dbias, int grad_dtype, int dtype,
+                          void* workspace, int64_t workspace_bytes, void* stream) {
+    PGEMM_TRY(check_sizes(M, N, K, dtype));
+    if (!known(w_order, act, grad_dtype, dtype) || !known(dw_order, act, grad_dtype, dtype))
+        return PGEMM_ERR_INVALID_ARG;
+    const int64_t es = elem_size(dtype), gs = elem_size(grad_dtype);
+    PGEMM_TRY(check_matrix(dY, M, N, lddy, es, dX || dW || dbias));
+    PGEMM_TRY(check_matrix(X, M, K, ldx, es, dW && N > 0));
+    PGEMM_TRY(check_weight(W, N, K, ldw, w_order, es, dX && M > 0));
+    PGEMM_TRY(check_matrix(Z, M, N, ldz, es, act != PGEMM_ACT_NONE));
+    PGEMM_TRY(check_matrix(dX, M, K, lddx, es, false));
+    PGEMM_TRY(check_weight(dW, N, K, lddw, dw_order, gs, false));
+    PGEMM_TRY(check_vector(dbias, gs));
+    PGEMM_TRY(check_workspace(workspace, workspace_bytes, backward_workspace(M, N, K, act, dtype, 1)));
+    Grad q;
+    std::memset(&q, 0, sizeof(q));
+    q.dY = dY;
+    q.lddy = lddy;
+    q.X = X;
+    q.ldx = ldx;
+    q.W[0] = q.W[1] = W;
+    q.ldw = ldw;
+    q.Z = Z;
+    q.ldz = ldz;
+    q.dX = dX;
+    q.lddx = lddx;
+    q.dW[0] = q.dW[1] = dW;
+    q.lddw = lddw;
+    q.db[0] = dbias;
+    return run_backward(M, N, K, q, w_order, dw_order, act, grad_dtype, dtype, 1, workspace, (hipStream_t)stream);
+}
+
+int pgemm_gated_backward(int64_t M, int64_t N, int64_t K, const void* dH, int64_t lddh, const void* X, int64_t ldx,
+                         const void* Wg, const void* Wu, int64_t ldw, int w_order, const void* G, int64_t ldg,
+                         const void* U, int64_t ldu, int act, void* dX, int64_t lddx, void* dWg, void* dWu,
+                         int64_t lddw, int dw_order, void* dbias_g, void* dbias_u, int grad_dtype, int dtype,
+                         void* workspace, int64_t workspace_bytes, void* stream) {
+    PGEMM_TRY(check_sizes(M, N, K, dtype));
+    if (!known(w_order, act, grad_dtype, dtype) || !known(dw_order, act, grad_dtype, dtype) || !dWg != !dWu)
+        return PGEMM_ERR_INVALID_ARG;
+    const int64_t es = elem_size(dtype), gs = elem_size(grad_dtype);
+    const bool any = dX || dWg || dbias_g || dbias_u;
+    PGEMM_TRY(check_matrix(dH, M, N, lddh, es, any));
+    PGEMM_TRY(check_matrix(G, M, N, ldg, es, any));
+    PGEMM_TRY(check_matrix(U, M, N, ldu, es, any));
+    PGEMM_TRY(check_matrix(X, M, K, ldx, es, dWg && N > 0));
+    PGEMM_TRY(check_weight(Wg, N, K, ldw, w_order, es, dX && M > 0));
+    PGEMM_TRY(check_weight(Wu, N, K, ldw, w_order, es, dX && M > 0));
+    PGEMM_TRY(check_matrix(dX, M, K, lddx, es, false));
+    PGEMM_TRY(check_weight(dWg, N, K, lddw, dw_order, gs, false));
+    PGEMM_TRY(check_weight(dWu, N, K, lddw, dw_order, gs, false));
+    PGEMM_TRY(check_vector(dbias_g, gs));
+    PGEMM_TRY(check_vector(dbias_u, gs));
+    PGEMM_TRY(check_workspace(workspace, workspace_bytes, backward_workspace(M, N, K, act, dtype, 2)));
+    Grad q;
+    std::memset(&q, 0, sizeof(q));
+    q.dY = dH;
+    q.lddy = lddh;
+    q.X = X;
+    q.ldx = ldx;
+    q.W[0] = Wg;
+    q.W[1] = Wu;
+    q.ldw = ldw;
+    q.Z = G;
+    q.ldz = ldg;
+    q.U = U;
+    q.ldu = ldu;
+    q.dX = dX;
+    q.lddx = lddx;
+    q.dW[0] = dWg;
+    q.dW[1] = dWu;
+    q.lddw = lddw;
+    q.db[0] = dbias_g;
+    q.db[1] = dbias_u;
+    return run_backward(M, N, K, q, w_order, dw_order, act, grad_dtype, dtype, 2, workspace, (hipStream_t)stream);
+}
+
+}  // extern "C"

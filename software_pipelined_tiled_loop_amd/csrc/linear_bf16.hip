@@ -1,0 +1,12 @@
+// linear_bf16.hip -- feed-forward operators on bf16 operands (fp32 accumulation).
+#include "linear_variants.hpp"
+
+namespace pgemm {
+
+static const LinVariant k_table[] = {
+    LIN_CLASS(DT_BF16, 128, 128, 64, 2, 2, 2),  // 4 waves of 64 x 64
+};
+
+LinKernels linear_kernels_bf16() { return LIN_KERNELS(DT_BF16, k_table); }
+
+}  // namespace pgemm

@@ -1,0 +1,799 @@
+// linear_kernel.hpp -- the feed-forward operators' kernels for gfx950: a
+// matrix product with a fused epilogue (bias, activation, residual, the kept
+// pre-activations), the gated block (two products, activation and product in
+// one kernel), and the products of both backward passes.
+//
+// Mathematics.  With A the activations (rows m, contraction index k) and B
+// the weights (columns n):
+//     acc[m][n] = sum_k A(m, k) B(k, n)
+//     linear   Z = acc + b,  Y = act(Z) + R
+//     gated    G = acc_g + bg,  U = acc_u + bu,  H = act(G) U
+// The backward pass is made of the same products with other operands:
+//     dX = dZ W^T (gated: dG Wg^T + dU Wu^T, one contraction over both
+//     halves), dW = X^T dZ (gated: two outputs of one launch sharing X).
+//
+// Operand layouts.  Each operand is stored either with the contraction index
+// contiguous (LAY_K: X, dZ as left operand, W stored [N][K], W as operand of
+// dX) or with its row / column index contiguous (LAY_X: W stored [K][N], X and
+// dZ as operands of dW).  Both are copied to LDS as they lie in memory, by
+// LDS-DMA (buffer_load_dwordx4 ... lds), in 16-byte chunks XOR-swizzled as in
+// pgemm_kernel.hpp; LAY_K fragments are read with ds_read_b128, LAY_X ones
+// with the transposing reads (fp32: ds_read_b32).  So no operand is ever
+// transposed in memory, forward or backward.
+//
+// The MFMAs are issued with the operands exchanged (B fragment first): the
+// result block then holds, in each lane, four consecutive columns n of one
+// row m, so bias, residual and outputs move as 8-byte (16-bit types) or
+// 16-byte (fp32) vectors instead of single elements.
+//
+// K loop: a ring of S LDS stages with one barrier per K tile, as in
+// pgemm_kernel.hpp.  Only whole K tiles of the contraction go through the
+// ring.  The last one, when it is cut by the end of K, or when an operand's
+// contiguous extent is not whole 16-byte chunks (a chunk of its last rows
+// could then end past the allocation), is loaded after the ring has drained,
+// through registers, with element loads where a chunk straddles an edge and
+// zeros beyond the edge.  Rows and columns beyond the output's edge load
+// zeros, or values that feed only outputs which are never stored.
+#pragma once
+
+#include "pgemm_kernel.hpp"
+
+namespace pgemm {
+
+enum Lay : int { LAY_K = 0, LAY_X = 1 };
+enum ActKind : int { ACTK_NONE = 0, ACTK_RELU = 1, ACTK_SILU = 2, ACTK_GELU = 3, ACTK_GELU_TANH = 4 };
+
+// Activations silu, gelu and gelu_tanh share one form,
+//     act(x) = x * sigmoid(x * P(x^2)):
+//   silu       P = 1
+//   gelu_tanh  P = sqrt(8/pi) (1 + 0.044715 t): (1 + tanh a)/2 = sigmoid(2a)
+//   gelu       P = degree-6 fit of logit(Phi(x)) / x in t = x^2 up to
+//              t = kGeluCap, constant beyond (weighted least squares iterated
+//              towards the minimax of x Phi(x)):
+//              |x sigmoid(x P) - x Phi(x)| < 7e-8 for every x
+// and the slopes
+//     act'(x) = p + x p (1 - p) (P + 2 t P'),  p = sigmoid(x P)
+// (gelu: Phi + x phi, phi(x) = exp(-x^2/2) / sqrt(2 pi)).
+struct ActArgs {
+    int kind;      // ActKind
+    float c[7];    // coefficients of -log2(e) * P: sigmoid(x P) = 1 / (1 + exp2(x c(t)))
+};
+constexpr float kGeluCap = 30.25f;
+
+struct EpiArgs {
+    void* Y[2];           // output (gated: H); two for a launch with two outputs side by side (dWg, dWu)
+    int64_t ldy;
+    const void* R;        // residual, Y's type
+    int64_t ldr;
+    void* Z;              // kept pre-activation (gated: G), operand type; may be null
+    void* U;              // gated: kept U
+    int64_t ldz, ldu;
+    const void* bias[2];  // operand type; may be null (gated: bg, bu)
+    ActArgs act;
+    int M, N;
+    int out_f32;          // Y and R are fp32 (else the operand type)
+};
+
+struct LinArgs {
+    const void* A[2];     // of contraction half h, or of output `out` where there are two
+    const void* B[2];     // likewise; gated: Wg, Wu
+    int64_t lda, ldb;
+    int K;                // contraction length of one half
+    int nfull;            // K tiles of a half that go through the ring
+    int halves;           // contraction halves (1, or 2 for the gated dX)
+    int outs;             // outputs side by side (1, or 2 for the gated dW)
+    int tiles_m, tiles_n, group_m;
+    int splits;           // workgroups that share one output tile's K tiles
+    float* part;          // fp32 sums of each split: [split][plane][M][np4] (planes: outs, or 2 for gated)
+    int np4;
+    EpiArgs e;
+};
+
+// ---- one operand's LDS tile: EXT rows (or columns) by BK of the contraction --------------
+
+template <int D, int LAY, int EXT, int BK>
+struct Opnd {
+    static constexpr int ES = Traits<D>::ES, EPC = Traits<D>::EPC, KSTEP = Traits<D>::KSTEP;
+    static constexpr int KC = BK * ES / 16, NCH = EXT * ES / 16;
+    static constexpr int BYTES = EXT * BK * ES;
+    // LDS reads of one fragment
+    static constexpr int READS = LAY == LAY_K ? 1 : (ES == 4 ? 4 : 2);
+    static_assert(BYTES % 1024 == 0, "tile must be whole 1-KiB blocks");
+    static_assert(LAY != LAY_K || KC == 4 || KC == 8, "rows must be 64 or 128 bytes");
+    static_assert(LAY != LAY_X || ((NCH & (NCH - 1)) == 0 && NCH >= 4 && EXT * ES <= 1024), "bad row of the tile");
+
+    // Memory chunk that sits at LDS byte `off` of the tile: extent index e
+    // and contraction index k of its first element.
+    static PGEMM_HD void chunk(int off, int& e, int& k) {
+        if constexpr (LAY == LAY_K) {
+            int kc;
+            a_inv<KC>(off, e, kc);
+            k = kc * EPC;
+        } else {
+            k = off / (EXT * ES);
+            e = (((off % (EXT * ES)) >> 4) ^ b_swz<D, NCH>(k)) * EPC;
+        }
+    }
+    // LDS byte that `lane` addresses for read h of the fragment of extent
+    // block e0 .. e0+15 at K step ks (lane semantics of the transposing reads:
+    // b_frag_off in pgemm_kernel.hpp).
+    static PGEMM_HD int frag(int ks, int e0, int lane, int h) {
+        const int li = lane & 15, lg = lane >> 4;
+        if constexpr (LAY == LAY_K) {
+            return a_off<KC>(e0 + li, ks * 4 + lg);
+        } else {
+            int k, e;
+            if constexpr (ES == 2) {
+                k = ks * KSTEP + 8 * lg + 4 * h + (li >> 2);
+                e = e0 + 4 * (li & 3);
+            } else {
+                k = ks * KSTEP + 4 * lg + h;
+                e = e0 + li;
+            }
+            return k * EXT * ES + (((e / EPC) ^ b_swz<D, NCH>(k)) << 4) + (e % EPC) * ES;
+        }
+    }
+    static __device__ __forceinline__ void read(const char PGEMM_LDS* tile, int ks, int e0, int lane, i32x4& out) {
+        if constexpr (LAY == LAY_K) {
+            out = *(const i32x4 PGEMM_LDS*)(tile + frag(ks, e0, lane, 0));
+        } else if constexpr (ES == 2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const i16x4 v =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((i16x4 PGEMM_LDS*)(tile + frag(ks, e0, lane, h)));
+                const i32x2 w = __builtin_bit_cast(i32x2, v);
+                out[2 * h] = w[0];
+                out[2 * h + 1] = w[1];
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) out[h] = *(const int PGEMM_LDS*)(tile + frag(ks, e0, lane, h));
+        }
+    }
+    // Byte offset in memory of the chunk (e, k) from the tile's origin.
+    static PGEMM_HD uint32_t mem_off(int e, int k, int64_t ld) {
+        return LAY == LAY_K ? (uint32_t)(e * (int)ld + k) * ES : (uint32_t)(k * (int)ld + e) * ES;
+    }
+    // Bytes from the matrix's origin to the tile at extent e0, K tile kt.
+    static PGEMM_HD int64_t origin(int64_t e0, int64_t kt, int64_t ld) {
+        return (LAY == LAY_K ? e0 * ld + kt * BK : kt * BK * ld + e0) * ES;
+    }
+    static PGEMM_HD int64_t step(int64_t ld) { return (LAY == LAY_K ? (int64_t)BK : (int64_t)BK * ld) * ES; }
+
+    // Elements of chunk (e, k) inside a matrix that ends at (e_left, k_left).
+    static PGEMM_HD int cut_valid(int e, int k, int e_left, int k_left) {
+        const int in_row = LAY == LAY_K ? k_left - k : e_left - e;
+        const bool row_ok = LAY == LAY_K ? e < e_left : k < k_left;
+        return !row_ok || in_row <= 0 ? 0 : in_row < EPC ? in_row : EPC;
+    }
+    // How many of K's K tiles may go through the ring, whose 16-byte loads
+    // check an extent index against the operand's edge only where the chunk
+    // starts: whole tiles, and for LAY_X rows that are not whole chunks only
+    // as many that a chunk straddling the edge in the last row loaded ends
+    // inside the rows behind it.
+    static PGEMM_HD int ring_tiles(int64_t K, int64_t extent, int64_t ld) {
+        int64_t n = K / BK;
+        if (LAY == LAY_X && extent % EPC != 0)
+            while (n > 0 && (K - n * BK) * ld < EPC - 1) --n;
+        return (int)n;
+    }
+
+    // The cut K tile, through registers: blocks [p0, p0 + n) of 1 KiB, chunks
+    // cut at `e_left` / `k_left` completed by element loads, zeros beyond.
+    static __device__ __forceinline__ void load_cut(const char* mem, int64_t ld, int e_left, int k_left,
+                                                    char PGEMM_LDS* tile, int p0, int n, int lane) {
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(mem);
+        for (int p = p0; p < p0 + n; ++p) {
+            int e, k;
+            chunk(p * 1024 + lane * 16, e, k);
+            const int valid = cut_valid(e, k, e_left, k_left);
+            *(i32x4 PGEMM_LDS*)(tile + p * 1024 + lane * 16) =
+                load_chunk_any<ES>(r, mem_off(e, k, ld), valid, valid == EPC);
+        }
+    }
+};
+
+// One MFMA block with the operands exchanged: lane l of the result holds
+// columns 4*(l/16) .. +3 (of the B block) of row l%16 (of the A block).
+template <int D>
+__device__ __forceinline__ void mfma_swapped(f32x4& acc, const i32x4& a, const i32x4& b) {
+    if constexpr (D == DT_BF16) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a),
+                                                      acc, 0, 0, 0);
+    } else if constexpr (D == DT_F16) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), acc,
+                                                     0, 0, 0);
+    } else {
+        const f32x4 af = __builtin_bit_cast(f32x4, a);  // whole vectors: see mfma_block
+        const f32x4 bf = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+        for (int jm = 0; jm < 4; ++jm) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[jm], af[jm], acc, 0, 0, 0);
+    }
+}
+
+// ---- values: four consecutive columns of a row ---------------------------------------------
+
+template <int D> struct Elem { typedef __bf16 type; };
+template <> struct Elem<DT_F16> { typedef _Float16 type; };
+template <> struct Elem<DT_F32> { typedef float type; };
+
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+template <class T> struct Vec4 { typedef f32x4 type; };
+template <> struct Vec4<__bf16> { typedef bf16x4 type; };
+template <> struct Vec4<_Float16> { typedef f16x4 type; };
+
+// Four elements at byte offset `off`, the first `valid` of them inside the
+// matrix (zeros for the others).  `cut` (uniform): some group of this launch
+// has 0 < valid < 4.
+template <class T>
+__device__ __forceinline__ f32x4 load4(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid, bool cut) {
+    const uint32_t o = valid >= 4 ? off : OOB;
+    f32x4 v;
+    if constexpr (sizeof(T) == 4) {
+        v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+    } else {
+        const i32x2 w = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0));
+        const typename Vec4<T>::type h = __builtin_bit_cast(typename Vec4<T>::type, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
+    }
+    if (cut && valid > 0 && valid < 4) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            const uint32_t oe = e < valid ? off + (uint32_t)(e * sizeof(T)) : OOB;
+            if constexpr (sizeof(T) == 4) {
+                v[e] = __builtin_bit_cast(float, (int)__builtin_amdgcn_raw_buffer_load_b32(r, oe, 0, 0));
+            } else {
+                v[e] = (float)__builtin_bit_cast(T, (short)__builtin_amdgcn_raw_buffer_load_b16(r, oe, 0, 0));
+            }
+        }
+    }
+    return v;
+}
+
+// Stores round to the output's type, to nearest even, once.
+template <class T>
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid, bool cut, f32x4 v) {
+    const uint32_t o = valid >= 4 ? off : OOB;
+    typename Vec4<T>::type h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = (T)v[e];
+    if constexpr (sizeof(T) == 4)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, h), r, o, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2, h), r, o, 0, 0);
+    if (cut && valid > 0 && valid < 4) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            const uint32_t oe = e < valid ? off + (uint32_t)(e * sizeof(T)) : OOB;
+            if constexpr (sizeof(T) == 4)
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, (float)h[e]), r, oe, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (T)h[e]), r, oe, 0, 0);
+        }
+    }
+}
+
+// -log2(e) * P(t), so that sigmoid(x P) = 1 / (1 + exp2(x c(t))).
+template <int DEG>
+__device__ __forceinline__ float act_poly(const ActArgs& a, float t) {
+    float p = a.c[DEG];
+#pragma unroll
+    for (int d = DEG - 1; d >= 0; --d) p = fmaf(p, t, a.c[d]);
+    return p;
+}
+
+template <int DEG>
+__device__ __forceinline__ f32x4 act_smooth4(const ActArgs& a, f32x4 x) {
+    f32x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float p = DEG == 0 ? a.c[0] : act_poly<DEG>(a, DEG == 6 ? fminf(x[e] * x[e], kGeluCap) : x[e] * x[e]);
+        y[e] = x[e] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[e] * p));
+    }
+    return y;
+}
+
+__device__ __forceinline__ f32x4 act4(const ActArgs& a, f32x4 x) {
+    f32x4 y;
+    switch (a.kind) {
+        case ACTK_NONE: return x;
+        case ACTK_RELU:
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = x[e] < 0.0f ? 0.0f : x[e];  // NaN stays NaN
+            return y;
+        case ACTK_SILU: return act_smooth4<0>(a, x);
+        case ACTK_GELU_TANH: return act_smooth4<1>(a, x);
+        default: return act_smooth4<6>(a, x);
+    }
+}
+
+// act(x) and act'(x) of a smooth activation.  The exponent is held below 2^120
+// so that e p = 1 - p stays finite where p vanishes.
+template <int DEG>
+__device__ __forceinline__ void act_slope(const ActArgs& a, float x, float& y, float& d) {
+    const float t = x * x;
+    const float c = DEG == 0 ? a.c[0] : act_poly<DEG>(a, DEG == 6 ? fminf(t, kGeluCap) : t);
+    const float e = __builtin_amdgcn_exp2f(fminf(x * c, 120.0f));
+    const float p = __builtin_amdgcn_rcpf(1.0f + e);
+    y = x * p;
+    if constexpr (DEG == 6) {
+        // Phi + x phi, phi(x) = exp2(-t log2(e) / 2) / sqrt(2 pi)
+        d = fmaf(x, 0.3989422804f * __builtin_amdgcn_exp2f(-0.7213475204f * t), p);
+    } else {
+        // d(x P)/dx = P + 2 t P', from the coefficients of -log2(e) P
+        const float s = -0.6931471806f * (DEG == 1 ? fmaf(2.0f * t, a.c[1], c) : c);
+        d = fmaf(y * s, e * p, p);
+    }
+}
+__device__ __forceinline__ void act_slope4(const ActArgs& a, f32x4 x, f32x4& y, f32x4& d) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float yi, di;
+        switch (a.kind) {
+            case ACTK_NONE: yi = x[i]; di = 1.0f; break;
+            case ACTK_RELU: yi = x[i] < 0.0f ? 0.0f : x[i]; di = x[i] > 0.0f ? 1.0f : 0.0f; break;
+            case ACTK_SILU: act_slope<0>(a, x[i], yi, di); break;
+            case ACTK_GELU_TANH: act_slope<1>(a, x[i], yi, di); break;
+            default: act_slope<6>(a, x[i], yi, di); break;
+        }
+        y[i] = yi;
+        d[i] = di;
+    }
+}
+
+// The fused epilogue of one tile: rows and columns relative to (m0, n0).
+template <int D, bool GATED>
+struct Epi {
+    typedef typename Elem<D>::type T;
+    __amdgpu_buffer_rsrc_t y, r, z, u;
+    int rows, cols;
+    bool cut;
+
+    __device__ __forceinline__ Epi(const EpiArgs& e, int m0, int n0, int out) {
+        const int64_t ys = e.out_f32 ? 4 : sizeof(T);
+        y = make_rsrc((char*)(out ? e.Y[1] : e.Y[0]) + (m0 * e.ldy + n0) * ys);
+        r = make_rsrc(e.R ? (const char*)e.R + (m0 * e.ldr + n0) * ys : nullptr);
+        z = make_rsrc(e.Z ? (char*)e.Z + (m0 * e.ldz + n0) * (int64_t)sizeof(T) : nullptr);
+        u = make_rsrc(e.U ? (char*)e.U + (m0 * e.ldu + n0) * (int64_t)sizeof(T) : nullptr);
+        rows = e.M - m0;
+        cols = e.N - n0;
+        cut = (e.N & 3) != 0;
+    }
+    __device__ __forceinline__ int valid(int row, int col) const { return row < rows ? cols - col : 0; }
+    // Bias of columns col .. col+3 (col relative to n0).
+    static __device__ __forceinline__ f32x4 bias(const EpiArgs& e, int which, int n0, int col) {
+        if (!e.bias[which]) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        return load4<T>(make_rsrc((const T*)e.bias[which] + n0), (uint32_t)(col * sizeof(T)), e.N - n0 - col,
+                        (e.N & 3) != 0);
+    }
+    __device__ __forceinline__ void put(const EpiArgs& e, int row, int col, f32x4 v, f32x4 w, const f32x4& b0,
+                                        const f32x4& b1) const {
+        const int ok = valid(row, col);
+        v += b0;
+        if (e.Z) store4<T>(z, (uint32_t)(row * (int)e.ldz + col) * sizeof(T), ok, cut, v);
+        v = act4(e.act, v);
+        if constexpr (GATED) {
+            w += b1;
+            if (e.U) store4<T>(u, (uint32_t)(row * (int)e.ldu + col) * sizeof(T), ok, cut, w);
+            v *= w;
+        }
+        if (sizeof(T) == 4 || e.out_f32) {
+            if (e.R) v += load4<float>(r, (uint32_t)(row * (int)e.ldr + col) * 4u, ok, cut);
+            store4<float>(y, (uint32_t)(row * (int)e.ldy + col) * 4u, ok, cut, v);
+        } else {
+            if (e.R) v += load4<T>(r, (uint32_t)(row * (int)e.ldr + col) * sizeof(T), ok, cut);
+            store4<T>(y, (uint32_t)(row * (int)e.ldy + col) * sizeof(T), ok, cut, v);
+        }
+    }
+};
+
+// ---- the tile kernel ---------------------------------------------------------------------------
+
+template <int D, int LA_, int LB_, int BM_, int BN_, int BK_, int S_, int WGM_, int WGN_, bool GATED_>
+struct LinCfg {
+    static constexpr int Dt = D, BM = BM_, BN = BN_, BK = BK_, S = S_, WGM = WGM_, WGN = WGN_;
+    static constexpr bool GATED = GATED_;
+    typedef Traits<D> T;
+    static constexpr int ES = T::ES;
+    static constexpr int NP = GATED ? 2 : 1;   // B panels side by side in LDS (gated: Wg, Wu)
+    static constexpr int BNP = BN / NP;        // output columns of the tile
+    typedef Opnd<D, LA_, BM, BK> OA;
+    typedef Opnd<D, LB_, BNP, BK> OB;
+    static constexpr int NW = WGM * WGN, NT = 64 * NW;
+    static constexpr int WM = BM / WGM, WNP = BNP / WGN;
+    static constexpr int FM = WM / 16, FNP = WNP / 16, FN = FNP * NP;
+    static constexpr int A_BYTES = OA::BYTES, B_BYTES = OB::BYTES * NP;
+    static constexpr int STAGE = A_BYTES + B_BYTES, LDS = S * STAGE;
+    static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW, LPS = A_INSTR + B_INSTR;
+    static constexpr int NKS = BK / T::KSTEP;
+    static_assert(NKS == 2, "the loop body is written for two K steps per K tile");
+    static_assert(A_BYTES % (1024 * NW) == 0 && OB::BYTES % (1024 * (NW / NP)) == 0, "1-KiB blocks per wave");
+    static_assert(LDS <= 163840 && S >= 2 && S <= 4 && LPS * (S - 2) <= 63, "ring");
+};
+
+template <class C>
+struct LinFrags {
+    i32x4 a[C::FM];
+    i32x4 b[C::FN];
+};
+
+// The wave's side of the producer: next K tile to load and this wave's
+// 1-KiB blocks of it.
+template <class C>
+struct LinSrc {
+    const char* pa;        // next K tile of A and of the wave's B panel
+    const char* pb;
+    const char* ha;        // first K tile of the second contraction half
+    const char* hb;
+    int64_t sa, sb;        // bytes from one K tile to the next
+    int next, nfull;       // K tile within its half, K tiles per half
+    int left;              // K tiles still to load
+    uint32_t va[C::A_INSTR], vb[C::B_INSTR];  // each lane's offset from the K tile's origin
+    i32x4 ra, rb;
+
+    // The descriptors of the next K tile; slots past the last one get an
+    // empty range, so every lane reads zeros.
+    __device__ __forceinline__ void arm() {
+        ra = make_rsrc_sgpr(pa);
+        rb = make_rsrc_sgpr(pb);
+        ra[2] = rb[2] = left > 0 ? (int)0x80000000u : 0;
+        --left;
+        ++next;
+        const bool turn = next == nfull;
+        pa = turn ? ha : pa + sa;
+        pb = turn ? hb : pb + sb;
+    }
+    template <int Q>
+    __device__ __forceinline__ void piece(uint32_t sa_lds, uint32_t sb_lds) const {
+        if constexpr (Q < C::A_INSTR)
+            dma16(ra, va[Q], sa_lds + (uint32_t)Q * 1024u);
+        else
+            dma16(rb, vb[Q - C::A_INSTR], sb_lds + (uint32_t)(Q - C::A_INSTR) * 1024u);
+    }
+};
+
+template <class C, int Q0, int Q1>
+__device__ __forceinline__ void lin_pieces(const LinSrc<C>& s, uint32_t a, uint32_t b) {
+    if constexpr (Q0 < Q1) {
+        s.template piece<Q0>(a, b);
+        lin_pieces<C, Q0 + 1, Q1>(s, a, b);
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void lin_read(const char PGEMM_LDS* stage, int ks, int r, int wm0, int wnp, int lane,
+                                         LinFrags<C>& f) {
+    // order b0, a0, b1 .. , a1 ..: the order in which the MFMAs need them
+    if (r == 1 || r > C::FN) {
+        const int i = r == 1 ? 0 : r - C::FN;
+        C::OA::read(stage, ks, wm0 + 16 * i, lane, f.a[i]);
+    } else {
+        const int j = r == 0 ? 0 : r - 1;
+        const int panel = j / C::FNP;
+        C::OB::read(stage + C::A_BYTES + panel * C::OB::BYTES, ks, wnp + 16 * (j % C::FNP), lane, f.b[j]);
+    }
+}
+
+// The MFMAs of one K step in eight groups; after each, a share of the next
+// K tile's LDS-DMA blocks (DMA) and of the next step's fragment reads.
+template <class C, bool READS, bool DMA, int G = 0>
+__device__ __forceinline__ void lin_step(f32x4 (&acc)[C::FM][C::FN], const LinFrags<C>& use, LinFrags<C>& nxt,
+                                         const char PGEMM_LDS* rstage, int rks, const LinSrc<C>& src, uint32_t sa,
+                                         uint32_t sb, int wm0, int wnp, int lane) {
+    constexpr int NMF = C::FM * C::FN, NG = NMF < 8 ? NMF : 8, GS = NMF / NG;
+    constexpr int NR = C::FM + C::FN, RPG = (NR + NG - 1) / NG, PPG = (C::LPS + NG - 1) / NG;
+    if constexpr (G < NG) {
+#pragma unroll
+        for (int m = G * GS; m < (G + 1) * GS; ++m)
+            mfma_swapped<C::Dt>(acc[m / C::FN][m % C::FN], use.a[m / C::FN], use.b[m % C::FN]);
+        if constexpr (DMA) {
+            constexpr int P0 = G * PPG < C::LPS ? G * PPG : C::LPS;
+            constexpr int P1 = (G + 1) * PPG < C::LPS ? (G + 1) * PPG : C::LPS;
+            lin_pieces<C, P0, P1>(src, sa, sb);
+        }
+        if constexpr (READS) {
+#pragma unroll
+            for (int r = G * RPG; r < (G + 1) * RPG; ++r)
+                if (r < NR) lin_read<C>(rstage, rks, r, wm0, wnp, lane, nxt);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        lin_step<C, READS, DMA, G + 1>(acc, use, nxt, rstage, rks, src, sa, sb, wm0, wnp, lane);
+    }
+}
+
+// Full wait of this wave's loads and LDS operations, then the barrier.
+__device__ __forceinline__ void drain_barrier() { wait_barrier<0>(); }
+
+template <class C>
+__global__ void __launch_bounds__(C::NT, 2) linear_kernel(LinArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS];
+    char PGEMM_LDS* smem = (char PGEMM_LDS*)smem_raw;
+    typedef typename C::OA OA;
+    typedef typename C::OB OB;
+
+    // Logical tiles: output tiles in a grouped raster, split-major, one
+    // contiguous range per XCD (wg_tiles_of).
+    const int tiles_n = g.tiles_n * g.outs, per_split = g.tiles_m * tiles_n;
+    const WgTiles w = wg_tiles_of(per_split * g.splits, (int)blockIdx.x, (int)gridDim.x);
+    if (w.count == 0) return;
+    int L = w.start + w.lb, split = 0;
+    if (g.splits > 1) {
+        split = L / per_split;
+        L -= split * per_split;
+    }
+    int tm, tn;
+    raster(L, g.tiles_m, tiles_n, g.group_m, tm, tn);
+    const int out = tn >= g.tiles_n ? 1 : 0;
+    tn -= out * g.tiles_n;
+    const int m0 = tm * C::BM, n0 = tn * C::BNP;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm0 = (wave / C::WGN) * C::WM;
+    const int wnp = (wave % C::WGN) * C::WNP;
+    const int rows_left = g.e.M - m0, cols_left = g.e.N - n0;
+
+    f32x4 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // This split's K tiles of the ring: [t0, t1) of both halves' nfull.
+    const int64_t total = (int64_t)g.nfull * g.halves;
+    const int t0 = (int)(total * split / g.splits), t1 = (int)(total * (split + 1) / g.splits);
+    const int panel = C::NP == 2 ? wave / (C::NW / 2) : 0;  // the wave's blocks of B lie in one panel
+    const int b_block = wave * C::B_INSTR - panel * (OB::BYTES / 1024);
+    const int b_base = C::A_BYTES + wave * C::B_INSTR * 1024, a_base = wave * C::A_INSTR * 1024;
+    const char* a_half[2];
+    const char* b_half[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = g.outs == 2 ? out : h < g.halves ? h : 0;
+        a_half[h] = (const char*)g.A[i] + OA::origin(m0, 0, g.lda);
+        b_half[h] = (const char*)g.B[C::NP == 2 ? panel : i] + OB::origin(n0, 0, g.ldb);
+    }
+
+    if (t1 > t0) {
+        LinSrc<C> src;
+        const int half = t0 >= g.nfull ? 1 : 0;
+        src.next = t0 - half * g.nfull;
+        src.nfull = half ? 0x7fffffff : g.nfull;
+        src.left = t1 - t0;
+        src.sa = OA::step(g.lda);
+        src.sb = OB::step(g.ldb);
+        src.pa = a_half[half] + src.sa * src.next;
+        src.pb = b_half[half] + src.sb * src.next;
+        src.ha = a_half[1];
+        src.hb = b_half[1];
+#pragma unroll
+        for (int q = 0; q < C::A_INSTR; ++q) {
+            int e, k;
+            OA::chunk(a_base + q * 1024 + lane * 16, e, k);
+            src.va[q] = e < rows_left ? OA::mem_off(e, k, g.lda) : OOB;
+        }
+#pragma unroll
+        for (int q = 0; q < C::B_INSTR; ++q) {
+            int e, k;
+            OB::chunk((b_block + q) * 1024 + lane * 16, e, k);
+            src.vb[q] = e < cols_left ? OB::mem_off(e, k, g.ldb) : OOB;
+        }
+
+        const uint32_t lds0 = (uint32_t)(size_t)smem;
+        // Prologue: slots 0 .. S-2.
+#pragma unroll
+        for (int p = 0; p < C::S - 1; ++p) {
+            src.arm();
+            lin_pieces<C, 0, C::LPS>(src, lds0 + p * C::STAGE + a_base, lds0 + p * C::STAGE + b_base);
+        }
+        wait_barrier<C::LPS*(C::S - 2)>();
+        src.arm();
+        lin_pieces<C, 0, C::LPS>(src, lds0 + (C::S - 1) * C::STAGE + a_base, lds0 + (C::S - 1) * C::STAGE + b_base);
+        LinFrags<C> f[2];
+#pragma unroll
+        for (int r = 0; r < C::FM + C::FN; ++r) lin_read<C>(smem, 0, r, wm0, wnp, lane, f[0]);
+        int cur = 0;
+        for (int t = t0; t < t1; ++t) {
+            const int nst = cur + 1 == C::S ? 0 : cur + 1;
+            lin_step<C, true, false>(acc, f[0], f[1], smem + cur * C::STAGE, 1, src, 0, 0, wm0, wnp, lane);
+            wait_barrier<C::LPS*(C::S - 2)>();  // K tile t+1 is in LDS, stage `cur` is free
+            src.arm();
+            const uint32_t freed = lds0 + cur * C::STAGE;
+            lin_step<C, true, true>(acc, f[1], f[0], smem + nst * C::STAGE, 0, src, freed + a_base, freed + b_base,
+                                    wm0, wnp, lane);
+            cur = nst;
+        }
+        __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing LDS
+    }
+
+    // What is left of each half after the ring's K tiles, by the last split.
+    if (split == g.splits - 1) {
+        const int ncut = (g.K + C::BK - 1) / C::BK - g.nfull;
+        for (int c = 0; c < ncut * g.halves; ++c) {
+            const int h = c >= ncut ? 1 : 0, kt = g.nfull + c - h * ncut, k_left = g.K - kt * C::BK;
+            drain_barrier();  // every wave has read the stage
+            OA::load_cut((h ? a_half[1] : a_half[0]) + OA::step(g.lda) * kt, g.lda, rows_left, k_left, smem,
+                         wave * C::A_INSTR, C::A_INSTR, lane);
+            OB::load_cut((h ? b_half[1] : b_half[0]) + OB::step(g.ldb) * kt, g.ldb, cols_left, k_left,
+                         smem + C::A_BYTES + panel * OB::BYTES, b_block, C::B_INSTR, lane);
+            drain_barrier();
+            LinFrags<C> f;
+#pragma unroll
+            for (int ks = 0; ks < C::NKS; ++ks) {
+#pragma unroll
+                for (int r = 0; r < C::FM + C::FN; ++r) lin_read<C>(smem, ks, r, wm0, wnp, lane, f);
+#pragma unroll
+                for (int m = 0; m < C::FM * C::FN; ++m)
+                    mfma_swapped<C::Dt>(acc[m / C::FN][m % C::FN], f.a[m / C::FN], f.b[m % C::FN]);
+            }
+        }
+    }
+
+    const int li = lane & 15, lg4 = 4 * (lane >> 4);
+    if (g.part) {
+        // fp32 sums of this split, joined by linear_join in the order of the splits
+        const int planes = C::GATED ? 2 : g.outs;
+        float* base = g.part + ((int64_t)split * planes + out) * g.e.M * g.np4;
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+            const int row = m0 + wm0 + 16 * i + li;
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+                const int col = n0 + wnp + 16 * (j % C::FNP) + lg4;
+                if (row < g.e.M && col < g.np4)
+                    *(f32x4*)(base + ((int64_t)(j / C::FNP) * g.e.M + row) * g.np4 + col) = acc[i][j];
+            }
+        }
+        return;
+    }
+    const Epi<C::Dt, C::GATED> ep(g.e, m0, n0, out);
+    f32x4 b0[C::FNP], b1[C::FNP];
+#pragma unroll
+    for (int j = 0; j < C::FNP; ++j) {
+        b0[j] = Epi<C::Dt, C::GATED>::bias(g.e, 0, n0, wnp + 16 * j + lg4);
+        b1[j] = C::GATED ? Epi<C::Dt, C::GATED>::bias(g.e, 1, n0, wnp + 16 * j + lg4) : b0[j];
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < C::FNP; ++j)
+            ep.put(g.e, wm0 + 16 * i + li, wnp + 16 * j + lg4, acc[i][j], acc[i][C::GATED ? j + C::FNP : j], b0[j],
+                   b1[j]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// ---- join of the splits ---------------------------------------------------------------------------
+
+// One thread per four columns of a row: the splits' sums in the order of the
+// splits, then the epilogue.  A workgroup covers one row's stretch of 1024
+// columns.
+template <int D, bool GATED>
+__global__ void __launch_bounds__(256) linear_join(LinArgs g) {
+    const int strips = (g.np4 + 1023) / 1024;
+    int b = (int)blockIdx.x;
+    const int strip = b % strips;
+    b /= strips;
+    const int m = b % g.e.M, out = b / g.e.M;
+    const int n0 = strip * 1024, col = 4 * (int)threadIdx.x;
+    if (n0 + col >= g.np4) return;
+    const int planes = GATED ? 2 : g.outs;
+    const int64_t plane = (int64_t)g.e.M * g.np4;
+    const float* p = g.part + out * plane + (int64_t)m * g.np4 + n0 + col;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, w = v;
+    for (int s = 0; s < g.splits; ++s) {
+        v += *(const f32x4*)p;
+        if constexpr (GATED) w += *(const f32x4*)(p + plane);
+        p += planes * plane;
+    }
+    const Epi<D, GATED> ep(g.e, m, n0, out);
+    const f32x4 b0 = Epi<D, GATED>::bias(g.e, 0, n0, col);
+    const f32x4 b1 = GATED ? Epi<D, GATED>::bias(g.e, 1, n0, col) : b0;
+    ep.put(g.e, 0, col, v, w, b0, b1);
+}
+
+// ---- gradients at the pre-activations -----------------------------------------------------------
+
+// linear: dZ = dY act'(Z).  gated: dG = dH U act'(G), dU = dH act(G).
+// They are rounded to the operand type (the matrix cores take no wider one):
+// each factor of the products that follow then carries half a step of that
+// type, as X and W do, and the sums over them stay in fp32.  The column sums
+// (bias gradients) add the unrounded values.
+struct SlopeArgs {
+    const void* dY;
+    const void* Z;      // linear: Z; gated: G
+    const void* U;      // gated
+    void* dZ;           // gated: dG; null: column sums only
+    void* dU;
+    int64_t ldy, ldz, ldu, ldd;
+    float* sums;        // [row block][planes][np4] column sums; null: none
+    int np4;
+    int M, N;
+    ActArgs act;
+};
+
+constexpr int kSlopeRows = 64;   // rows per workgroup
+constexpr int kSlopeCols = 128;  // columns per workgroup: 32 threads of four columns
+
+template <int D, bool GATED>
+__global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
+    typedef typename Elem<D>::type T;
+    __shared__ f32x4 red[GATED ? 2 : 1][256];
+    const int strips = (g.N + kSlopeCols - 1) / kSlopeCols;
+    const int strip = (int)blockIdx.x % strips, block = (int)blockIdx.x / strips;
+    const int n0 = strip * kSlopeCols, m0 = block * kSlopeRows;
+    const int col = 4 * ((int)threadIdx.x & 31), r0 = (int)threadIdx.x >> 5;
+    const int rows = g.M - m0 < kSlopeRows ? g.M - m0 : kSlopeRows;
+    const int valid = g.N - n0 - col;
+    const bool cut = (g.N & 3) != 0;
+    const auto at = [&](const void* p, int64_t ld) {
+        return make_rsrc(p ? (const char*)p + (m0 * ld + n0) * (int64_t)sizeof(T) : nullptr);
+    };
+    const __amdgpu_buffer_rsrc_t ry = at(g.dY, g.ldy), rz = at(g.Z, g.ldz), ru = at(g.U, g.ldu), rd = at(g.dZ, g.ldd),
+                                 re = at(g.dU, g.ldd);
+    f32x4 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
+    for (int row = r0; row < rows; row += 8) {
+        const f32x4 dy = load4<T>(ry, (uint32_t)(row * (int)g.ldy + col) * sizeof(T), valid, cut);
+        f32x4 d = dy, e = s1;
+        if (GATED || g.act.kind != ACTK_NONE) {
+            const f32x4 z = load4<T>(rz, (uint32_t)(row * (int)g.ldz + col) * sizeof(T), valid, cut);
+            f32x4 y;
+            act_slope4(g.act, z, y, d);
+            d *= dy;
+            if constexpr (GATED) {
+                const f32x4 u = load4<T>(ru, (uint32_t)(row * (int)g.ldu + col) * sizeof(T), valid, cut);
+                d *= u;
+                e = dy * y;
+            }
+        }
+        s0 += d;
+        if constexpr (GATED) s1 += e;
+        if (g.dZ) {
+            // the workspace rows are whole groups: no partial store, and no
+            // lane beyond the row
+            const uint32_t o = (uint32_t)(row * (int)g.ldd + col) * sizeof(T);
+            const int all = valid > 0 ? 4 : 0;
+            store4<T>(rd, o, all, false, d);
+            if constexpr (GATED) store4<T>(re, o, all, false, e);
+        }
+    }
+    if (!g.sums) return;
+    // columns of the eight row groups, in their order
+    red[0][threadIdx.x] = s0;
+    if constexpr (GATED) red[1][threadIdx.x] = s1;
+    __syncthreads();
+    constexpr int planes = GATED ? 2 : 1;
+    if (threadIdx.x < 32 && valid > 0) {
+#pragma unroll
+        for (int p = 0; p < planes; ++p) {
+            f32x4 s = red[p][threadIdx.x];
+            for (int k = 1; k < 8; ++k) s += red[p][threadIdx.x + 32 * k];
+            *(f32x4*)(g.sums + ((int64_t)block * planes + p) * g.np4 + n0 + col) = s;
+        }
+    }
+}
+
+// Bias gradients: the row blocks' column sums, in their order.
+struct SumArgs {
+    const float* sums;  // [blocks][planes][np4]
+    void* out[2];       // planes; null: none
+    int blocks, planes, np4, N;
+    int out_f32;
+};
+
+template <int D>
+__global__ void __launch_bounds__(64) linear_colsum(SumArgs g) {
+    typedef typename Elem<D>::type T;
+    const int n = (int)blockIdx.x * 64 + (int)threadIdx.x, p = (int)blockIdx.y;
+    if (n >= g.N || !g.out[p]) return;
+    float s = 0.0f;
+    for (int b = 0; b < g.blocks; ++b) s += g.sums[((int64_t)b * g.planes + p) * g.np4 + n];
+    if (g.out_f32)
+        ((float*)g.out[p])[n] = s;
+    else
+        ((T*)g.out[p])[n] = (T)s;
+}
+
+}  // namespace pgemm

@@ -1,0 +1,87 @@
+// linear_variants.hpp -- the compiled kernels of the feed-forward operators (host side).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include "linear_kernel.hpp"
+
+namespace pgemm {
+
+typedef hipError_t (*LinLaunch)(const LinArgs&, int grid, hipStream_t);
+
+// Operand layouts of a product: activations times W [K][N] or W [N][K], and
+// X^T times dZ.
+enum LinLay : int { LIN_KX = 0, LIN_KK = 1, LIN_XX = 2 };
+
+struct LinVariant {
+    int lay, gated;
+    int bm, bn, bk;  // bn: output columns of the tile
+    int (*ring_tiles)(int64_t K, int64_t rows, int64_t lda, int64_t cols, int64_t ldb);
+    LinLaunch launch;
+};
+
+struct LinKernels {
+    const LinVariant* v;
+    int n;
+    LinLaunch join, join_gated;
+    hipError_t (*slope)(const SlopeArgs&, bool gated, int grid, hipStream_t);
+    hipError_t (*colsum)(const SumArgs&, int grid, hipStream_t);
+};
+
+template <class Args>
+hipError_t lin_launch(void (*kernel)(Args), const Args& a, dim3 grid, int threads, hipStream_t s) {
+    Args arg = a;
+    void* args[] = {&arg};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, 0, s);
+}
+
+template <class C>
+hipError_t lin_launch_tile(const LinArgs& a, int grid, hipStream_t s) {
+    return lin_launch<LinArgs>(&linear_kernel<C>, a, dim3(grid), C::NT, s);
+}
+template <class C>
+int lin_ring_tiles(int64_t K, int64_t rows, int64_t lda, int64_t cols, int64_t ldb) {
+    const int a = C::OA::ring_tiles(K, rows, lda), b = C::OB::ring_tiles(K, cols, ldb);
+    return a < b ? a : b;
+}
+template <int D, bool GATED>
+hipError_t lin_launch_join(const LinArgs& a, int grid, hipStream_t s) {
+    return lin_launch<LinArgs>(&linear_join<D, GATED>, a, dim3(grid), 256, s);
+}
+template <int D>
+hipError_t lin_launch_slope(const SlopeArgs& a, bool gated, int grid, hipStream_t s) {
+    return gated ? lin_launch<SlopeArgs>(&linear_slope<D, true>, a, dim3(grid), 256, s)
+                 : lin_launch<SlopeArgs>(&linear_slope<D, false>, a, dim3(grid), 256, s);
+}
+template <int D>
+hipError_t lin_launch_colsum(const SumArgs& a, int grid, hipStream_t s) {
+    return lin_launch<SumArgs>(&linear_colsum<D>, a, dim3(grid, a.planes), 64, s);
+}
+
+constexpr int lin_la(int lay) { return lay == LIN_XX ? LAY_X : LAY_K; }
+constexpr int lin_lb(int lay) { return lay == LIN_KK ? LAY_K : LAY_X; }
+
+#define LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN) \
+    LinCfg<D, lin_la(LAY), lin_lb(LAY), BM, BN, BK, S, WGM, WGN, GATED != 0>
+#define LIN_VARIANT(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)                                 \
+    LinVariant {                                                                            \
+        LAY, GATED, BM, GATED ? BN / 2 : BN, BK,                                            \
+            &lin_ring_tiles<LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)>,               \
+            &lin_launch_tile<LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)>               \
+    }
+// A tile class in every layout.
+#define LIN_CLASS(D, BM, BN, BK, S, WGM, WGN)                                                           \
+    LIN_VARIANT(D, LIN_KX, 0, BM, BN, BK, S, WGM, WGN), LIN_VARIANT(D, LIN_KK, 0, BM, BN, BK, S, WGM, WGN), \
+        LIN_VARIANT(D, LIN_KX, 1, BM, BN, BK, S, WGM, WGN), LIN_VARIANT(D, LIN_KK, 1, BM, BN, BK, S, WGM, WGN), \
+        LIN_VARIANT(D, LIN_XX, 0, BM, BN, BK, S, WGM, WGN)
+#define LIN_KERNELS(D, table)                                                                              \
+    LinKernels {                                                                                           \
+        table, (int)(sizeof(table) / sizeof(table[0])), &lin_launch_join<D, false>, &lin_launch_join<D, true>, \
+            &lin_launch_slope<D>, &lin_launch_colsum<D>                                                    \
+    }
+
+// Per-dtype kernels, each in its own translation unit.
+LinKernels linear_kernels_f32();
+LinKernels linear_kernels_f16();
+LinKernels linear_kernels_bf16();
+
+}  // namespace pgemm
