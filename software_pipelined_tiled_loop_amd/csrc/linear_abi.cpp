@@ -64,32 +64,52 @@ struct Plan {
     int np4;
 };
 
+// Estimated microseconds of a product on tiles of variant v with its K tiles
+// split in `splits`: the workgroups run in rounds, one 256 x 256 tile or up to
+// two 128 x 128 tiles per CU at a time, at measured rates of the whole part.
+double est_us(const LinVariant& v, const Shape& p, int dtype, int64_t splits) {
+    const bool f32 = dtype == PGEMM_F32, large = v.bm == 256;
+    // FLOP/us of one CU: alone with one workgroup, and shared by two
+    const double alone = (large ? (f32 ? 148e6 : 1340e6) : (f32 ? 90e6 : 600e6)) / kNumCU;
+    const double shared = large ? alone : (f32 ? 140e6 : 950e6) / kNumCU;
+    const int64_t wgs = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs * splits;
+    const double kt = (double)ceil_div(ceil_div(p.K, v.bk) * p.halves, splits);
+    const double flop = 2.0 * v.bm * v.bn * v.bk * kt * (p.gated ? 2 : 1);
+    const int64_t slots = large ? kNumCU : 2 * kNumCU;
+    const int64_t rounds = wgs / slots, rest = wgs % slots;
+    const double round_us = (large ? 1 : 2) * flop / shared, fixed = large ? 6.0 : 4.0;
+    double us = rounds * (round_us + fixed);
+    if (rest > kNumCU) us += round_us + fixed;
+    else if (rest > 0) us += flop / alone + fixed;
+    // the join: a launch, and the partial sums written and read
+    if (splits > 1) us += 4.0 + 2.0 * splits * p.rows * p.cols * (p.gated ? 2 : p.outs) * 4.0 / 4e6;
+    return us;
+}
+
 // The tile and the splits of a product, from its sizes and type alone (so the
 // workspace functions and the calls agree).
 Plan plan_product(const Shape& p, int dtype) {
     const LinKernels k = kernels_for(dtype);
     Plan best{};
+    double best_us = 0.0;
     for (int i = 0; i < k.n; ++i) {
         const LinVariant& v = k.v[i];
         if (v.lay != p.lay || v.gated != p.gated) continue;
-        best.v = &v;
-        break;
+        const int64_t kt = ceil_div(p.K, v.bk) * p.halves;
+        const int64_t tiles = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs;
+        for (int64_t s = 1; s <= 32 && (s == 1 || (s * 4 <= kt && tiles * s <= 2 * kNumCU)); ++s) {
+            const double us = est_us(v, p, dtype, s);
+            if (best.v && us >= best_us) continue;
+            best_us = us;
+            best.v = &v;
+            best.splits = s;
+        }
     }
     const LinVariant& v = *best.v;
     best.tiles_m = ceil_div(p.rows, v.bm);
     best.tiles_n = ceil_div(p.cols, v.bn);
-    const int64_t tiles = best.tiles_m * best.tiles_n * p.outs;
-    const int64_t kt = ceil_div(p.K, v.bk) * p.halves;
-    int64_t s = 1;
-    if (tiles > 0 && tiles < kNumCU) {
-        s = kNumCU / tiles;
-        if (s > kt / 4) s = kt / 4;
-        if (s > 32) s = 32;
-        if (s < 1) s = 1;
-    }
-    best.splits = s;
     best.np4 = (int)round_up(p.cols, 4);
-    best.part_bytes = s > 1 ? s * (p.gated ? 2 : p.outs) * p.rows * best.np4 * 4 : 0;
+    best.part_bytes = best.splits > 1 ? best.splits * (p.gated ? 2 : p.outs) * p.rows * best.np4 * 4 : 0;
     return best;
 }
 

@@ -179,8 +179,12 @@ static void classes(Cs... cs) {
 }
 
 int main() {
+    classes(LIN_CLASS(DT_BF16, 256, 256, 64, 2, 2, 4));
+    classes(LIN_CLASS(DT_F32, 256, 256, 32, 2, 2, 4));
     classes(LIN_CLASS(DT_BF16, 128, 128, 64, 2, 2, 2));
     classes(LIN_CLASS(DT_F32, 128, 128, 32, 2, 2, 2));
+    check_bounds_all<DT_BF16, 256, 64>();
+    check_bounds_all<DT_F32, 256, 32>();
     check_bounds_all<DT_BF16, 128, 64>();
     check_bounds_all<DT_BF16, 64, 64>();
     check_bounds_all<DT_F32, 128, 32>();

@@ -227,6 +227,50 @@ def test_nan_and_infinity_stay_in_their_rows_and_columns(pg, dtype):
         assert torch.equal(torch.isnan(y)[~skip], torch.isnan(want)[~skip]), act
 
 
+@pytest.fixture
+def on_gpu(monkeypatch):
+    """The 64-bit form evaluated on the GPU (float64 products), for the large sizes."""
+    monkeypatch.setattr(ref, "WHERE", "cuda")
+
+
+#        M     N     K
+LARGE = [(2500, 2310, 200), (4096, 2048, 96), (3001, 2999, 65), (1100, 8200, 130)]
+
+
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("i", range(len(LARGE)))
+def test_large_tiles(pg, on_gpu, dtype, order, i):
+    """Sizes that fill the GPU, where the planner takes the large tile, in every layout."""
+    M, N, K = LARGE[i]
+    say("large", dtype, order, (M, N, K))
+    t, act = TYPES[dtype], ref.ACTS[1 + i]
+    m = Maker(500 + i, t, (0, 1, 8, 0)[i], (0, 1, 0, 3)[i])
+    X, W, Wu = m.rows(M, K), m.weight(K, N, order), m.weight(K, N, order)
+    b, R = m.vector(N), m.rows(M, N)
+    Y, Z = m.out(M, N), m.out(M, N)
+    pg.linear(X, W, Y, bias=b, residual=R, act=act, Z=Z)
+    y, z = ref.linear(X, W, b, R, act, t)
+    ref.check("Y", Y, y)
+    ref.check("Z", Z, z)
+    H, G, U = m.out(M, N), m.out(M, N), m.out(M, N)
+    pg.gated(X, W, Wu, H, act=act, G=G, U=U)
+    for name, got, want in zip("HGU", (H, G, U), ref.gated(X, W, Wu, None, None, act, t)):
+        ref.check(name, got, want)
+    # the gradients contract over N and over M; dW is K x N
+    dX, dW, dWu = m.out(M, K), m.weight_out(K, N, order), m.weight_out(K, N, order)
+    pg.gated_backward(R, X, W, Wu, G, U, act=act, dX=dX, dWg=dW, dWu=dWu)
+    for name, got, want in zip(("dX", "dWg", "dWu"), (dX, dW, dWu), ref.gated_backward(R, X, W, Wu, G, U, act, t)):
+        ref.check(name, got, want)
+    # dX of many columns and dW of many rows: the other roles of the large tile
+    X2, W2, dY = m.rows(K, N), m.weight(N, M, order), m.rows(K, M)
+    dX2, dW2, db = m.out(K, N), m.weight_out(N, M, order), m.vector_out(M)
+    pg.linear_backward(dY, X2, W2, dX=dX2, dW=dW2, dbias=db)
+    for name, got, want in zip(("dX", "dW", "db"), (dX2, dW2, db), ref.linear_backward(dY, X2, W2, None, "none", t)):
+        ref.check(name, got, want)
+    m.check_frames()
+
+
 def d64(t):
     return t.detach().cpu().double()
 
