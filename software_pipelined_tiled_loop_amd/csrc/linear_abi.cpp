@@ -61,7 +61,7 @@ struct Shape {
 struct Plan {
     const LinVariant* v;
     int64_t tiles_m, tiles_n, splits, part_bytes;
-    int np4;
+    int np8;
 };
 
 // Estimated microseconds of a product on tiles of variant v with its K tiles
@@ -108,8 +108,8 @@ Plan plan_product(const Shape& p, int dtype) {
     const LinVariant& v = *best.v;
     best.tiles_m = ceil_div(p.rows, v.bm);
     best.tiles_n = ceil_div(p.cols, v.bn);
-    best.np4 = (int)round_up(p.cols, 4);
-    best.part_bytes = best.splits > 1 ? best.splits * (p.gated ? 2 : p.outs) * p.rows * best.np4 * 4 : 0;
+    best.np8 = (int)round_up(p.cols, 8);
+    best.part_bytes = best.splits > 1 ? best.splits * (p.gated ? 2 : p.outs) * p.rows * best.np8 * 4 : 0;
     return best;
 }
 
@@ -137,7 +137,7 @@ int run_product(const Shape& p, LinArgs& a, int dtype, void* part, hipStream_t s
     a.group_m = 4;
     a.splits = (int)pl.splits;
     a.part = pl.splits > 1 ? (float*)part : nullptr;
-    a.np4 = pl.np4;
+    a.np8 = pl.np8;
     a.e.M = (int)p.rows;
     a.e.N = (int)p.cols;
     a.nfull = v.ring_tiles(p.K, p.rows, a.lda, p.cols, a.ldb);
@@ -145,7 +145,7 @@ int run_product(const Shape& p, LinArgs& a, int dtype, void* part, hipStream_t s
     hipError_t e = v.launch(a, (int)grid, stream);
     if (e != hipSuccess) return hip_failed("linear_kernel", e);
     if (pl.splits > 1) {
-        const int64_t g2 = ceil_div(pl.np4, 1024) * p.rows * p.outs;
+        const int64_t g2 = ceil_div(p.cols, kJoinCols) * p.rows * p.outs;
         e = (p.gated ? k.join_gated : k.join)(a, (int)g2, stream);
         if (e != hipSuccess) return hip_failed("linear_join", e);
     }
@@ -154,7 +154,7 @@ int run_product(const Shape& p, LinArgs& a, int dtype, void* part, hipStream_t s
 
 bool in_range(int64_t M, int64_t N, int64_t K) { return M <= kMaxDim && N <= kMaxDim && K <= kMaxDim; }
 // Work items of the largest grids (tiles, rows x strips) fit an int.
-bool grids_fit(int64_t a, int64_t b) { return ceil_div(a, 64) * ceil_div(b, 64) < 0x3fffff00 && a * ceil_div(b, 1024) < 0x3fffff00; }
+bool grids_fit(int64_t a, int64_t b) { return ceil_div(a, 64) * ceil_div(b, 64) < 0x3fffff00 && a * ceil_div(b, kJoinCols) < 0x3fffff00; }
 
 int check_sizes(int64_t M, int64_t N, int64_t K, int dtype) {
     if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
@@ -200,16 +200,16 @@ int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
 // Workspace of a backward pass: gradients at the pre-activations, the row
 // blocks' column sums, the splits' sums (of dX, then of dW).
 struct Backward {
-    int64_t ldd, np4, blocks, dz_bytes, sum_bytes, split_bytes;
+    int64_t ldd, np8, blocks, dz_bytes, sum_bytes, split_bytes;
     int64_t total(int planes, bool keeps) const { return (keeps ? planes * dz_bytes : 0) + sum_bytes + split_bytes; }
 };
 Backward backward_layout(int64_t M, int64_t N, int64_t K, int dtype, int planes) {
     Backward b;
     b.ldd = round_up(N, 64);
-    b.np4 = round_up(N, 4);
+    b.np8 = round_up(N, 8);
     b.blocks = ceil_div(M, kSlopeRows);
     b.dz_bytes = M * b.ldd * elem_size(dtype);  // a multiple of 128
-    b.sum_bytes = round_up(b.blocks * planes * b.np4 * 4, 256);
+    b.sum_bytes = round_up(b.blocks * planes * b.np8 * 4, 256);
     b.split_bytes = 0;
     for (int order = 0; order < 2; ++order) {
         b.split_bytes = larger(b.split_bytes, part_bytes(dx_shape(M, N, K, order, planes), dtype));
@@ -252,7 +252,7 @@ int run_backward(int64_t M, int64_t N, int64_t K, const Grad& q, int w_order, in
         s.dU = gated && products ? dz[1] : nullptr;
         s.ldd = b.ldd;
         s.sums = bias ? sums : nullptr;
-        s.np4 = (int)b.np4;
+        s.np8 = (int)b.np8;
         s.M = (int)M;
         s.N = (int)N;
         s.act = act_args(act);
@@ -267,7 +267,7 @@ int run_backward(int64_t M, int64_t N, int64_t K, const Grad& q, int w_order, in
         s.out[1] = q.db[1];
         s.blocks = (int)b.blocks;
         s.planes = planes;
-        s.np4 = (int)b.np4;
+        s.np8 = (int)b.np8;
         s.N = (int)N;
         s.out_f32 = grad_dtype == PGEMM_F32;
         const hipError_t e = k.colsum(s, (int)ceil_div(N, 64), stream);

@@ -23,8 +23,7 @@
 //
 // The MFMAs are issued with the operands exchanged (B fragment first): the
 // result block then holds, in each lane, four consecutive columns n of one
-// row m, so bias, residual and outputs move as 8-byte (16-bit types) or
-// 16-byte (fp32) vectors instead of single elements.
+// row m, one 16-byte piece of the output tile that the epilogue lays out in LDS.
 //
 // K loop: a ring of S LDS stages with one barrier per K tile, as in
 // pgemm_kernel.hpp.  Only whole K tiles of the contraction go through the
@@ -84,8 +83,8 @@ struct LinArgs {
     int outs;             // outputs side by side (1, or 2 for the gated dW)
     int tiles_m, tiles_n, group_m;
     int splits;           // workgroups that share one output tile's K tiles
-    float* part;          // fp32 sums of each split: [split][plane][M][np4] (planes: outs, or 2 for gated)
-    int np4;
+    float* part;          // fp32 sums of each split: [split][plane][M][np8] (planes: outs, or 2 for gated)
+    int np8;
     EpiArgs e;
 };
 
@@ -211,69 +210,69 @@ __device__ __forceinline__ void mfma_swapped(f32x4& acc, const i32x4& a, const i
     }
 }
 
-// ---- values: four consecutive columns of a row ---------------------------------------------
+// ---- values: eight consecutive columns of a row ----------------------------------------------
 
 template <int D> struct Elem { typedef __bf16 type; };
 template <> struct Elem<DT_F16> { typedef _Float16 type; };
 template <> struct Elem<DT_F32> { typedef float type; };
 
-typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
-typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
-template <class T> struct Vec4 { typedef f32x4 type; };
-template <> struct Vec4<__bf16> { typedef bf16x4 type; };
-template <> struct Vec4<_Float16> { typedef f16x4 type; };
+typedef __attribute__((ext_vector_type(8))) float f32x8;
+template <class T> struct Vec8 { typedef f32x8 type; };
+template <> struct Vec8<__bf16> { typedef bf16x8 type; };
+template <> struct Vec8<_Float16> { typedef f16x8 type; };
 
-// Four elements at byte offset `off`, the first `valid` of them inside the
-// matrix (zeros for the others).  `cut` (uniform): some group of this launch
-// has 0 < valid < 4.
+__device__ __forceinline__ f32x8 zero8() { return f32x8{0, 0, 0, 0, 0, 0, 0, 0}; }
+__device__ __forceinline__ f32x8 join8(f32x4 a, f32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
 template <class T>
-__device__ __forceinline__ f32x4 load4(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid, bool cut) {
-    const uint32_t o = valid >= 4 ? off : OOB;
-    f32x4 v;
+__device__ __forceinline__ f32x8 load8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     if constexpr (sizeof(T) == 4) {
-        v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+        return join8(__builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0)),
+                     __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16, 0, 0)));
     } else {
-        const i32x2 w = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0));
-        const typename Vec4<T>::type h = __builtin_bit_cast(typename Vec4<T>::type, w);
+        const typename Vec8<T>::type h =
+            __builtin_bit_cast(typename Vec8<T>::type, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+        f32x8 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
+        for (int e = 0; e < 8; ++e) v[e] = (float)h[e];
+        return v;
     }
-    if (cut && valid > 0 && valid < 4) {
+}
+// Stores round to the output's type, to nearest even, once.  The uniform part
+// of the offset is added in the lanes, not passed as the instruction's scalar
+// offset: with one the compiler lets the very next instruction overwrite the
+// registers of a 16-byte store, and here that changed what was stored (first
+// dword of a group, seen in the kept pre-activations of a large tile).
+template <class T>
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x8 v) {
+    if constexpr (sizeof(T) == 4) {
+        const f32x4 a = __builtin_shufflevector(v, v, 0, 1, 2, 3), b = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, a), r, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, b), r, at + 16, 0, 0);
+    } else {
+        typename Vec8<T>::type h;
 #pragma unroll
-        for (int e = 0; e < 3; ++e) {
-            const uint32_t oe = e < valid ? off + (uint32_t)(e * sizeof(T)) : OOB;
-            if constexpr (sizeof(T) == 4) {
-                v[e] = __builtin_bit_cast(float, (int)__builtin_amdgcn_raw_buffer_load_b32(r, oe, 0, 0));
-            } else {
-                v[e] = (float)__builtin_bit_cast(T, (short)__builtin_amdgcn_raw_buffer_load_b16(r, oe, 0, 0));
-            }
-        }
+        for (int e = 0; e < 8; ++e) h[e] = (T)v[e];
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, h), r, at, 0, 0);
     }
-    return v;
+}
+template <class T>
+__device__ __forceinline__ float load1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    if constexpr (sizeof(T) == 4)
+        return __builtin_bit_cast(float, (int)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    else
+        return (float)__builtin_bit_cast(T, (short)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+}
+template <class T>
+__device__ __forceinline__ void store1(__amdgpu_buffer_rsrc_t r, uint32_t off, float v) {
+    if constexpr (sizeof(T) == 4)
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v), r, off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (T)v), r, off, 0, 0);
 }
 
-// Stores round to the output's type, to nearest even, once.
-template <class T>
-__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid, bool cut, f32x4 v) {
-    const uint32_t o = valid >= 4 ? off : OOB;
-    typename Vec4<T>::type h;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = (T)v[e];
-    if constexpr (sizeof(T) == 4)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, h), r, o, 0, 0);
-    else
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2, h), r, o, 0, 0);
-    if (cut && valid > 0 && valid < 4) {
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-            const uint32_t oe = e < valid ? off + (uint32_t)(e * sizeof(T)) : OOB;
-            if constexpr (sizeof(T) == 4)
-                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, (float)h[e]), r, oe, 0, 0);
-            else
-                __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (T)h[e]), r, oe, 0, 0);
-        }
-    }
-}
+// Whether some group of eight columns is cut by the output's edge.
+__device__ __forceinline__ bool cols_cut(int n) { return (n & 7) != 0; }
 
 // -log2(e) * P(t), so that sigmoid(x P) = 1 / (1 + exp2(x c(t))).
 template <int DEG>
@@ -285,27 +284,40 @@ __device__ __forceinline__ float act_poly(const ActArgs& a, float t) {
 }
 
 template <int DEG>
-__device__ __forceinline__ f32x4 act_smooth4(const ActArgs& a, f32x4 x) {
-    f32x4 y;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float p = DEG == 0 ? a.c[0] : act_poly<DEG>(a, DEG == 6 ? fminf(x[e] * x[e], kGeluCap) : x[e] * x[e]);
-        y[e] = x[e] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[e] * p));
-    }
-    return y;
+__device__ __forceinline__ float act_smooth(const ActArgs& a, float x) {
+    const float p = DEG == 0 ? a.c[0] : act_poly<DEG>(a, DEG == 6 ? fminf(x * x, kGeluCap) : x * x);
+    return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * p));
 }
 
-__device__ __forceinline__ f32x4 act4(const ActArgs& a, f32x4 x) {
-    f32x4 y;
-    switch (a.kind) {
-        case ACTK_NONE: return x;
-        case ACTK_RELU:
+template <int KIND>
+__device__ __forceinline__ float act1(const ActArgs& a, float x) {
+    if constexpr (KIND == ACTK_NONE) return x;
+    else if constexpr (KIND == ACTK_RELU) return x < 0.0f ? 0.0f : x;  // NaN stays NaN
+    else if constexpr (KIND == ACTK_SILU) return act_smooth<0>(a, x);
+    else if constexpr (KIND == ACTK_GELU_TANH) return act_smooth<1>(a, x);
+    else return act_smooth<6>(a, x);
+}
+template <int KIND>
+__device__ __forceinline__ f32x8 act8(const ActArgs& a, f32x8 x) {
+    if constexpr (KIND != ACTK_NONE) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = x[e] < 0.0f ? 0.0f : x[e];  // NaN stays NaN
-            return y;
-        case ACTK_SILU: return act_smooth4<0>(a, x);
-        case ACTK_GELU_TANH: return act_smooth4<1>(a, x);
-        default: return act_smooth4<6>(a, x);
+        for (int e = 0; e < 8; ++e) x[e] = act1<KIND>(a, x[e]);
+    }
+    return x;
+}
+// Calls f with the activation as a constant: one branch, not one a group.
+template <int K>
+struct KindC {
+    static constexpr int value = K;
+};
+template <class F>
+__device__ __forceinline__ void with_act(int kind, F&& f) {
+    switch (kind) {
+        case ACTK_NONE: f(KindC<ACTK_NONE>{}); break;
+        case ACTK_RELU: f(KindC<ACTK_RELU>{}); break;
+        case ACTK_SILU: f(KindC<ACTK_SILU>{}); break;
+        case ACTK_GELU_TANH: f(KindC<ACTK_GELU_TANH>{}); break;
+        default: f(KindC<ACTK_GELU>{}); break;
     }
 }
 
@@ -327,64 +339,126 @@ __device__ __forceinline__ void act_slope(const ActArgs& a, float x, float& y, f
         d = fmaf(y * s, e * p, p);
     }
 }
-__device__ __forceinline__ void act_slope4(const ActArgs& a, f32x4 x, f32x4& y, f32x4& d) {
+template <int KIND>
+__device__ __forceinline__ void act_slope8(const ActArgs& a, f32x8 x, f32x8& y, f32x8& d) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float yi, di;
-        switch (a.kind) {
-            case ACTK_NONE: yi = x[i]; di = 1.0f; break;
-            case ACTK_RELU: yi = x[i] < 0.0f ? 0.0f : x[i]; di = x[i] > 0.0f ? 1.0f : 0.0f; break;
-            case ACTK_SILU: act_slope<0>(a, x[i], yi, di); break;
-            case ACTK_GELU_TANH: act_slope<1>(a, x[i], yi, di); break;
-            default: act_slope<6>(a, x[i], yi, di); break;
+    for (int i = 0; i < 8; ++i) {
+        float yi = x[i], di = 1.0f;
+        if constexpr (KIND == ACTK_RELU) {
+            yi = x[i] < 0.0f ? 0.0f : x[i];
+            di = x[i] > 0.0f ? 1.0f : 0.0f;
+        } else if constexpr (KIND != ACTK_NONE) {
+            act_slope<KIND == ACTK_SILU ? 0 : KIND == ACTK_GELU_TANH ? 1 : 6>(a, x[i], yi, di);
         }
         y[i] = yi;
         d[i] = di;
     }
 }
 
-// The fused epilogue of one tile: rows and columns relative to (m0, n0).
+// The fused epilogue of one tile, eight columns of a row at a time (16-byte
+// accesses of 16-bit types).  Rows and columns are relative to (m0, n0); a lane
+// holds the offsets of its first group (row, col) and moves from there by rows
+// that are the same for all lanes.  A group that the edge of the output cuts
+// goes element by element.
 template <int D, bool GATED>
 struct Epi {
     typedef typename Elem<D>::type T;
+    static constexpr uint32_t TS = sizeof(T);
+    const EpiArgs& e;
     __amdgpu_buffer_rsrc_t y, r, z, u;
-    int rows, cols;
-    bool cut;
+    int n0, row, col, rows, cols;
+    uint32_t ys, oy, orr, oz, ou;  // bytes of an element of Y; the lane's offsets
 
-    __device__ __forceinline__ Epi(const EpiArgs& e, int m0, int n0, int out) {
-        const int64_t ys = e.out_f32 ? 4 : sizeof(T);
-        y = make_rsrc((char*)(out ? e.Y[1] : e.Y[0]) + (m0 * e.ldy + n0) * ys);
-        r = make_rsrc(e.R ? (const char*)e.R + (m0 * e.ldr + n0) * ys : nullptr);
-        z = make_rsrc(e.Z ? (char*)e.Z + (m0 * e.ldz + n0) * (int64_t)sizeof(T) : nullptr);
-        u = make_rsrc(e.U ? (char*)e.U + (m0 * e.ldu + n0) * (int64_t)sizeof(T) : nullptr);
+    __device__ __forceinline__ Epi(const EpiArgs& a, int m0, int n0_, int out, int row_, int col_)
+        : e(a), n0(n0_), row(row_), col(col_) {
+        ys = sizeof(T) == 4 || e.out_f32 ? 4u : TS;
+        y = make_rsrc((char*)(out ? e.Y[1] : e.Y[0]) + (m0 * e.ldy + n0) * (int64_t)ys);
+        r = make_rsrc(e.R ? (const char*)e.R + (m0 * e.ldr + n0) * (int64_t)ys : nullptr);
+        z = make_rsrc(e.Z ? (char*)e.Z + (m0 * e.ldz + n0) * (int64_t)TS : nullptr);
+        u = make_rsrc(e.U ? (char*)e.U + (m0 * e.ldu + n0) * (int64_t)TS : nullptr);
         rows = e.M - m0;
         cols = e.N - n0;
-        cut = (e.N & 3) != 0;
+        oy = (uint32_t)(row * (int)e.ldy + col) * ys;
+        orr = (uint32_t)(row * (int)e.ldr + col) * ys;
+        oz = (uint32_t)(row * (int)e.ldz + col) * TS;
+        ou = (uint32_t)(row * (int)e.ldu + col) * TS;
     }
-    __device__ __forceinline__ int valid(int row, int col) const { return row < rows ? cols - col : 0; }
-    // Bias of columns col .. col+3 (col relative to n0).
-    static __device__ __forceinline__ f32x4 bias(const EpiArgs& e, int which, int n0, int col) {
-        if (!e.bias[which]) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        return load4<T>(make_rsrc((const T*)e.bias[which] + n0), (uint32_t)(col * sizeof(T)), e.N - n0 - col,
-                        (e.N & 3) != 0);
+    // Columns of the group `by` rows on inside the output (8 or more: all).
+    __device__ __forceinline__ int valid(int by) const { return row + by < rows ? cols - col : 0; }
+    __device__ __forceinline__ bool same() const { return ys == TS; }  // Y has the operand type
+    __device__ __forceinline__ f32x8 bias(int which) const {
+        if (!e.bias[which] || cols - col < 8) return zero8();
+        return load8<T>(make_rsrc((const T*)e.bias[which] + n0), (uint32_t)col * TS);
     }
-    __device__ __forceinline__ void put(const EpiArgs& e, int row, int col, f32x4 v, f32x4 w, const f32x4& b0,
-                                        const f32x4& b1) const {
-        const int ok = valid(row, col);
-        v += b0;
-        if (e.Z) store4<T>(z, (uint32_t)(row * (int)e.ldz + col) * sizeof(T), ok, cut, v);
-        v = act4(e.act, v);
+    // Whether the group `by` rows on is whole; its offset, or one out of range,
+    // where loads give zeros and stores do nothing: no branch, so the groups of
+    // a batch are scheduled together.
+    __device__ __forceinline__ bool whole(int by) const { return row + by < rows && cols - col >= 8; }
+    static __device__ __forceinline__ uint32_t at(bool ok, uint32_t o) { return ok ? o : OOB; }
+    // The residual of a group as it lies in memory, where Y has the operand type.
+    struct Raw {
+        i32x4 a[sizeof(T) / 2];
+    };
+    __device__ __forceinline__ Raw residual(int by) const {
+        const uint32_t o = at(whole(by), orr + (uint32_t)(by * (int)e.ldr) * TS);
+        Raw x;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            x.a[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o + 16 * i, 0, 0));
+        return x;
+    }
+    static __device__ __forceinline__ f32x8 value(const Raw& x) {
+        if constexpr (sizeof(T) == 4) {
+            return join8(__builtin_bit_cast(f32x4, x.a[0]), __builtin_bit_cast(f32x4, x.a[1]));
+        } else {
+            const typename Vec8<T>::type h = __builtin_bit_cast(typename Vec8<T>::type, x.a[0]);
+            f32x8 v;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
+            return v;
+        }
+    }
+    // A whole group: v (gated: and w) the product's sums, b0 and b1 the biases, res the residual.
+    template <int KIND>
+    __device__ __forceinline__ void put(int by, f32x8 v, f32x8 w, const f32x8& b0, const f32x8& b1,
+                                        const Raw& res) const {
+        const bool ok = whole(by);
+        if (e.bias[0]) v += b0;
+        if (e.Z) store8<T>(z, at(ok, oz + (uint32_t)(by * (int)e.ldz) * TS), v);
+        v = act8<KIND>(e.act, v);
         if constexpr (GATED) {
-            w += b1;
-            if (e.U) store4<T>(u, (uint32_t)(row * (int)e.ldu + col) * sizeof(T), ok, cut, w);
+            if (e.bias[1]) w += b1;
+            if (e.U) store8<T>(u, at(ok, ou + (uint32_t)(by * (int)e.ldu) * TS), w);
             v *= w;
         }
-        if (sizeof(T) == 4 || e.out_f32) {
-            if (e.R) v += load4<float>(r, (uint32_t)(row * (int)e.ldr + col) * 4u, ok, cut);
-            store4<float>(y, (uint32_t)(row * (int)e.ldy + col) * 4u, ok, cut, v);
+        const uint32_t o = at(ok, oy + (uint32_t)(by * (int)e.ldy) * ys);
+        if (same()) {
+            if (e.R) v += value(res);
+            store8<T>(y, o, v);
         } else {
-            if (e.R) v += load4<T>(r, (uint32_t)(row * (int)e.ldr + col) * sizeof(T), ok, cut);
-            store4<T>(y, (uint32_t)(row * (int)e.ldy + col) * sizeof(T), ok, cut, v);
+            if (e.R) v += load8<float>(r, at(ok, orr + (uint32_t)(by * (int)e.ldr) * ys));
+            store8<float>(y, o, v);
+        }
+    }
+    // Element x of a group.
+    template <int KIND>
+    __device__ __forceinline__ void put1(int by, int x, float v, float w) const {
+        const uint32_t bo = (uint32_t)(col + x) * TS, at = (uint32_t)x * ys;
+        if (e.bias[0]) v += load1<T>(make_rsrc((const T*)e.bias[0] + n0), bo);
+        if (e.Z) store1<T>(z, oz + (uint32_t)(by * (int)e.ldz + x) * TS, v);
+        v = act1<KIND>(e.act, v);
+        if constexpr (GATED) {
+            if (e.bias[1]) w += load1<T>(make_rsrc((const T*)e.bias[1] + n0), bo);
+            if (e.U) store1<T>(u, ou + (uint32_t)(by * (int)e.ldu + x) * TS, w);
+            v *= w;
+        }
+        const uint32_t ro = orr + (uint32_t)(by * (int)e.ldr) * ys + at, o = oy + (uint32_t)(by * (int)e.ldy) * ys + at;
+        if (same()) {
+            if (e.R) v += load1<T>(r, ro);
+            store1<T>(y, o, v);
+        } else {
+            if (e.R) v += load1<float>(r, ro);
+            store1<float>(y, o, v);
         }
     }
 };
@@ -402,6 +476,10 @@ struct LinCfg {
     typedef Opnd<D, LA_, BM, BK> OA;
     typedef Opnd<D, LB_, BNP, BK> OB;
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
+    // One wave per SIMD, its 128 x 128 accumulators in all 256 AGPRs.
+    static constexpr bool LONE = BM * BN / NW >= 128 * 128;
+    static constexpr int MINW = LONE ? 1 : 2;  // waves per SIMD
+    static_assert(!LONE || ES == 2, "the fp32 MFMAs of one block depend on each other");
     static constexpr int WM = BM / WGM, WNP = BNP / WGN;
     static constexpr int FM = WM / 16, FNP = WNP / 16, FN = FNP * NP;
     static constexpr int A_BYTES = OA::BYTES, B_BYTES = OB::BYTES * NP;
@@ -419,45 +497,71 @@ struct LinFrags {
     i32x4 b[C::FN];
 };
 
-// The wave's side of the producer: next K tile to load and this wave's
-// 1-KiB blocks of it.
+// The wave's side of the producer: descriptors of the next K tile of A and of
+// the wave's B panel, and this wave's 1-KiB blocks of it.
 template <class C>
 struct LinSrc {
-    const char* pa;        // next K tile of A and of the wave's B panel
-    const char* pb;
+    i32x4 ra, rb;
     const char* ha;        // first K tile of the second contraction half
     const char* hb;
     int64_t sa, sb;        // bytes from one K tile to the next
-    int next, nfull;       // K tile within its half, K tiles per half
+    int turn;              // K tiles until the second half begins
     int left;              // K tiles still to load
     uint32_t va[C::A_INSTR], vb[C::B_INSTR];  // each lane's offset from the K tile's origin
-    i32x4 ra, rb;
 
-    // The descriptors of the next K tile; slots past the last one get an
-    // empty range, so every lane reads zeros.
-    __device__ __forceinline__ void arm() {
-        ra = make_rsrc_sgpr(pa);
-        rb = make_rsrc_sgpr(pb);
-        ra[2] = rb[2] = left > 0 ? (int)0x80000000u : 0;
-        --left;
-        ++next;
-        const bool turn = next == nfull;
-        pa = turn ? ha : pa + sa;
-        pb = turn ? hb : pb + sb;
+    static __device__ __forceinline__ void move(i32x4& r, int64_t by) {
+        const uint64_t p = (((uint64_t)(uint32_t)r[1] << 32) | (uint32_t)r[0]) + (uint64_t)by;
+        r[0] = (int)(uint32_t)p;
+        r[1] = (int)(uint32_t)(p >> 32);  // the address stays below 2^48: the stride field stays zero
+    }
+    // On to the next K tile, in four short parts that a lone wave spreads
+    // between its MFMAs.  Slots past the last one get an empty range, so every
+    // lane reads zeros.
+    template <int PART>
+    __device__ __forceinline__ void advance() {
+        if constexpr (PART == 0) {
+            --left;
+            ra[2] = rb[2] = left > 0 ? (int)0x80000000u : 0;
+        } else if constexpr (PART == 1) {
+            move(ra, sa);
+        } else if constexpr (PART == 2) {
+            move(rb, sb);
+        } else if (--turn == 0) {
+            ra[0] = (int)(uint32_t)(uint64_t)ha;
+            ra[1] = (int)(uint32_t)((uint64_t)ha >> 32);
+            rb[0] = (int)(uint32_t)(uint64_t)hb;
+            rb[1] = (int)(uint32_t)((uint64_t)hb >> 32);
+        }
+    }
+    __device__ __forceinline__ void advance_all() {
+        advance<0>();
+        advance<1>();
+        advance<2>();
+        advance<3>();
+    }
+    // Block Q of the K tile, to LDS: its place (M0), and the load, which needs
+    // an instruction between them.
+    template <int Q>
+    __device__ __forceinline__ void place(uint32_t a_lds, uint32_t b_lds) const {
+        constexpr uint32_t off = (Q < C::A_INSTR ? Q : Q - C::A_INSTR) * 1024u;
+        asm volatile("s_add_u32 m0, %0, %1" : : "s"(Q < C::A_INSTR ? a_lds : b_lds), "n"(off) : "m0", "scc");
     }
     template <int Q>
-    __device__ __forceinline__ void piece(uint32_t sa_lds, uint32_t sb_lds) const {
-        if constexpr (Q < C::A_INSTR)
-            dma16(ra, va[Q], sa_lds + (uint32_t)Q * 1024u);
-        else
-            dma16(rb, vb[Q - C::A_INSTR], sb_lds + (uint32_t)(Q - C::A_INSTR) * 1024u);
+    __device__ __forceinline__ void load() const {
+        asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds"
+                     :
+                     : "v"(Q < C::A_INSTR ? va[Q < C::A_INSTR ? Q : 0] : vb[Q < C::A_INSTR ? 0 : Q - C::A_INSTR]),
+                       "s"(Q < C::A_INSTR ? ra : rb)
+                     : "memory");
     }
 };
 
 template <class C, int Q0, int Q1>
 __device__ __forceinline__ void lin_pieces(const LinSrc<C>& s, uint32_t a, uint32_t b) {
     if constexpr (Q0 < Q1) {
-        s.template piece<Q0>(a, b);
+        s.template place<Q0>(a, b);
+        asm volatile("s_nop 0");
+        s.template load<Q0>();
         lin_pieces<C, Q0 + 1, Q1>(s, a, b);
     }
 }
@@ -476,15 +580,58 @@ __device__ __forceinline__ void lin_read(const char PGEMM_LDS* stage, int ks, in
     }
 }
 
+// The MFMA of a lone wave, from inline asm with the accumulator held in AGPRs:
+// left to the compiler, some accumulators land in VGPRs and 17 to 109
+// registers spill.  The hazards the compiler cannot see are the caller's:
+// acc_settle() between any other access to the accumulators and these.
+template <int D>
+__device__ __forceinline__ void mfma_lone(f32x4& acc, const i32x4& a, const i32x4& b) {
+    if constexpr (D == DT_BF16)
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+    else
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+__device__ __forceinline__ void acc_settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// One K step of a lone wave.  Nothing else issues on its SIMD, so what stands
+// between two MFMAs has to fit the 16 clocks that the matrix core is busy with
+// the first: one instruction in each place.  With the sixteen LDS-DMA blocks'
+// three instructions in a row in every second place the core was busy 57 % of
+// the time.  Reads of the next fragments go to places 0, 3, 6 ..; with DMA, each
+// block's M0 and load to the places behind them; without, the producer's way
+// to the next K tile.
+template <class C, bool READS, bool DMA, int M = 0>
+__device__ __forceinline__ void lone_step(f32x4 (&acc)[C::FM][C::FN], const LinFrags<C>& use, LinFrags<C>& nxt,
+                                          const char PGEMM_LDS* rstage, int rks, LinSrc<C>& src, uint32_t sa,
+                                          uint32_t sb, int wm0, int wnp, int lane) {
+    constexpr int NMF = C::FM * C::FN, NR = C::FM + C::FN, Q = M / 3;
+    static_assert(C::LPS <= NMF / 3 && NR <= NMF / 3, "places");
+    if constexpr (M < NMF) {
+        mfma_lone<C::Dt>(acc[M / C::FN][M % C::FN], use.a[M / C::FN], use.b[M % C::FN]);
+        if constexpr (READS && M % 3 == 0 && Q < NR) lin_read<C>(rstage, rks, Q, wm0, wnp, lane, nxt);
+        if constexpr (DMA && M % 3 == 1 && Q < C::LPS) src.template place<Q>(sa, sb);
+        if constexpr (DMA && M % 3 == 2 && Q < C::LPS) src.template load<Q>();
+        if constexpr (!DMA && M % 3 == 1 && Q < 4) src.template advance<Q>();
+        __builtin_amdgcn_sched_barrier(0);
+        lone_step<C, READS, DMA, M + 1>(acc, use, nxt, rstage, rks, src, sa, sb, wm0, wnp, lane);
+    }
+}
+
 // The MFMAs of one K step in eight groups; after each, a share of the next
 // K tile's LDS-DMA blocks (DMA) and of the next step's fragment reads.
 template <class C, bool READS, bool DMA, int G = 0>
 __device__ __forceinline__ void lin_step(f32x4 (&acc)[C::FM][C::FN], const LinFrags<C>& use, LinFrags<C>& nxt,
-                                         const char PGEMM_LDS* rstage, int rks, const LinSrc<C>& src, uint32_t sa,
+                                         const char PGEMM_LDS* rstage, int rks, LinSrc<C>& src, uint32_t sa,
                                          uint32_t sb, int wm0, int wnp, int lane) {
     constexpr int NMF = C::FM * C::FN, NG = NMF < 8 ? NMF : 8, GS = NMF / NG;
     constexpr int NR = C::FM + C::FN, RPG = (NR + NG - 1) / NG, PPG = (C::LPS + NG - 1) / NG;
-    if constexpr (G < NG) {
+    if constexpr (C::LONE) {
+        lone_step<C, READS, DMA>(acc, use, nxt, rstage, rks, src, sa, sb, wm0, wnp, lane);
+    } else if constexpr (G < NG) {
 #pragma unroll
         for (int m = G * GS; m < (G + 1) * GS; ++m)
             mfma_swapped<C::Dt>(acc[m / C::FN][m % C::FN], use.a[m / C::FN], use.b[m % C::FN]);
@@ -506,8 +653,107 @@ __device__ __forceinline__ void lin_step(f32x4 (&acc)[C::FM][C::FN], const LinFr
 // Full wait of this wave's loads and LDS operations, then the barrier.
 __device__ __forceinline__ void drain_barrier() { wait_barrier<0>(); }
 
+// The epilogue goes through LDS: the accumulators' lanes hold four columns of
+// sixteen rows, and indexing them needs straight-line code, which for a whole
+// tile (128 groups a lane, several activations) is far larger than the
+// instruction cache and was fetched at 13 to 36 us a tile.  Each wave writes
+// its sums to its own part of the ring's memory (16-byte chunks, XOR-swizzled
+// by the row against bank conflicts), in as many passes as fit, and a short
+// loop reads them back eight columns a lane, a row's lanes side by side.
 template <class C>
-__global__ void __launch_bounds__(C::NT, 2) linear_kernel(LinArgs g) {
+struct LinOut {
+    static constexpr int WN = C::FN * 16, NCHK = WN / 4;    // sums of a row; in 16-byte chunks
+    static constexpr int AREA = C::LDS / C::NW;              // bytes of a wave
+    static constexpr int FIT = AREA / (WN * 4) / 16;         // 16-row blocks that fit
+    static constexpr int BLOCKS = FIT < C::FM ? FIT : C::FM;  // of a pass
+    static constexpr int PASSES = C::FM / BLOCKS;
+    static constexpr int LPR = C::WNP / 8;                   // lanes of a row
+    static constexpr int RPI = 64 / LPR;                     // rows at a time
+    static constexpr int STEPS = BLOCKS * 16 / RPI;
+    // Groups of a lane in flight (with the next batch's residual): what the
+    // registers beside the accumulators hold.
+    static constexpr int WANT = C::ES == 4 ? (C::GATED ? 1 : 2) : C::LONE && !C::GATED ? 8 : 4;
+    static constexpr int UNROLL = STEPS < WANT ? STEPS : WANT;
+    static_assert(PASSES * BLOCKS == C::FM && STEPS % UNROLL == 0 && (NCHK & (NCHK - 1)) == 0, "passes");
+    static PGEMM_HD int at(int row, int chunk) { return (row * NCHK + (chunk ^ (row & (NCHK - 1)))) * 16; }
+};
+
+template <class C>
+__device__ __forceinline__ void lin_epilogue(const EpiArgs& e, int m0, int n0, int out, char PGEMM_LDS* smem,
+                                             f32x4 (&acc)[C::FM][C::FN], int wave, int lane, int wm0, int wnp) {
+    typedef LinOut<C> O;
+    const int li = lane & 15, lg = lane >> 4, r0 = lane / O::LPR, c8 = lane % O::LPR;
+    const Epi<C::Dt, C::GATED> ep(e, m0, n0, out, wm0 + r0, wnp + 8 * c8);
+    char PGEMM_LDS* area = smem + wave * O::AREA;
+    const f32x8 b0 = ep.bias(0), b1 = C::GATED ? ep.bias(1) : b0;
+    // The residual of the next batch of groups is under way while one is
+    // computed, across the passes too: what a CU has in flight bounds how fast
+    // the tile's residual arrives.
+    typename Epi<C::Dt, C::GATED>::Raw next[O::UNROLL];
+    const auto fetch = [&](int by) {
+        if (!e.R || !ep.same()) return;
+#pragma unroll
+        for (int q = 0; q < O::UNROLL; ++q) next[q] = ep.residual(by + q * O::RPI);
+    };
+    fetch(0);
+    drain_barrier();  // the ring's memory is free
+#pragma unroll 1
+    for (int pass = 0; pass < O::PASSES; ++pass) {
+#pragma unroll
+        for (int p = 0; p < O::PASSES; ++p) {
+            if (p != pass) continue;
+#pragma unroll
+            for (int i = 0; i < O::BLOCKS; ++i)
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+                    *(f32x4 PGEMM_LDS*)(area + O::at(16 * i + li, 4 * j + lg)) = acc[p * O::BLOCKS + i][j];
+        }
+        asm volatile("" ::: "memory");  // a wave's LDS operations stay in order
+        const int down = pass * O::BLOCKS * 16;
+        with_act(e.act.kind, [&](auto kind) {
+            constexpr int KIND = decltype(kind)::value;
+#pragma unroll 1
+            for (int s = 0; s < O::STEPS; s += O::UNROLL) {
+                typename Epi<C::Dt, C::GATED>::Raw res[O::UNROLL];
+                f32x8 v[O::UNROLL], w[C::GATED ? O::UNROLL : 1];
+#pragma unroll
+                for (int q = 0; q < O::UNROLL; ++q) res[q] = next[q];
+                fetch(down + (s + O::UNROLL) * O::RPI);
+#pragma unroll
+                for (int q = 0; q < O::UNROLL; ++q) {
+                    const int row = r0 + (s + q) * O::RPI;
+                    const auto sums = [&](int c) {
+                        return join8(*(const f32x4 PGEMM_LDS*)(area + O::at(row, c)),
+                                     *(const f32x4 PGEMM_LDS*)(area + O::at(row, c + 1)));
+                    };
+                    v[q] = sums(2 * c8);
+                    if constexpr (C::GATED) w[q] = sums(C::WNP / 4 + 2 * c8);
+                }
+#pragma unroll
+                for (int q = 0; q < O::UNROLL; ++q)
+                    ep.template put<KIND>(down + (s + q) * O::RPI, v[q], w[C::GATED ? q : 0], b0, b1, res[q]);
+            }
+            if (cols_cut(e.N)) {
+#pragma unroll 1
+                for (int s = 0; s < O::STEPS; ++s) {
+                    const int n = ep.valid(down + s * O::RPI);
+#pragma unroll 1
+                    for (int x = 0; x < (n < 8 ? n : 0); ++x) {
+                        const auto one = [&](int c) {
+                            return *(const float PGEMM_LDS*)(area + O::at(r0 + s * O::RPI, c >> 2) + 4 * (c & 3));
+                        };
+                        ep.template put1<KIND>(down + s * O::RPI, x, one(8 * c8 + x),
+                                               C::GATED ? one(C::WNP + 8 * c8 + x) : 0.0f);
+                    }
+                }
+            }
+        });
+        asm volatile("" ::: "memory");
+    }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::NT, C::MINW) linear_kernel(LinArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS];
     char PGEMM_LDS* smem = (char PGEMM_LDS*)smem_raw;
     typedef typename C::OA OA;
@@ -520,11 +766,13 @@ __global__ void __launch_bounds__(C::NT, 2) linear_kernel(LinArgs g) {
     if (w.count == 0) return;
     int L = w.start + w.lb, split = 0;
     if (g.splits > 1) {
-        split = L / per_split;
+        split = __builtin_amdgcn_readfirstlane(L / per_split);
         L -= split * per_split;
     }
     int tm, tn;
     raster(L, g.tiles_m, tiles_n, g.group_m, tm, tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
     const int out = tn >= g.tiles_n ? 1 : 0;
     tn -= out * g.tiles_n;
     const int m0 = tm * C::BM, n0 = tn * C::BNP;
@@ -540,6 +788,7 @@ __global__ void __launch_bounds__(C::NT, 2) linear_kernel(LinArgs g) {
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (C::LONE) acc_settle();
 
     // This split's K tiles of the ring: [t0, t1) of both halves' nfull.
     const int64_t total = (int64_t)g.nfull * g.halves;
@@ -558,14 +807,13 @@ __global__ void __launch_bounds__(C::NT, 2) linear_kernel(LinArgs g) {
 
     if (t1 > t0) {
         LinSrc<C> src;
-        const int half = t0 >= g.nfull ? 1 : 0;
-        src.next = t0 - half * g.nfull;
-        src.nfull = half ? 0x7fffffff : g.nfull;
+        const int half = t0 >= g.nfull ? 1 : 0, first = t0 - half * g.nfull;
+        src.turn = half ? 0x7fffffff : g.nfull - first;
         src.left = t1 - t0;
         src.sa = OA::step(g.lda);
         src.sb = OB::step(g.ldb);
-        src.pa = a_half[half] + src.sa * src.next;
-        src.pb = b_half[half] + src.sb * src.next;
+        src.ra = make_rsrc_sgpr((half ? a_half[1] : a_half[0]) + src.sa * first);
+        src.rb = make_rsrc_sgpr((half ? b_half[1] : b_half[0]) + src.sb * first);
         src.ha = a_half[1];
         src.hb = b_half[1];
 #pragma unroll
@@ -585,11 +833,10 @@ __global__ void __launch_bounds__(C::NT, 2) linear_kernel(LinArgs g) {
         // Prologue: slots 0 .. S-2.
 #pragma unroll
         for (int p = 0; p < C::S - 1; ++p) {
-            src.arm();
             lin_pieces<C, 0, C::LPS>(src, lds0 + p * C::STAGE + a_base, lds0 + p * C::STAGE + b_base);
+            src.advance_all();
         }
         wait_barrier<C::LPS*(C::S - 2)>();
-        src.arm();
         lin_pieces<C, 0, C::LPS>(src, lds0 + (C::S - 1) * C::STAGE + a_base, lds0 + (C::S - 1) * C::STAGE + b_base);
         LinFrags<C> f[2];
 #pragma unroll
@@ -599,7 +846,7 @@ __global__ void __launch_bounds__(C::NT, 2) linear_kernel(LinArgs g) {
             const int nst = cur + 1 == C::S ? 0 : cur + 1;
             lin_step<C, true, false>(acc, f[0], f[1], smem + cur * C::STAGE, 1, src, 0, 0, wm0, wnp, lane);
             wait_barrier<C::LPS*(C::S - 2)>();  // K tile t+1 is in LDS, stage `cur` is free
-            src.arm();
+            if constexpr (!C::LONE) src.advance_all();
             const uint32_t freed = lds0 + cur * C::STAGE;
             lin_step<C, true, true>(acc, f[1], f[0], smem + nst * C::STAGE, 0, src, freed + a_base, freed + b_base,
                                     wm0, wnp, lane);
@@ -625,73 +872,76 @@ __global__ void __launch_bounds__(C::NT, 2) linear_kernel(LinArgs g) {
 #pragma unroll
                 for (int r = 0; r < C::FM + C::FN; ++r) lin_read<C>(smem, ks, r, wm0, wnp, lane, f);
 #pragma unroll
-                for (int m = 0; m < C::FM * C::FN; ++m)
-                    mfma_swapped<C::Dt>(acc[m / C::FN][m % C::FN], f.a[m / C::FN], f.b[m % C::FN]);
+                for (int m = 0; m < C::FM * C::FN; ++m) {
+                    if constexpr (C::LONE)
+                        mfma_lone<C::Dt>(acc[m / C::FN][m % C::FN], f.a[m / C::FN], f.b[m % C::FN]);
+                    else
+                        mfma_swapped<C::Dt>(acc[m / C::FN][m % C::FN], f.a[m / C::FN], f.b[m % C::FN]);
+                }
             }
         }
     }
+    if constexpr (C::LONE) acc_settle();
 
     const int li = lane & 15, lg4 = 4 * (lane >> 4);
     if (g.part) {
         // fp32 sums of this split, joined by linear_join in the order of the splits
         const int planes = C::GATED ? 2 : g.outs;
-        float* base = g.part + ((int64_t)split * planes + out) * g.e.M * g.np4;
+        float* base = g.part + ((int64_t)split * planes + out) * g.e.M * g.np8;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
             const int row = m0 + wm0 + 16 * i + li;
 #pragma unroll
             for (int j = 0; j < C::FN; ++j) {
                 const int col = n0 + wnp + 16 * (j % C::FNP) + lg4;
-                if (row < g.e.M && col < g.np4)
-                    *(f32x4*)(base + ((int64_t)(j / C::FNP) * g.e.M + row) * g.np4 + col) = acc[i][j];
+                if (row < g.e.M && col < g.np8)
+                    *(f32x4*)(base + ((int64_t)(j / C::FNP) * g.e.M + row) * g.np8 + col) = acc[i][j];
             }
         }
         return;
     }
-    const Epi<C::Dt, C::GATED> ep(g.e, m0, n0, out);
-    f32x4 b0[C::FNP], b1[C::FNP];
-#pragma unroll
-    for (int j = 0; j < C::FNP; ++j) {
-        b0[j] = Epi<C::Dt, C::GATED>::bias(g.e, 0, n0, wnp + 16 * j + lg4);
-        b1[j] = C::GATED ? Epi<C::Dt, C::GATED>::bias(g.e, 1, n0, wnp + 16 * j + lg4) : b0[j];
-    }
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-#pragma unroll
-        for (int j = 0; j < C::FNP; ++j)
-            ep.put(g.e, wm0 + 16 * i + li, wnp + 16 * j + lg4, acc[i][j], acc[i][C::GATED ? j + C::FNP : j], b0[j],
-                   b1[j]);
-        __builtin_amdgcn_sched_barrier(0);
-    }
+    lin_epilogue<C>(g.e, m0, n0, out, smem, acc, wave, lane, wm0, wnp);
 }
 
 // ---- join of the splits ---------------------------------------------------------------------------
 
-// One thread per four columns of a row: the splits' sums in the order of the
-// splits, then the epilogue.  A workgroup covers one row's stretch of 1024
-// columns.
+// One thread per eight columns of a row: the splits' sums in the order of the
+// splits, then the epilogue.  A workgroup covers one row's stretch of
+// kJoinCols columns.
+constexpr int kJoinCols = 512;
+
 template <int D, bool GATED>
-__global__ void __launch_bounds__(256) linear_join(LinArgs g) {
-    const int strips = (g.np4 + 1023) / 1024;
+__global__ void __launch_bounds__(kJoinCols / 8) linear_join(LinArgs g) {
+    const int strips = (g.e.N + kJoinCols - 1) / kJoinCols;
     int b = (int)blockIdx.x;
     const int strip = b % strips;
     b /= strips;
     const int m = b % g.e.M, out = b / g.e.M;
-    const int n0 = strip * 1024, col = 4 * (int)threadIdx.x;
-    if (n0 + col >= g.np4) return;
+    const int n0 = strip * kJoinCols, col = 8 * (int)threadIdx.x;
+    if (n0 + col >= g.e.N) return;
     const int planes = GATED ? 2 : g.outs;
-    const int64_t plane = (int64_t)g.e.M * g.np4;
-    const float* p = g.part + out * plane + (int64_t)m * g.np4 + n0 + col;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, w = v;
+    const int64_t plane = (int64_t)g.e.M * g.np8;
+    const float* p = g.part + out * plane + (int64_t)m * g.np8 + n0 + col;
+    const Epi<D, GATED> ep(g.e, m, n0, out, 0, col);
+    const f32x8 b0 = ep.bias(0), b1 = GATED ? ep.bias(1) : b0;
+    typename Epi<D, GATED>::Raw res{};
+    if (g.e.R && ep.same()) res = ep.residual(0);
+    f32x8 v = zero8(), w = v;
+#pragma unroll 4
     for (int s = 0; s < g.splits; ++s) {
-        v += *(const f32x4*)p;
-        if constexpr (GATED) w += *(const f32x4*)(p + plane);
+        v += *(const f32x8*)p;
+        if constexpr (GATED) w += *(const f32x8*)(p + plane);
         p += planes * plane;
     }
-    const Epi<D, GATED> ep(g.e, m, n0, out);
-    const f32x4 b0 = Epi<D, GATED>::bias(g.e, 0, n0, col);
-    const f32x4 b1 = GATED ? Epi<D, GATED>::bias(g.e, 1, n0, col) : b0;
-    ep.put(g.e, 0, col, v, w, b0, b1);
+    with_act(g.e.act.kind, [&](auto kind) {
+        constexpr int KIND = decltype(kind)::value;
+        ep.template put<KIND>(0, v, w, b0, b1, res);
+        if (!ep.whole(0)) {
+#pragma unroll
+            for (int x = 0; x < 7; ++x)
+                if (x < ep.valid(0)) ep.template put1<KIND>(0, x, v[x], w[x]);
+        }
+    });
 }
 
 // ---- gradients at the pre-activations -----------------------------------------------------------
@@ -708,56 +958,68 @@ struct SlopeArgs {
     void* dZ;           // gated: dG; null: column sums only
     void* dU;
     int64_t ldy, ldz, ldu, ldd;
-    float* sums;        // [row block][planes][np4] column sums; null: none
-    int np4;
+    float* sums;        // [row block][planes][np8] column sums; null: none
+    int np8;
     int M, N;
     ActArgs act;
 };
 
 constexpr int kSlopeRows = 64;   // rows per workgroup
-constexpr int kSlopeCols = 128;  // columns per workgroup: 32 threads of four columns
+constexpr int kSlopeCols = 256;  // columns per workgroup: 32 threads of eight columns
+
+// The first `valid` of eight elements at byte offset `off`, zeros for the rest.
+template <class T>
+__device__ __forceinline__ f32x8 load_cut8(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
+    if (valid >= 8) return load8<T>(r, off);
+    f32x8 v = zero8();
+#pragma unroll
+    for (int x = 0; x < 7; ++x)
+        if (x < valid) v[x] = load1<T>(r, off + (uint32_t)(x * sizeof(T)));
+    return v;
+}
 
 template <int D, bool GATED>
 __global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
     typedef typename Elem<D>::type T;
-    __shared__ f32x4 red[GATED ? 2 : 1][256];
+    __shared__ f32x8 red[GATED ? 2 : 1][256];
     const int strips = (g.N + kSlopeCols - 1) / kSlopeCols;
     const int strip = (int)blockIdx.x % strips, block = (int)blockIdx.x / strips;
     const int n0 = strip * kSlopeCols, m0 = block * kSlopeRows;
-    const int col = 4 * ((int)threadIdx.x & 31), r0 = (int)threadIdx.x >> 5;
+    const int col = 8 * ((int)threadIdx.x & 31), r0 = (int)threadIdx.x >> 5;
     const int rows = g.M - m0 < kSlopeRows ? g.M - m0 : kSlopeRows;
     const int valid = g.N - n0 - col;
-    const bool cut = (g.N & 3) != 0;
     const auto at = [&](const void* p, int64_t ld) {
         return make_rsrc(p ? (const char*)p + (m0 * ld + n0) * (int64_t)sizeof(T) : nullptr);
     };
     const __amdgpu_buffer_rsrc_t ry = at(g.dY, g.ldy), rz = at(g.Z, g.ldz), ru = at(g.U, g.ldu), rd = at(g.dZ, g.ldd),
                                  re = at(g.dU, g.ldd);
-    f32x4 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
-    for (int row = r0; row < rows; row += 8) {
-        const f32x4 dy = load4<T>(ry, (uint32_t)(row * (int)g.ldy + col) * sizeof(T), valid, cut);
-        f32x4 d = dy, e = s1;
-        if (GATED || g.act.kind != ACTK_NONE) {
-            const f32x4 z = load4<T>(rz, (uint32_t)(row * (int)g.ldz + col) * sizeof(T), valid, cut);
-            f32x4 y;
-            act_slope4(g.act, z, y, d);
-            d *= dy;
-            if constexpr (GATED) {
-                const f32x4 u = load4<T>(ru, (uint32_t)(row * (int)g.ldu + col) * sizeof(T), valid, cut);
-                d *= u;
-                e = dy * y;
+    f32x8 s0 = zero8(), s1 = s0;
+    if (valid > 0) {
+        with_act(g.act.kind, [&](auto kind) {
+            constexpr int KIND = decltype(kind)::value;
+            for (int row = r0; row < rows; row += 8) {
+                const f32x8 dy = load_cut8<T>(ry, (uint32_t)(row * (int)g.ldy + col) * sizeof(T), valid);
+                f32x8 d = dy, e = dy;
+                if constexpr (GATED || KIND != ACTK_NONE) {
+                    const f32x8 z = load_cut8<T>(rz, (uint32_t)(row * (int)g.ldz + col) * sizeof(T), valid);
+                    f32x8 y;
+                    act_slope8<KIND>(g.act, z, y, d);
+                    d *= dy;
+                    if constexpr (GATED) {
+                        const f32x8 u = load_cut8<T>(ru, (uint32_t)(row * (int)g.ldu + col) * sizeof(T), valid);
+                        d *= u;
+                        e = dy * y;
+                    }
+                }
+                s0 += d;
+                if constexpr (GATED) s1 += e;
+                if (g.dZ) {  // the workspace's rows are whole groups
+                    const uint32_t o = (uint32_t)(row * (int)g.ldd + col) * sizeof(T);
+                    store8<T>(rd, o, d);
+                    if constexpr (GATED) store8<T>(re, o, e);
+                }
             }
-        }
-        s0 += d;
-        if constexpr (GATED) s1 += e;
-        if (g.dZ) {
-            // the workspace rows are whole groups: no partial store, and no
-            // lane beyond the row
-            const uint32_t o = (uint32_t)(row * (int)g.ldd + col) * sizeof(T);
-            const int all = valid > 0 ? 4 : 0;
-            store4<T>(rd, o, all, false, d);
-            if constexpr (GATED) store4<T>(re, o, all, false, e);
-        }
+        });
     }
     if (!g.sums) return;
     // columns of the eight row groups, in their order
@@ -768,28 +1030,37 @@ __global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
     if (threadIdx.x < 32 && valid > 0) {
 #pragma unroll
         for (int p = 0; p < planes; ++p) {
-            f32x4 s = red[p][threadIdx.x];
+            f32x8 s = red[p][threadIdx.x];
             for (int k = 1; k < 8; ++k) s += red[p][threadIdx.x + 32 * k];
-            *(f32x4*)(g.sums + ((int64_t)block * planes + p) * g.np4 + n0 + col) = s;
+            *(f32x8*)(g.sums + ((int64_t)block * planes + p) * g.np8 + n0 + col) = s;
         }
     }
 }
 
-// Bias gradients: the row blocks' column sums, in their order.
+// Bias gradients: the row blocks' column sums, in a fixed order: sixteen
+// interleaved runs of blocks, then the runs.
 struct SumArgs {
-    const float* sums;  // [blocks][planes][np4]
+    const float* sums;  // [blocks][planes][np8]
     void* out[2];       // planes; null: none
-    int blocks, planes, np4, N;
+    int blocks, planes, np8, N;
     int out_f32;
 };
 
 template <int D>
-__global__ void __launch_bounds__(64) linear_colsum(SumArgs g) {
+__global__ void __launch_bounds__(1024) linear_colsum(SumArgs g) {
     typedef typename Elem<D>::type T;
-    const int n = (int)blockIdx.x * 64 + (int)threadIdx.x, p = (int)blockIdx.y;
-    if (n >= g.N || !g.out[p]) return;
+    __shared__ float red[16][64];
+    const int c = (int)threadIdx.x & 63, run = (int)threadIdx.x >> 6;
+    const int n = (int)blockIdx.x * 64 + c, p = (int)blockIdx.y;
     float s = 0.0f;
-    for (int b = 0; b < g.blocks; ++b) s += g.sums[((int64_t)b * g.planes + p) * g.np4 + n];
+    if (n < g.N && g.out[p]) {
+#pragma unroll 4
+        for (int b = run; b < g.blocks; b += 16) s += g.sums[((int64_t)b * g.planes + p) * g.np8 + n];
+    }
+    red[run][c] = s;
+    __syncthreads();
+    if (run != 0 || n >= g.N || !g.out[p]) return;
+    for (int k = 1; k < 16; ++k) s += red[k][c];
     if (g.out_f32)
         ((float*)g.out[p])[n] = s;
     else

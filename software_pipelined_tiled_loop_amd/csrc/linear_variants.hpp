@@ -45,7 +45,7 @@ int lin_ring_tiles(int64_t K, int64_t rows, int64_t lda, int64_t cols, int64_t l
 }
 template <int D, bool GATED>
 hipError_t lin_launch_join(const LinArgs& a, int grid, hipStream_t s) {
-    return lin_launch<LinArgs>(&linear_join<D, GATED>, a, dim3(grid), 256, s);
+    return lin_launch<LinArgs>(&linear_join<D, GATED>, a, dim3(grid), kJoinCols / 8, s);
 }
 template <int D>
 hipError_t lin_launch_slope(const SlopeArgs& a, bool gated, int grid, hipStream_t s) {
@@ -54,7 +54,7 @@ hipError_t lin_launch_slope(const SlopeArgs& a, bool gated, int grid, hipStream_
 }
 template <int D>
 hipError_t lin_launch_colsum(const SumArgs& a, int grid, hipStream_t s) {
-    return lin_launch<SumArgs>(&linear_colsum<D>, a, dim3(grid, a.planes), 64, s);
+    return lin_launch<SumArgs>(&linear_colsum<D>, a, dim3(grid, a.planes), 1024, s);
 }
 
 constexpr int lin_la(int lay) { return lay == LIN_XX ? LAY_X : LAY_K; }
