@@ -12,7 +12,6 @@ library has not been built: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -321,140 +320,161 @@ pgemm_gated_backward_workspace = _lib.pgemm_gated_backward_workspace
 
 
 class _Call:
-    """The checks that the four operators share.  Collects the tensors of one
-    call; `go` launches it on their GPU once every check has passed."""
+    """The checks that the four operators share, and their launch.
 
-    __slots__ = ("dtype", "device", "ins", "outs")
+    An operator's checks of types, shapes, strides and devices depend on
+    nothing else, so they run once for each combination of them: the operator
+    describes its call on an instance, which `_cached` then keeps.  What
+    depends on addresses (overlaps, the workspace) is checked at every call.
+    """
 
-    def __init__(self, X, name="X"):
+    __slots__ = ("dtype", "device", "index", "tensors", "pairs", "args", "need", "function")
+
+    def __init__(self, X):
         code = _FLOAT_CODE.get(X.dtype)
         if code is None:
-            raise ValueError("%s has unsupported dtype %s: float32, float16 or bfloat16 is needed" % (name, X.dtype))
+            raise ValueError("X has unsupported dtype %s: float32, float16 or bfloat16 is needed" % X.dtype)
         self.dtype = code
         self.device = X.device
-        self.ins, self.outs = [], []
+        self.index = X.device.index
+        self.tensors = []  # (name, tensor's place among the operator's, bytes from first to last, written)
 
-    def _place(self, name, t, dtypes, out):
+    def _place(self, name, slot, t, dtypes, out):
         if t.dtype not in dtypes:
             raise ValueError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
         if t.device != self.device:
             raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, self.device))
-        (self.outs if out else self.ins).append((name, t))
+        if t.numel():
+            last = sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
+            self.tensors.append((name, slot, (last + 1) * t.element_size(), out))
 
-    def rows(self, name, t, shape, dtypes, out=False):
-        """(address, leading dimension) of a row-major matrix with unit column stride."""
+    def rows(self, name, slot, t, shape, dtypes, out=False):
+        """Leading dimension of a row-major matrix with unit column stride."""
         if t is None:
-            return None, 0
+            return 0
         if t.dim() != 2 or tuple(t.shape) != shape:
             raise ValueError("%s is %s, the call needs %s" % (name, tuple(t.shape), shape))
-        self._place(name, t, dtypes, out)
+        self._place(name, slot, t, dtypes, out)
         r, c = shape
         s0, s1 = t.stride()
         if (s1 != 1 and c > 1) or (s0 < c and r > 1):
             raise ValueError("%s must be row-major with unit column stride, got strides %s" % (name, (s0, s1)))
-        return t.data_ptr(), (s0 if r > 1 else c) or 1
+        return (s0 if r > 1 else c) or 1
 
-    def weight(self, name, t, shape, dtypes, out=False):
-        """(address, leading dimension, order) of a K x N weight stored either way."""
+    def weight(self, name, slot, t, shape, dtypes, out=False):
+        """(leading dimension, order) of a K x N weight stored either way."""
         if t is None:
-            return None, 0, ORDER_KN
+            return 0, ORDER_KN
         if t.dim() != 2 or tuple(t.shape) != shape:
             raise ValueError("%s is %s, the call needs %s" % (name, tuple(t.shape), shape))
-        self._place(name, t, dtypes, out)
+        self._place(name, slot, t, dtypes, out)
         k, n = shape
         s0, s1 = t.stride()
         if (s1 == 1 or n <= 1) and (s0 >= n or k <= 1):
-            return t.data_ptr(), (s0 if k > 1 else n) or 1, ORDER_KN
+            return (s0 if k > 1 else n) or 1, ORDER_KN
         if (s0 == 1 or k <= 1) and (s1 >= k or n <= 1):
-            return t.data_ptr(), (s1 if n > 1 else k) or 1, ORDER_NK
+            return (s1 if n > 1 else k) or 1, ORDER_NK
         raise ValueError("%s must have unit stride along one axis and whole rows along the other, got strides %s"
                          % (name, (s0, s1)))
 
-    def vector(self, name, t, n, dtypes, out=False):
+    def weights(self, names, slots, ts, shape, dtypes, out=False):
+        """The same of two weights, which must agree."""
+        if (ts[0] is None) != (ts[1] is None):
+            raise ValueError("%s and %s must be given together" % names)
+        a, b = (self.weight(n, i, t, shape, dtypes, out) for n, i, t in zip(names, slots, ts))
+        if a != b:
+            raise ValueError("%s and %s must have the same strides, got %s and %s"
+                             % (names + tuple(tuple(t.stride()) for t in ts)))
+        return a
+
+    def vector(self, name, slot, t, n, dtypes, out=False):
         if t is None:
-            return None
+            return
         if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
             raise ValueError("%s must be a contiguous vector of %d, got %s" % (name, n, tuple(t.shape)))
-        self._place(name, t, dtypes, out)
-        return t.data_ptr()
+        self._place(name, slot, t, dtypes, out)
 
-    def check_overlap(self, same=None):
-        """No output may share memory with an input or another output; `same` is
-        an (input, output) pair that may be one and the same matrix."""
-        spans = []
-        for kind, group in ((0, self.ins), (1, self.outs)):
-            for name, t in group:
-                if t.numel():
-                    p = t.data_ptr()
-                    last = sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
-                    spans.append((p, p + (last + 1) * t.element_size(), kind, name, t))
-        spans.sort(key=_first)
-        top, i = 0, 0
-        for i, a in enumerate(spans):
-            if a[0] < top:
-                break
-            top = max(top, a[1])
-        else:
+    def done(self, function, need, args):
+        """`args(pointers)` gives the C function's arguments before the workspace."""
+        self.function, self.need, self.args = function, need, args
+        self.pairs = [(i, bi, j, bj) for x, (_, i, bi, oi) in enumerate(self.tensors)
+                      for _, j, bj, oj in self.tensors[x + 1:] if oi or oj]
+        return self
+
+    def _overlap(self, ts, i, j, same):
+        """Raises unless the matrices at places i and j share no byte (their ranges do)."""
+        x, y = ts[i], ts[j]
+        if same == (i, j) and x.data_ptr() == y.data_ptr() and x.stride() == y.stride():
             return
-        for i, a in enumerate(spans):
-            for b in spans[i + 1:]:
-                if b[0] >= a[1] or not (a[2] or b[2]):
-                    continue
-                x, y = a[4], b[4]
-                if same is not None and {id(x), id(y)} == {id(same[0]), id(same[1])}:
-                    if x.data_ptr() == y.data_ptr() and x.stride() == y.stride() and x.dtype == y.dtype:
-                        continue
-                if x.dim() == 2 and y.dim() == 2:  # stored rows: the axis of larger stride
-                    x, y = _stored_rows(x), _stored_rows(y)
-                    if not _regions_overlap(x, x.shape[0], x.shape[1], y, y.shape[0], y.shape[1]):
-                        continue
-                raise ValueError("%s and %s overlap: outputs must not share memory with inputs or each other"
-                                 % (a[3], b[3]))
+        if x.dim() == 2 and y.dim() == 2:
+            x, y = _stored_rows(x), _stored_rows(y)
+            if not _regions_overlap(x, x.shape[0], x.shape[1], y, y.shape[0], y.shape[1]):
+                return
+        names = {slot: name for name, slot, _, _ in self.tensors}
+        raise ValueError("%s and %s overlap: outputs must not share memory with inputs or each other"
+                         % (names[i], names[j]))
 
-    def go(self, need, workspace, stream, call):
-        """Runs call(workspace address, bytes, stream) on the tensors' GPU."""
-        import torch
+    def run(self, ts, workspace, stream, same=None):
+        """Launches on the tensors' GPU; `same`: places of an input and an output that may be one matrix."""
+        p = [None if t is None else t.data_ptr() for t in ts]
+        for i, bi, j, bj in self.pairs:
+            if p[i] < p[j] + bj and p[j] < p[i] + bi:
+                self._overlap(ts, i, j, same)
+        index = self.index
         if self.device.type != "cuda":
             raise ValueError("the tensors must be on a GPU, got %s" % self.device)
-        index = self.device.index
-        if index != torch.cuda.current_device():
-            with torch.cuda.device(index):
-                return self.go(need, workspace, stream, call)
+        need = self.need
         if need < 0:
             raise PgemmError(need)
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return self.run(ts, workspace, stream, same)
         if workspace is not None:
-            if workspace.device != self.device or not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor on %s" % self.device)
-            p = workspace.data_ptr()
-            n = workspace.numel() * workspace.element_size()
-            if n < need or p % 16:
-                raise ValueError("workspace must be 16-byte aligned and hold %d bytes, got %d" % (need, n))
-            if n:
-                for name, t in self.ins + self.outs:
-                    if t.numel():
-                        q = t.data_ptr()
-                        last = sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
-                        if q < p + n and p < q + (last + 1) * t.element_size():
-                            raise ValueError("workspace overlaps %s" % name)
+            w, n = self._given(p, workspace)
         elif need == 0:
-            p, n = None, 0
+            w, n = None, 0
         elif stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            p, n = workspace.data_ptr(), need
+            w, n = workspace.data_ptr(), need
         else:
             # from the pool of the stream that the kernels run on: freed with
             # this call, it can only be handed out again behind them
             with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
                                    torch.cuda.ExternalStream(stream, device=self.device)):
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            p, n = workspace.data_ptr(), need
-        r = call(p, n, torch.cuda.current_stream(index).cuda_stream if stream is None else _stream(stream))
+            w, n = workspace.data_ptr(), need
+        r = self.function(*self.args(p), w, n, _raw_stream(index) if stream is None else _stream(stream))
         if r != 0:
             raise PgemmError(r)
 
+    def _given(self, p, workspace):
+        if workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % self.device)
+        w, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if n < self.need or w % 16:
+            raise ValueError("workspace must be 16-byte aligned and hold %d bytes, got %d" % (self.need, n))
+        for name, i, bytes_, _ in self.tensors:
+            if n and p[i] < w + n and w < p[i] + bytes_:
+                raise ValueError("workspace overlaps %s" % name)
+        return w, n
 
-def _first(span):
-    return span[0]
+
+_CALLS = {}
+
+
+def _cached(describe, ts, act):
+    """The checked call of these types, shapes, strides and devices."""
+    try:
+        key = (describe, act) + tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in ts])
+        c = _CALLS.get(key)
+    except TypeError:  # an activation that is no name
+        raise ValueError("unknown activation %r: one of %s" % (act, ", ".join(ACT))) from None
+    if c is None:
+        c = describe(*ts, act)
+        if len(_CALLS) >= 4096:
+            _CALLS.clear()
+        _CALLS[key] = c
+    return c
 
 
 def _stored_rows(t):
@@ -466,6 +486,8 @@ try:
     _BY_CODE = {c: t for t, c in _FLOAT_CODE.items()}
     _OUT_TYPES = {c: (t,) if c == PGEMM_F32 else (t, torch.float32) for c, t in _BY_CODE.items()}
     _OWN_TYPE = {c: (t,) for c, t in _BY_CODE.items()}
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
 except NameError:  # without torch only the C entry points above are used
     pass
 
@@ -475,11 +497,6 @@ def _act_code(act):
         return ACT[act]
     except (KeyError, TypeError):
         raise ValueError("unknown activation %r: one of %s" % (act, ", ".join(ACT))) from None
-
-
-@functools.lru_cache(maxsize=1024)
-def _workspace_bytes(function, *args):
-    return getattr(_lib, function)(*args)
 
 
 def _sizes(X, W, name="W"):
@@ -506,21 +523,25 @@ def linear(X, W, Y, bias=None, residual=None, act="none", Z=None, workspace=None
     unless one is passed.  Bad arguments raise ValueError before anything is
     launched; a status the library returns raises PgemmError.  Returns Y.
     """
+    ts = (X, W, Y, bias, residual, Z)
+    _cached(_describe_linear, ts, act).run(ts, workspace, stream, (2, 4))
+    return Y
+
+
+def _describe_linear(X, W, Y, bias, residual, Z, act):
     M, N, K = _sizes(X, W)
     c = _Call(X)
-    own, out = _OWN_TYPE[c.dtype], _OUT_TYPES[c.dtype]
+    t, own = c.dtype, _OWN_TYPE[c.dtype]
     a = _act_code(act)
-    px, ldx = c.rows("X", X, (M, K), own)
-    pw, ldw, order = c.weight("W", W, (K, N), own)
-    pb = c.vector("bias", bias, N, own)
-    py, ldy = c.rows("Y", Y, (M, N), out, True)
-    pr, ldr = c.rows("residual", residual, (M, N), (Y.dtype,))
-    pz, ldz = c.rows("Z", Z, (M, N), own, True)
-    c.check_overlap((residual, Y))
-    c.go(_workspace_bytes("pgemm_linear_workspace", M, N, K, c.dtype), workspace, stream,
-         lambda p, n, s: pgemm_linear(M, N, K, px, ldx, pw, ldw, order, pb, pr, ldr, a, pz, ldz, py, ldy,
-                                      _FLOAT_CODE[Y.dtype], c.dtype, p, n, s))
-    return Y
+    ldx = c.rows("X", 0, X, (M, K), own)
+    ldw, order = c.weight("W", 1, W, (K, N), own)
+    ldy = c.rows("Y", 2, Y, (M, N), _OUT_TYPES[t], True)
+    c.vector("bias", 3, bias, N, own)
+    ldr = c.rows("residual", 4, residual, (M, N), (Y.dtype,))
+    ldz = c.rows("Z", 5, Z, (M, N), own, True)
+    out = _FLOAT_CODE[Y.dtype]
+    return c.done(pgemm_linear, pgemm_linear_workspace(M, N, K, t), lambda p: (
+        M, N, K, p[0], ldx, p[1], ldw, order, p[3], p[4], ldr, a, p[5], ldz, p[2], ldy, out, t))
 
 
 def gated(X, Wg, Wu, H, bias_g=None, bias_u=None, act="silu", G=None, U=None, workspace=None, stream=None):
@@ -530,32 +551,26 @@ def gated(X, Wg, Wu, H, bias_g=None, bias_u=None, act="silu", G=None, U=None, wo
     receive the two projections (with bias, before the activation) in X's type,
     which gated_backward reads.  Returns H.
     """
-    M, N, K = _sizes(X, Wg, "Wg")
-    c = _Call(X)
-    own, out = _OWN_TYPE[c.dtype], _OUT_TYPES[c.dtype]
-    a = _act_code(act)
-    px, ldx = c.rows("X", X, (M, K), own)
-    pg, pu, ldw, order = _two_weights(c, "Wg", Wg, "Wu", Wu, (K, N), own, False)
-    pbg, pbu = c.vector("bias_g", bias_g, N, own), c.vector("bias_u", bias_u, N, own)
-    ph, ldh = c.rows("H", H, (M, N), out, True)
-    pG, ldg = c.rows("G", G, (M, N), own, True)
-    pU, ldu = c.rows("U", U, (M, N), own, True)
-    c.check_overlap()
-    c.go(_workspace_bytes("pgemm_gated_workspace", M, N, K, c.dtype), workspace, stream,
-         lambda p, n, s: pgemm_gated(M, N, K, px, ldx, pg, pu, ldw, order, pbg, pbu, a, pG, ldg, pU, ldu, ph, ldh,
-                                     _FLOAT_CODE[H.dtype], c.dtype, p, n, s))
+    ts = (X, Wg, Wu, H, bias_g, bias_u, G, U)
+    _cached(_describe_gated, ts, act).run(ts, workspace, stream)
     return H
 
 
-def _two_weights(c, name0, w0, name1, w1, shape, dtypes, out):
-    p0, ld0, order0 = c.weight(name0, w0, shape, dtypes, out)
-    p1, ld1, order1 = c.weight(name1, w1, shape, dtypes, out)
-    if (w0 is None) != (w1 is None):
-        raise ValueError("%s and %s must be given together" % (name0, name1))
-    if w0 is not None and (ld0 != ld1 or order0 != order1):
-        raise ValueError("%s and %s must have the same strides, got %s and %s"
-                         % (name0, name1, tuple(w0.stride()), tuple(w1.stride())))
-    return p0, p1, ld0, order0
+def _describe_gated(X, Wg, Wu, H, bias_g, bias_u, G, U, act):
+    M, N, K = _sizes(X, Wg, "Wg")
+    c = _Call(X)
+    t, own = c.dtype, _OWN_TYPE[c.dtype]
+    a = _act_code(act)
+    ldx = c.rows("X", 0, X, (M, K), own)
+    ldw, order = c.weights(("Wg", "Wu"), (1, 2), (Wg, Wu), (K, N), own)
+    ldh = c.rows("H", 3, H, (M, N), _OUT_TYPES[t], True)
+    c.vector("bias_g", 4, bias_g, N, own)
+    c.vector("bias_u", 5, bias_u, N, own)
+    ldg = c.rows("G", 6, G, (M, N), own, True)
+    ldu = c.rows("U", 7, U, (M, N), own, True)
+    out = _FLOAT_CODE[H.dtype]
+    return c.done(pgemm_gated, pgemm_gated_workspace(M, N, K, t), lambda p: (
+        M, N, K, p[0], ldx, p[1], p[2], ldw, order, p[4], p[5], a, p[6], ldg, p[7], ldu, p[3], ldh, out, t))
 
 
 def _grad_type(c, outs):
@@ -582,25 +597,29 @@ def linear_backward(dY, X, W, Z=None, act="none", dX=None, dW=None, dbias=None, 
     (pgemm_linear_backward_workspace) and errors as for linear.
     Returns (dX, dW, dbias).
     """
+    ts = (dY, X, W, Z, dX, dW, dbias)
+    _cached(_describe_linear_backward, ts, act).run(ts, workspace, stream)
+    return dX, dW, dbias
+
+
+def _describe_linear_backward(dY, X, W, Z, dX, dW, dbias, act):
     M, N, K = _sizes(X, W)
     c = _Call(X)
-    own = _OWN_TYPE[c.dtype]
+    t, own = c.dtype, _OWN_TYPE[c.dtype]
     a = _act_code(act)
     if a != 0 and Z is None:
         raise ValueError("Z, the pre-activation, is needed for act %r" % act)
     gt = _grad_type(c, (dW, dbias))
-    pdy, lddy = c.rows("dY", dY, (M, N), own)
-    px, ldx = c.rows("X", X, (M, K), own)
-    pw, ldw, order = c.weight("W", W, (K, N), own)
-    pz, ldz = c.rows("Z", Z, (M, N), own)
-    pdx, lddx = c.rows("dX", dX, (M, K), own, True)
-    pdw, lddw, dorder = c.weight("dW", dW, (K, N), (gt,), True)
-    pdb = c.vector("dbias", dbias, N, (gt,), True)
-    c.check_overlap()
-    c.go(_workspace_bytes("pgemm_linear_backward_workspace", M, N, K, a, c.dtype), workspace, stream,
-         lambda p, n, s: pgemm_linear_backward(M, N, K, pdy, lddy, px, ldx, pw, ldw, order, pz, ldz, a, pdx, lddx,
-                                               pdw, lddw, dorder, pdb, _FLOAT_CODE[gt], c.dtype, p, n, s))
-    return dX, dW, dbias
+    lddy = c.rows("dY", 0, dY, (M, N), own)
+    ldx = c.rows("X", 1, X, (M, K), own)
+    ldw, order = c.weight("W", 2, W, (K, N), own)
+    ldz = c.rows("Z", 3, Z, (M, N), own)
+    lddx = c.rows("dX", 4, dX, (M, K), own, True)
+    lddw, dorder = c.weight("dW", 5, dW, (K, N), (gt,), True)
+    c.vector("dbias", 6, dbias, N, (gt,), True)
+    g = _FLOAT_CODE[gt]
+    return c.done(pgemm_linear_backward, pgemm_linear_backward_workspace(M, N, K, a, t), lambda p: (
+        M, N, K, p[0], lddy, p[1], ldx, p[2], ldw, order, p[3], ldz, a, p[4], lddx, p[5], lddw, dorder, p[6], g, t))
 
 
 def gated_backward(dH, X, Wg, Wu, G, U, act="silu", dX=None, dWg=None, dWu=None, dbias_g=None, dbias_u=None,
@@ -614,25 +633,30 @@ def gated_backward(dH, X, Wg, Wu, G, U, act="silu", dX=None, dWg=None, dWu=None,
     (pgemm_gated_backward_workspace) and errors as for linear_backward.
     Returns (dX, dWg, dWu, dbias_g, dbias_u).
     """
+    ts = (dH, X, Wg, Wu, G, U, dX, dWg, dWu, dbias_g, dbias_u)
+    _cached(_describe_gated_backward, ts, act).run(ts, workspace, stream)
+    return dX, dWg, dWu, dbias_g, dbias_u
+
+
+def _describe_gated_backward(dH, X, Wg, Wu, G, U, dX, dWg, dWu, dbias_g, dbias_u, act):
     M, N, K = _sizes(X, Wg, "Wg")
     c = _Call(X)
-    own = _OWN_TYPE[c.dtype]
+    t, own = c.dtype, _OWN_TYPE[c.dtype]
     a = _act_code(act)
     gt = _grad_type(c, (dWg, dWu, dbias_g, dbias_u))
-    pdh, lddh = c.rows("dH", dH, (M, N), own)
-    px, ldx = c.rows("X", X, (M, K), own)
-    pg, pu, ldw, order = _two_weights(c, "Wg", Wg, "Wu", Wu, (K, N), own, False)
-    pG, ldg = c.rows("G", G, (M, N), own)
-    pU, ldu = c.rows("U", U, (M, N), own)
-    pdx, lddx = c.rows("dX", dX, (M, K), own, True)
-    pdg, pdu, lddw, dorder = _two_weights(c, "dWg", dWg, "dWu", dWu, (K, N), (gt,), True)
-    pbg, pbu = c.vector("dbias_g", dbias_g, N, (gt,), True), c.vector("dbias_u", dbias_u, N, (gt,), True)
-    c.check_overlap()
-    c.go(_workspace_bytes("pgemm_gated_backward_workspace", M, N, K, c.dtype), workspace, stream,
-         lambda p, n, s: pgemm_gated_backward(M, N, K, pdh, lddh, px, ldx, pg, pu, ldw, order, pG, ldg, pU, ldu, a,
-                                              pdx, lddx, pdg, pdu, lddw, dorder, pbg, pbu, _FLOAT_CODE[gt], c.dtype,
-                                              p, n, s))
-    return dX, dWg, dWu, dbias_g, dbias_u
+    lddh = c.rows("dH", 0, dH, (M, N), own)
+    ldx = c.rows("X", 1, X, (M, K), own)
+    ldw, order = c.weights(("Wg", "Wu"), (2, 3), (Wg, Wu), (K, N), own)
+    ldg = c.rows("G", 4, G, (M, N), own)
+    ldu = c.rows("U", 5, U, (M, N), own)
+    lddx = c.rows("dX", 6, dX, (M, K), own, True)
+    lddw, dorder = c.weights(("dWg", "dWu"), (7, 8), (dWg, dWu), (K, N), (gt,), True)
+    c.vector("dbias_g", 9, dbias_g, N, (gt,), True)
+    c.vector("dbias_u", 10, dbias_u, N, (gt,), True)
+    g = _FLOAT_CODE[gt]
+    return c.done(pgemm_gated_backward, pgemm_gated_backward_workspace(M, N, K, t), lambda p: (
+        M, N, K, p[0], lddh, p[1], ldx, p[2], p[3], ldw, order, p[4], ldg, p[5], ldu, a, p[6], lddx, p[7], p[8],
+        lddw, dorder, p[9], p[10], g, t))
 
 
 def pgemm_hazard_copy_reduce(X, rows, cols, ldx, row_sums, reuse_wait, delay_wave=-1, delay_cycles=0, trace=None,

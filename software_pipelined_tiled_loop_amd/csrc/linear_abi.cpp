@@ -64,31 +64,62 @@ struct Plan {
     int np8;
 };
 
-// Estimated microseconds of a product on tiles of variant v with its K tiles
-// split in `splits`: the workgroups run in rounds, one 256 x 256 tile or up to
-// two 128 x 128 tiles per CU at a time, at measured rates of the whole part.
-double est_us(const LinVariant& v, const Shape& p, int dtype, int64_t splits) {
-    const bool f32 = dtype == PGEMM_F32, large = v.bm == 256;
+// Estimated microseconds of a product with its K tiles split in `splits`, from
+// rates and fixed costs measured on calls back to back (see the tables beside
+// the variants).
+//
+// Tiles: the workgroups run in rounds, one 256 x 256 tile or up to two
+// 128 x 128 tiles per CU at a time.
+double est_tiles(const LinVariant& v, const Shape& p, bool f32, int64_t wgs, double kt) {
+    const bool large = v.bm == 256;
     // FLOP/us of one CU: alone with one workgroup, and shared by two
-    const double alone = (large ? (f32 ? 148e6 : 1340e6) : (f32 ? 90e6 : 600e6)) / kNumCU;
+    const double alone = (large ? (f32 ? 148e6 : 1640e6) : (f32 ? 90e6 : 600e6)) / kNumCU;
     const double shared = large ? alone : (f32 ? 140e6 : 950e6) / kNumCU;
-    const int64_t wgs = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs * splits;
-    const double kt = (double)ceil_div(ceil_div(p.K, v.bk) * p.halves, splits);
     const double flop = 2.0 * v.bm * v.bn * v.bk * kt * (p.gated ? 2 : 1);
     const int64_t slots = large ? kNumCU : 2 * kNumCU;
     const int64_t rounds = wgs / slots, rest = wgs % slots;
-    const double round_us = (large ? 1 : 2) * flop / shared, fixed = large ? 6.0 : 4.0;
+    const double round_us = (large ? 1 : 2) * flop / shared, fixed = large ? 14.0 : 6.0;
     double us = rounds * (round_us + fixed);
     if (rest > kNumCU) us += round_us + fixed;
     else if (rest > 0) us += flop / alone + fixed;
+    const double bytes = (double)p.K * p.halves * (f32 ? 4 : 2) * (p.rows + p.cols * (p.gated ? 2.0 : 1.0));
+    const double mem = bytes / 4.9e6 + fixed;
+    return (us > mem ? us : mem) + 2.0;
+}
+// Few rows: a CU streams up to 35 bytes/ns, all of them together 4.9 TB/s, and
+// each round of workgroups costs 2.5 us.
+double est_few(const LinVariant& v, const Shape& p, bool f32, int64_t wgs, double kt) {
+    const double cols = v.bn * (p.gated ? 2 : 1), es = f32 ? 4 : 2;
+    const double kb = kt * v.bk * ((p.rows < v.bm ? p.rows : v.bm) + cols) * es / 1e3;
+    const double load = wgs > kNumCU ? (double)wgs / kNumCU : 1.0;
+    const double rate = wgs * 35.0 < 4900.0 ? 35.0 : 4900.0 / (wgs < kNumCU ? wgs : kNumCU);
+    const double mem = kb / rate, mfma = 2.0 * v.bm * cols * v.bk * kt / (f32 ? 0.45e6 : 2.5e6);
+    return 2.5 * ceil_div(wgs, (int64_t)kNumCU * v.per_cu) + load * (mem > mfma ? mem : mfma);
+}
+// Splits of a few-rows product.  Below one workgroup a CU, splitting K up to
+// that fills the CUs (one token by 4096 x 4096 on 64 columns: 15.9 / 13.6 /
+// 11.9 / 12.6 us in 1 / 2 / 4 / 8).  Beyond, it does not pay (16 rows, K =
+// 16384: 32.1 us in 4, 36.0 in 8) but for the gated block with W [N][K], where
+// 1024 workgroups stream faster than 256 (one token to 16384 x 4096: 61.9 /
+// 66.9 / 52.4 / 55.1 us in 1 / 2 / 4 / 8; W [K][N]: 59.7 / 61.1 / 60.5).
+int64_t few_splits(const LinVariant& v, const Shape& p, int64_t tiles, int64_t kt) {
+    int64_t s = tiles < kNumCU ? kNumCU / tiles : p.gated && p.lay == LIN_KK ? 4 * kNumCU / tiles : 1;
+    if (s > kt / v.few) s = kt / v.few;  // a K tile for each wave
+    return s < 1 ? 1 : s > 32 ? 32 : s;
+}
+double est_us(const LinVariant& v, const Shape& p, int dtype, int64_t splits) {
+    const bool f32 = dtype == PGEMM_F32;
+    const int64_t wgs = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs * splits;
+    const double kt = (double)ceil_div(ceil_div(p.K, v.bk) * p.halves, splits);
+    double us = v.few ? est_few(v, p, f32, wgs, kt) : est_tiles(v, p, f32, wgs, kt);
     // the join: a launch, and the partial sums written and read
-    if (splits > 1) us += 4.0 + 2.0 * splits * p.rows * p.cols * (p.gated ? 2 : p.outs) * 4.0 / 4e6;
+    if (splits > 1) us += 4.5 + 2.0 * splits * p.rows * p.cols * (p.gated ? 2 : p.outs) * 4.0 / 4e6;
     return us;
 }
 
 // The tile and the splits of a product, from its sizes and type alone (so the
 // workspace functions and the calls agree).
-Plan plan_product(const Shape& p, int dtype) {
+Plan search_plan(const Shape& p, int dtype) {
     const LinKernels k = kernels_for(dtype);
     Plan best{};
     double best_us = 0.0;
@@ -97,7 +128,10 @@ Plan plan_product(const Shape& p, int dtype) {
         if (v.lay != p.lay || v.gated != p.gated) continue;
         const int64_t kt = ceil_div(p.K, v.bk) * p.halves;
         const int64_t tiles = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs;
-        for (int64_t s = 1; s <= 32 && (s == 1 || (s * 4 <= kt && tiles * s <= 2 * kNumCU)); ++s) {
+        const int64_t few = v.few ? few_splits(v, p, tiles, kt) : 0;
+        const bool must = few > 1 && tiles >= kNumCU;  // the gated block's many workgroups
+        for (int64_t s = 1; s <= 32; ++s) {
+            if (v.few ? s != few && (s > 1 || must) : s > 1 && (s * 4 > kt || tiles * s > 2 * kNumCU)) continue;
             const double us = est_us(v, p, dtype, s);
             if (best.v && us >= best_us) continue;
             best_us = us;
@@ -111,6 +145,30 @@ Plan plan_product(const Shape& p, int dtype) {
     best.np8 = (int)round_up(p.cols, 8);
     best.part_bytes = best.splits > 1 ? best.splits * (p.gated ? 2 : p.outs) * p.rows * best.np8 * 4 : 0;
     return best;
+}
+
+// The search takes some microseconds, as long as a small product runs: each
+// thread keeps the plans of the last shapes it met (a plan depends on nothing
+// but its key).
+Plan plan_product(const Shape& p, int dtype) {
+    struct Slot {
+        Shape key;
+        int dtype;
+        Plan plan;
+    };
+    static thread_local Slot slots[64];
+    uint64_t h = (uint64_t)p.rows * 0x9e3779b97f4a7c15ull + (uint64_t)p.cols * 0xc2b2ae3d27d4eb4full +
+                 (uint64_t)p.K * 0x165667b19e3779f9ull +
+                 (uint64_t)(p.lay + 3 * p.gated + 6 * p.halves + 18 * p.outs + 54 * dtype) * 0xd6e8feb86659fd93ull;
+    Slot& s = slots[(h ^ (h >> 29)) >> 32 & 63];
+    const Shape& k = s.key;
+    if (!s.plan.v || s.dtype != dtype || k.rows != p.rows || k.cols != p.cols || k.K != p.K || k.lay != p.lay ||
+        k.gated != p.gated || k.halves != p.halves || k.outs != p.outs) {
+        s.plan = search_plan(p, dtype);
+        s.key = p;
+        s.dtype = dtype;
+    }
+    return s.plan;
 }
 
 int64_t part_bytes(const Shape& p, int dtype) {

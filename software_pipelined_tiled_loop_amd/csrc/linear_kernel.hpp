@@ -903,6 +903,199 @@ __global__ void __launch_bounds__(C::NT, C::MINW) linear_kernel(LinArgs g) {
     lin_epilogue<C>(g.e, m0, n0, out, smem, acc, wave, lane, wm0, wnp);
 }
 
+// ---- few rows -----------------------------------------------------------------------------------
+
+// One token to a few dozen: the weights' bytes bound the time, so what counts is
+// how many of them each CU has under way.  The waves of a workgroup share its
+// output tile (16 FM rows, NCOL columns) and deal out its K tiles in turn; each
+// has a ring of its own, which only it fills and reads, so nothing in the loop
+// waits for another wave: a wave waits for its own oldest K tile (vmcnt) while
+// S - 1 more are in flight.  At the end the waves' sums are added in LDS, in the
+// order of the waves.
+template <int D, int LA_, int LB_, int FM_, int NCOL_, int NW_, int S_, bool GATED_>
+struct FewCfg {
+    static constexpr int Dt = D, FM = FM_, NCOL = NCOL_, NW = NW_, S = S_;
+    static constexpr bool GATED = GATED_;
+    static constexpr int NP = GATED ? 2 : 1, NCOLP = NCOL / NP;  // output columns of the tile
+    static constexpr int ES = Traits<D>::ES, BK = 128 / ES, NKS = BK / Traits<D>::KSTEP;
+    static constexpr int BM = 16 * FM, NT = 64 * NW;
+    typedef Opnd<D, LA_, BM, BK> OA;
+    typedef Opnd<D, LB_, NCOLP, BK> OB;
+    static constexpr int FNP = NCOLP / 16, FN = FNP * NP;
+    static constexpr int STAGE = OA::BYTES + NP * OB::BYTES, RING = S * STAGE, LDS = NW * RING;
+    static constexpr int LPA = OA::BYTES / 1024, LPB = OB::BYTES / 1024, LPS = LPA + NP * LPB;
+    static_assert(LDS <= 163840 && S >= 2 && LPS * (S - 2) <= 63, "ring");
+    static_assert(FM * FN * 1024 <= RING, "the sums fit the wave's ring");
+    static_assert(NKS == 2, "K steps");
+};
+
+template <class C>
+__device__ __forceinline__ void few_multiply(f32x4 (&acc)[C::FM][C::FN], const char PGEMM_LDS* stage, int lane) {
+#pragma unroll
+    for (int ks = 0; ks < C::NKS; ++ks) {
+        i32x4 a[C::FM], b[C::FN];
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) C::OA::read(stage, ks, 16 * i, lane, a[i]);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            C::OB::read(stage + C::OA::BYTES + (j / C::FNP) * C::OB::BYTES, ks, 16 * (j % C::FNP), lane, b[j]);
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) mfma_swapped<C::Dt>(acc[i][j], a[i], b[j]);
+    }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::NT) linear_few(LinArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS];
+    typedef typename C::OA OA;
+    typedef typename C::OB OB;
+    const int tiles_n = g.tiles_n * g.outs, per_split = g.tiles_m * tiles_n;
+    const WgTiles w = wg_tiles_of(per_split * g.splits, (int)blockIdx.x, (int)gridDim.x);
+    if (w.count == 0) return;
+    int L = w.start + w.lb, split = 0;
+    if (g.splits > 1) {
+        split = __builtin_amdgcn_readfirstlane(L / per_split);
+        L -= split * per_split;
+    }
+    // row tiles of the same columns side by side: they share the weights in L2
+    int tn = __builtin_amdgcn_readfirstlane(L / g.tiles_m);
+    const int tm = L - tn * g.tiles_m, out = tn >= g.tiles_n ? 1 : 0;
+    tn -= out * g.tiles_n;
+    const int m0 = tm * C::BM, n0 = tn * C::NCOLP;
+    const int rows_left = g.e.M - m0, cols_left = g.e.N - n0;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char PGEMM_LDS* ring = (char PGEMM_LDS*)smem_raw + wave * C::RING;
+    const uint32_t lds0 = (uint32_t)(size_t)ring;
+
+    const char* a_half[2];
+    const char* b_half[2];  // gated: the two panels
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = g.outs == 2 ? out : h < g.halves ? h : 0;
+        a_half[h] = (const char*)g.A[i] + OA::origin(m0, 0, g.lda);
+        b_half[h] = (const char*)g.B[C::NP == 2 ? h : i] + OB::origin(n0, 0, g.ldb);
+    }
+    const int64_t sa = OA::step(g.lda), sb = OB::step(g.ldb);
+    uint32_t va[C::LPA], vb[C::LPB];
+#pragma unroll
+    for (int q = 0; q < C::LPA; ++q) {
+        int e, k;
+        OA::chunk(q * 1024 + lane * 16, e, k);
+        va[q] = e < rows_left ? OA::mem_off(e, k, g.lda) : OOB;
+    }
+#pragma unroll
+    for (int q = 0; q < C::LPB; ++q) {
+        int e, k;
+        OB::chunk(q * 1024 + lane * 16, e, k);
+        vb[q] = e < cols_left ? OB::mem_off(e, k, g.ldb) : OOB;
+    }
+
+    f32x4 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // This split's K tiles [t0, t1); the wave's are t0 + wave, + NW, ...
+    const int64_t total = (int64_t)g.nfull * g.halves;
+    const int t0 = (int)(total * split / g.splits), t1 = (int)(total * (split + 1) / g.splits);
+    // Loads K tile t into stage st; past the last one every lane reads zeros.
+    const auto issue = [&](int t, int st) {
+        const int h = t >= g.nfull ? 1 : 0, kt = t - h * g.nfull;
+        const int range = t < t1 ? (int)0x80000000u : 0;
+        const uint32_t at = lds0 + (uint32_t)(st * C::STAGE);
+        i32x4 r = make_rsrc_sgpr((h ? a_half[1] : a_half[0]) + sa * kt);
+        r[2] = range;
+#pragma unroll
+        for (int q = 0; q < C::LPA; ++q) dma16(r, va[q], at + q * 1024u);
+#pragma unroll
+        for (int p = 0; p < C::NP; ++p) {
+            r = make_rsrc_sgpr((C::NP == 2 ? b_half[p] : h ? b_half[1] : b_half[0]) + sb * kt);
+            r[2] = range;
+#pragma unroll
+            for (int q = 0; q < C::LPB; ++q) dma16(r, vb[q], at + OA::BYTES + p * OB::BYTES + q * 1024u);
+        }
+    };
+    int t = t0 + wave;
+    if (t < t1) {
+#pragma unroll
+        for (int p = 0; p < C::S - 1; ++p) issue(t + p * C::NW, p);
+        int st = 0;
+        for (; t < t1; t += C::NW) {
+            // the oldest K tile has landed, and the stage before it has been read
+            lgkm_drain();
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(C::LPS * (C::S - 2)) : "memory");
+            issue(t + (C::S - 1) * C::NW, st == 0 ? C::S - 1 : st - 1);
+            few_multiply<C>(acc, ring + st * C::STAGE, lane);
+            st = st + 1 == C::S ? 0 : st + 1;
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing LDS
+    asm volatile("" ::: "memory");
+    // What is left of each half after the ring's K tiles, one cut tile a wave.
+    if (split == g.splits - 1) {
+        const int ncut = (g.K + C::BK - 1) / C::BK - g.nfull;
+        for (int c = wave; c < ncut * g.halves; c += C::NW) {
+            const int h = c >= ncut ? 1 : 0, kt = g.nfull + c - h * ncut, k_left = g.K - kt * C::BK;
+            OA::load_cut((h ? a_half[1] : a_half[0]) + sa * kt, g.lda, rows_left, k_left, ring, 0, C::LPA, lane);
+#pragma unroll
+            for (int p = 0; p < C::NP; ++p)
+                OB::load_cut((C::NP == 2 ? b_half[p] : h ? b_half[1] : b_half[0]) + sb * kt, g.ldb, cols_left, k_left,
+                             ring + OA::BYTES + p * OB::BYTES, 0, C::LPB, lane);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            few_multiply<C>(acc, ring, lane);
+            lgkm_drain();
+            asm volatile("" ::: "memory");
+        }
+    }
+
+    // The waves' sums, each in its own ring.
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) *(f32x4 PGEMM_LDS*)(ring + ((i * C::FN + j) * 64 + lane) * 16) = acc[i][j];
+    lgkm_barrier();
+    constexpr int GPR = C::NCOLP / 8, GROUPS = C::BM * GPR;  // groups of eight columns
+    for (int q = (int)threadIdx.x; q < GROUPS; q += C::NT) {
+        const int row = q / GPR, c8 = q % GPR;
+        if (row >= rows_left || 8 * c8 >= cols_left) continue;
+        f32x8 s[C::NP];
+#pragma unroll
+        for (int p = 0; p < C::NP; ++p) {
+            s[p] = zero8();
+            const int block = (row >> 4) * C::FN + p * C::FNP + (c8 >> 1);
+            const char PGEMM_LDS* at =
+                (const char PGEMM_LDS*)smem_raw + (block * 64 + (row & 15) + 32 * (c8 & 1)) * 16;
+#pragma unroll
+            for (int v = 0; v < C::NW; ++v)
+                s[p] += join8(*(const f32x4 PGEMM_LDS*)(at + v * C::RING), *(const f32x4 PGEMM_LDS*)(at + v * C::RING + 256));
+        }
+        if (g.part) {
+            const int planes = C::GATED ? 2 : g.outs;
+            float* o = g.part + (((int64_t)split * planes + out) * g.e.M + m0 + row) * g.np8 + n0 + 8 * c8;
+#pragma unroll
+            for (int p = 0; p < C::NP; ++p) *(f32x8*)(o + (int64_t)p * g.e.M * g.np8) = s[p];
+            continue;
+        }
+        const Epi<C::Dt, C::GATED> ep(g.e, m0, n0, out, row, 8 * c8);
+        const f32x8 b0 = ep.bias(0), b1 = C::GATED ? ep.bias(1) : b0;
+        typename Epi<C::Dt, C::GATED>::Raw res{};
+        if (g.e.R && ep.same()) res = ep.residual(0);
+        with_act(g.e.act.kind, [&](auto kind) {
+            constexpr int KIND = decltype(kind)::value;
+            ep.template put<KIND>(0, s[0], s[C::NP - 1], b0, b1, res);
+            if (!ep.whole(0)) {
+#pragma unroll
+                for (int x = 0; x < 7; ++x)
+                    if (x < ep.valid(0)) ep.template put1<KIND>(0, x, s[0][x], s[C::NP - 1][x]);
+            }
+        });
+    }
+}
+
 // ---- join of the splits ---------------------------------------------------------------------------
 
 // One thread per eight columns of a row: the splits' sums in the order of the
@@ -964,8 +1157,8 @@ struct SlopeArgs {
     ActArgs act;
 };
 
-constexpr int kSlopeRows = 64;   // rows per workgroup
-constexpr int kSlopeCols = 256;  // columns per workgroup: 32 threads of eight columns
+constexpr int kSlopeRows = 32;   // rows per workgroup: two for each of 16 row groups, both under way at once
+constexpr int kSlopeCols = 128;  // columns per workgroup: 16 threads of eight columns
 
 // The first `valid` of eight elements at byte offset `off`, zeros for the rest.
 template <class T>
@@ -985,7 +1178,7 @@ __global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
     const int strips = (g.N + kSlopeCols - 1) / kSlopeCols;
     const int strip = (int)blockIdx.x % strips, block = (int)blockIdx.x / strips;
     const int n0 = strip * kSlopeCols, m0 = block * kSlopeRows;
-    const int col = 8 * ((int)threadIdx.x & 31), r0 = (int)threadIdx.x >> 5;
+    const int col = 8 * ((int)threadIdx.x & 15), r0 = (int)threadIdx.x >> 4;
     const int rows = g.M - m0 < kSlopeRows ? g.M - m0 : kSlopeRows;
     const int valid = g.N - n0 - col;
     const auto at = [&](const void* p, int64_t ld) {
@@ -997,20 +1190,30 @@ __global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
     if (valid > 0) {
         with_act(g.act.kind, [&](auto kind) {
             constexpr int KIND = decltype(kind)::value;
-            for (int row = r0; row < rows; row += 8) {
-                const f32x8 dy = load_cut8<T>(ry, (uint32_t)(row * (int)g.ldy + col) * sizeof(T), valid);
-                f32x8 d = dy, e = dy;
+            f32x8 dy[2], z[2], u[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = r0 + 16 * i;
+                const int n = row < rows ? valid : 0;
+                dy[i] = load_cut8<T>(ry, (uint32_t)(row * (int)g.ldy + col) * sizeof(T), n);
+                if constexpr (GATED || KIND != ACTK_NONE)
+                    z[i] = load_cut8<T>(rz, (uint32_t)(row * (int)g.ldz + col) * sizeof(T), n);
+                if constexpr (GATED) u[i] = load_cut8<T>(ru, (uint32_t)(row * (int)g.ldu + col) * sizeof(T), n);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = r0 + 16 * i;
+                f32x8 d = dy[i], e = dy[i];
                 if constexpr (GATED || KIND != ACTK_NONE) {
-                    const f32x8 z = load_cut8<T>(rz, (uint32_t)(row * (int)g.ldz + col) * sizeof(T), valid);
                     f32x8 y;
-                    act_slope8<KIND>(g.act, z, y, d);
-                    d *= dy;
+                    act_slope8<KIND>(g.act, z[i], y, d);
+                    d *= dy[i];
                     if constexpr (GATED) {
-                        const f32x8 u = load_cut8<T>(ru, (uint32_t)(row * (int)g.ldu + col) * sizeof(T), valid);
-                        d *= u;
-                        e = dy * y;
+                        d *= u[i];
+                        e = dy[i] * y;
                     }
                 }
+                if (row >= rows) continue;
                 s0 += d;
                 if constexpr (GATED) s1 += e;
                 if (g.dZ) {  // the workspace's rows are whole groups
@@ -1022,16 +1225,16 @@ __global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
         });
     }
     if (!g.sums) return;
-    // columns of the eight row groups, in their order
+    // columns of the sixteen row groups, in their order
     red[0][threadIdx.x] = s0;
     if constexpr (GATED) red[1][threadIdx.x] = s1;
     __syncthreads();
     constexpr int planes = GATED ? 2 : 1;
-    if (threadIdx.x < 32 && valid > 0) {
+    if (threadIdx.x < 16 && valid > 0) {
 #pragma unroll
         for (int p = 0; p < planes; ++p) {
             f32x8 s = red[p][threadIdx.x];
-            for (int k = 1; k < 8; ++k) s += red[p][threadIdx.x + 32 * k];
+            for (int k = 1; k < 16; ++k) s += red[p][threadIdx.x + 16 * k];
             *(f32x8*)(g.sums + ((int64_t)block * planes + p) * g.np8 + n0 + col) = s;
         }
     }

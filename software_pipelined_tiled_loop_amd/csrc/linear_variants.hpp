@@ -15,6 +15,8 @@ enum LinLay : int { LIN_KX = 0, LIN_KK = 1, LIN_XX = 2 };
 struct LinVariant {
     int lay, gated;
     int bm, bn, bk;  // bn: output columns of the tile
+    int few;         // waves that share the K tiles of a few-rows kernel, else 0
+    int per_cu;      // workgroups whose LDS a CU holds
     int (*ring_tiles)(int64_t K, int64_t rows, int64_t lda, int64_t cols, int64_t ldb);
     LinLaunch launch;
 };
@@ -37,6 +39,10 @@ hipError_t lin_launch(void (*kernel)(Args), const Args& a, dim3 grid, int thread
 template <class C>
 hipError_t lin_launch_tile(const LinArgs& a, int grid, hipStream_t s) {
     return lin_launch<LinArgs>(&linear_kernel<C>, a, dim3(grid), C::NT, s);
+}
+template <class C>
+hipError_t lin_launch_few(const LinArgs& a, int grid, hipStream_t s) {
+    return lin_launch<LinArgs>(&linear_few<C>, a, dim3(grid), C::NT, s);
 }
 template <class C>
 int lin_ring_tiles(int64_t K, int64_t rows, int64_t lda, int64_t cols, int64_t ldb) {
@@ -64,7 +70,7 @@ constexpr int lin_lb(int lay) { return lay == LIN_KK ? LAY_K : LAY_X; }
     LinCfg<D, lin_la(LAY), lin_lb(LAY), BM, BN, BK, S, WGM, WGN, GATED != 0>
 #define LIN_VARIANT(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)                                 \
     LinVariant {                                                                            \
-        LAY, GATED, BM, GATED ? BN / 2 : BN, BK,                                            \
+        LAY, GATED, BM, GATED ? BN / 2 : BN, BK, 0, 163840 / LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)::LDS, \
             &lin_ring_tiles<LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)>,               \
             &lin_launch_tile<LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)>               \
     }
@@ -73,6 +79,31 @@ constexpr int lin_lb(int lay) { return lay == LIN_KK ? LAY_K : LAY_X; }
     LIN_VARIANT(D, LIN_KX, 0, BM, BN, BK, S, WGM, WGN), LIN_VARIANT(D, LIN_KK, 0, BM, BN, BK, S, WGM, WGN), \
         LIN_VARIANT(D, LIN_KX, 1, BM, BN, BK, S, WGM, WGN), LIN_VARIANT(D, LIN_KK, 1, BM, BN, BK, S, WGM, WGN), \
         LIN_VARIANT(D, LIN_XX, 0, BM, BN, BK, S, WGM, WGN)
+// A few-rows kernel of 16 FM rows by NCOL columns (gated: of both weights), NW
+// waves with rings of S stages.
+#define LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S) FewCfg<D, lin_la(LAY), lin_lb(LAY), FM, NCOL, NW, S, GATED != 0>
+#define LIN_FEW(D, LAY, GATED, FM, NCOL, NW, S)                                                      \
+    LinVariant {                                                                                     \
+        LAY, GATED, 16 * FM, GATED ? NCOL / 2 : NCOL, LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)::BK, NW, \
+            163840 / LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)::LDS,                               \
+            &lin_ring_tiles<LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)>,                            \
+            &lin_launch_few<LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)>                             \
+    }
+// The few-rows kernels of every layout, of 16, 32 and 64 rows.  Rings of 64 to
+// 128 KiB a workgroup: measured on one token to 16384 x 4096 gated, two
+// workgroups a CU with short rings stream faster (5.0 TB/s) than one with all
+// of the CU's LDS (4.2 TB/s).  Sixteen columns a tile (W [N][K] only, where they
+// are whole rows) give 256 workgroups at N = 4096 without splitting K: 9.5 us
+// for one token by 4096 x 4096, 12.6 us on 64 columns in four splits.
+#define LIN_FEW_CLASSES(D)                                                                                    \
+    LIN_FEW(D, LIN_KK, 0, 1, 16, 8, 3), LIN_FEW(D, LIN_KK, 0, 2, 16, 4, 4), LIN_FEW(D, LIN_KK, 0, 4, 16, 4, 3), \
+        LIN_FEW(D, LIN_KK, 0, 1, 64, 4, 2), LIN_FEW(D, LIN_KK, 0, 2, 64, 4, 2),                               \
+        LIN_FEW(D, LIN_KK, 0, 4, 64, 4, 2), LIN_FEW(D, LIN_KX, 0, 1, 64, 4, 2),                               \
+        LIN_FEW(D, LIN_KX, 0, 2, 64, 4, 2), LIN_FEW(D, LIN_KX, 0, 4, 64, 4, 2),                               \
+        LIN_FEW(D, LIN_KK, 1, 1, 128, 2, 2), LIN_FEW(D, LIN_KK, 1, 1, 64, 4, 2),                              \
+        LIN_FEW(D, LIN_KK, 1, 2, 64, 4, 2), LIN_FEW(D, LIN_KK, 1, 4, 64, 4, 2),                               \
+        LIN_FEW(D, LIN_KX, 1, 1, 64, 4, 2), LIN_FEW(D, LIN_KX, 1, 1, 128, 2, 2),                              \
+        LIN_FEW(D, LIN_KX, 1, 2, 64, 4, 2), LIN_FEW(D, LIN_KX, 1, 4, 64, 4, 2), LIN_FEW(D, LIN_XX, 0, 4, 64, 4, 2)
 #define LIN_KERNELS(D, table)                                                                              \
     LinKernels {                                                                                           \
         table, (int)(sizeof(table) / sizeof(table[0])), &lin_launch_join<D, false>, &lin_launch_join<D, true>, \

@@ -184,14 +184,48 @@ static void check_bounds(int extent, int64_t K, int64_t ld) {
 
 template <int D, int EXT, int BK>
 static void check_bounds_all() {
+    // (16 columns: only along K)
+    constexpr int LX = EXT * Traits<D>::ES >= 64 ? LAY_X : LAY_K;
     for (int extent : {1, 3, 7, 8, 9, 16, 63, 64, 100, 129, 200, 255, 257})
         for (int K : {1, 2, 7, 8, 15, 31, 32, 33, 63, 64, 65, 96, 127, 128, 130, 200})
             for (int pad : {0, 1, 5}) {
                 check_bounds<D, LAY_K, EXT, BK>(extent, K, K + pad);
-                check_bounds<D, LAY_X, EXT, BK>(extent, K, extent + pad);
+                check_bounds<D, LX, EXT, BK>(extent, K, (LX == LAY_X ? extent : K) + pad);
             }
 }
 
+// A few-rows kernel: each wave fills its own stage.
+template <int D, int LA, int LB, int FM, int NCOL, int NW, int S, bool GATED>
+static void check_class(FewCfg<D, LA, LB, FM, NCOL, NW, S, GATED>) {
+    typedef FewCfg<D, LA, LB, FM, NCOL, NW, S, GATED> C;
+    const std::vector<int> a = fill<typename C::OA, C::BM, C::BK, 1>(va);
+    const std::vector<int> b = fill<typename C::OB, C::NCOLP, C::BK, 1>(vb);
+    for (int i = 0; i < FM; ++i)
+        for (int j = 0; j < C::FNP; ++j) {
+            long acc[64][4] = {};
+            for (int ks = 0; ks < C::NKS; ++ks) {
+                static std::vector<int> fa[64], fb[64];
+                fragment<D, LA, C::BM, C::BK>(a, ks, 16 * i, fa);
+                fragment<D, LB, C::NCOLP, C::BK>(b, ks, 16 * j, fb);
+                for (int l = 0; l < 64; ++l)
+                    for (int r = 0; r < 4; ++r)
+                        for (int g = 0; g < 4; ++g)
+                            for (size_t x = 0; x < fa[0].size(); ++x)
+                                acc[l][r] += (long)fa[16 * g + l % 16][x] * fb[16 * g + 4 * (l / 16) + r][x];
+            }
+            for (int l = 0; l < 64; ++l)
+                for (int r = 0; r < 4; ++r) {
+                    const int m = 16 * i + l % 16, n = 16 * j + 4 * (l / 16) + r;
+                    long want = 0;
+                    for (int k = 0; k < C::BK; ++k) want += (long)va(m, k) * vb(n, k);
+                    EXPECT(acc[l][r] == want, "m %d n %d", m, n);
+                }
+        }
+}
+
+#undef LIN_FEW
+#define LIN_FEW(D, LAY, GATED, FM, NCOL, NW, S) \
+    LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S) {}
 #undef LIN_VARIANT
 #define LIN_VARIANT(D, LAY, GATED, BM, BN, BK, S, WGM, WGN) \
     LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN) {}
@@ -205,6 +239,11 @@ int main() {
     classes(LIN_CLASS(DT_F32, 256, 256, 32, 2, 2, 4));
     classes(LIN_CLASS(DT_BF16, 128, 128, 64, 2, 2, 2));
     classes(LIN_CLASS(DT_F32, 128, 128, 32, 2, 2, 2));
+    classes(LIN_FEW_CLASSES(DT_BF16));
+    classes(LIN_FEW_CLASSES(DT_F32));
+    check_bounds_all<DT_BF16, 16, 64>();
+    check_bounds_all<DT_BF16, 32, 64>();
+    check_bounds_all<DT_F32, 64, 32>();
     check_bounds_all<DT_BF16, 256, 64>();
     check_bounds_all<DT_F32, 256, 32>();
     check_bounds_all<DT_BF16, 128, 64>();

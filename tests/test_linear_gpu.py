@@ -418,14 +418,14 @@ def test_graph_replays_equal_the_eager_call(pg):
 def test_two_graphs_share_a_workspace(pg):
     """Replayed one after the other on one stream; the workspace holds nothing between them."""
     say("two graphs")
-    need = max(pg._workspace_bytes("pgemm_gated_backward_workspace", 300, 520, 256, 2),
-               pg._workspace_bytes("pgemm_linear_backward_workspace", 300, 256, 520, 0, 2),
-               pg._workspace_bytes("pgemm_gated_workspace", 300, 520, 256, 2),
-               pg._workspace_bytes("pgemm_linear_workspace", 300, 256, 520, 2),
-               pg._workspace_bytes("pgemm_gated_backward_workspace", 70, 520, 256, 2),
-               pg._workspace_bytes("pgemm_linear_backward_workspace", 70, 256, 520, 0, 2),
-               pg._workspace_bytes("pgemm_gated_workspace", 70, 520, 256, 2),
-               pg._workspace_bytes("pgemm_linear_workspace", 70, 256, 520, 2))
+    need = max(pg.pgemm_gated_backward_workspace(300, 520, 256, 2),
+               pg.pgemm_linear_backward_workspace(300, 256, 520, 0, 2),
+               pg.pgemm_gated_workspace(300, 520, 256, 2),
+               pg.pgemm_linear_workspace(300, 256, 520, 2),
+               pg.pgemm_gated_backward_workspace(70, 520, 256, 2),
+               pg.pgemm_linear_backward_workspace(70, 256, 520, 0, 2),
+               pg.pgemm_gated_workspace(70, 520, 256, 2),
+               pg.pgemm_linear_workspace(70, 256, 520, 2))
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     runs = []
     for M in (300, 70):
