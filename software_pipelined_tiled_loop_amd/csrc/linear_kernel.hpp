@@ -418,26 +418,55 @@ struct Epi {
             return v;
         }
     }
-    // A whole group: v (gated: and w) the product's sums, b0 and b1 the biases, res the residual.
-    template <int KIND>
-    __device__ __forceinline__ void put(int by, f32x8 v, f32x8 w, const f32x8& b0, const f32x8& b1,
-                                        const Raw& res) const {
-        const bool ok = whole(by);
-        if (e.bias[0]) v += b0;
-        if (e.Z) store8<T>(z, at(ok, oz + (uint32_t)(by * (int)e.ldz) * TS), v);
-        v = act8<KIND>(e.act, v);
-        if constexpr (GATED) {
-            if (e.bias[1]) w += b1;
-            if (e.U) store8<T>(u, at(ok, ou + (uint32_t)(by * (int)e.ldu) * TS), w);
-            v *= w;
+    // U whole groups, `step` rows apart: v (gated: and w) the product's sums, b0
+    // and b1 the biases, res the residual.  What is uniform is decided once for
+    // all of them: a branch for each group and option took longer than the
+    // arithmetic (325 clocks a group of eight columns with nothing to add).
+    template <int KIND, int U>
+    __device__ __forceinline__ void put(int by, int step, f32x8 (&v)[U], f32x8 (&w)[GATED ? U : 1], const f32x8& b0,
+                                        const f32x8& b1, const Raw (&res)[U]) const {
+        uint32_t o[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) o[q] = whole(by + q * step) ? 0u : OOB;
+        const auto to = [&](int q, uint32_t lane, int64_t ld, uint32_t size) {
+            return (lane + (uint32_t)((by + q * step) * (int)ld) * size) | o[q];
+        };
+        if (e.bias[0]) {
+#pragma unroll
+            for (int q = 0; q < U; ++q) v[q] += b0;
         }
-        const uint32_t o = at(ok, oy + (uint32_t)(by * (int)e.ldy) * ys);
+        if (e.Z) {
+#pragma unroll
+            for (int q = 0; q < U; ++q) store8<T>(z, to(q, oz, e.ldz, TS), v[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) v[q] = act8<KIND>(e.act, v[q]);
+        if constexpr (GATED) {
+            if (e.bias[1]) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) w[q] += b1;
+            }
+            if (e.U) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) store8<T>(u, to(q, ou, e.ldu, TS), w[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) v[q] *= w[q];
+        }
         if (same()) {
-            if (e.R) v += value(res);
-            store8<T>(y, o, v);
+            if (e.R) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) v[q] += value(res[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) store8<T>(y, to(q, oy, e.ldy, TS), v[q]);
         } else {
-            if (e.R) v += load8<float>(r, at(ok, orr + (uint32_t)(by * (int)e.ldr) * ys));
-            store8<float>(y, o, v);
+            if (e.R) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) v[q] += load8<float>(r, to(q, orr, e.ldr, 4u));
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) store8<float>(y, to(q, oy, e.ldy, 4u), v[q]);
         }
     }
     // Element x of a group.
@@ -672,10 +701,14 @@ struct LinOut {
     static constexpr int STEPS = BLOCKS * 16 / RPI;
     // Groups of a lane in flight (with the next batch's residual): what the
     // registers beside the accumulators hold.
-    static constexpr int WANT = C::ES == 4 ? (C::GATED ? 1 : 2) : C::LONE && !C::GATED ? 8 : 4;
+    static constexpr int WANT = C::ES == 4 ? (C::GATED ? 1 : 2) : C::GATED ? 2 : 4;
     static constexpr int UNROLL = STEPS < WANT ? STEPS : WANT;
     static_assert(PASSES * BLOCKS == C::FM && STEPS % UNROLL == 0 && (NCHK & (NCHK - 1)) == 0, "passes");
-    static PGEMM_HD int at(int row, int chunk) { return (row * NCHK + (chunk ^ (row & (NCHK - 1)))) * 16; }
+    // Even chunks in the first half of a row, odd ones in the second: the lanes
+    // of a row read every second chunk at a time.
+    static PGEMM_HD int at(int row, int chunk) {
+        return (row * NCHK + (chunk & 1) * (NCHK / 2) + ((chunk >> 1) ^ (row & (NCHK / 2 - 1)))) * 16;
+    }
 };
 
 template <class C>
@@ -729,9 +762,7 @@ __device__ __forceinline__ void lin_epilogue(const EpiArgs& e, int m0, int n0, i
                     v[q] = sums(2 * c8);
                     if constexpr (C::GATED) w[q] = sums(C::WNP / 4 + 2 * c8);
                 }
-#pragma unroll
-                for (int q = 0; q < O::UNROLL; ++q)
-                    ep.template put<KIND>(down + (s + q) * O::RPI, v[q], w[C::GATED ? q : 0], b0, b1, res[q]);
+                ep.template put<KIND>(down + s * O::RPI, O::RPI, v, w, b0, b1, res);
             }
             if (cols_cut(e.N)) {
 #pragma unroll 1
@@ -1093,11 +1124,12 @@ __global__ void __launch_bounds__(C::NT) linear_few(LinArgs g) {
         }
         const Epi<C::Dt, C::GATED> ep(g.e, m0, n0, out, row, 8 * c8);
         const f32x8 b0 = ep.bias(0), b1 = C::GATED ? ep.bias(1) : b0;
-        typename Epi<C::Dt, C::GATED>::Raw res{};
-        if (g.e.R && ep.same()) res = ep.residual(0);
+        typename Epi<C::Dt, C::GATED>::Raw res[1] = {};
+        if (g.e.R && ep.same()) res[0] = ep.residual(0);
+        f32x8 v[1] = {s[0]}, u[1] = {s[C::NP - 1]};
         with_act(g.e.act.kind, [&](auto kind) {
             constexpr int KIND = decltype(kind)::value;
-            ep.template put<KIND>(0, s[0], s[C::NP - 1], b0, b1, res);
+            ep.template put<KIND>(0, 0, v, u, b0, b1, res);
             if (!ep.whole(0)) {
 #pragma unroll
                 for (int x = 0; x < 7; ++x)
@@ -1128,23 +1160,23 @@ __global__ void __launch_bounds__(kJoinCols / 8) linear_join(LinArgs g) {
     const float* p = g.part + out * plane + (int64_t)m * g.np8 + n0 + col;
     const Epi<D, GATED> ep(g.e, m, n0, out, 0, col);
     const f32x8 b0 = ep.bias(0), b1 = GATED ? ep.bias(1) : b0;
-    typename Epi<D, GATED>::Raw res{};
-    if (g.e.R && ep.same()) res = ep.residual(0);
-    f32x8 v = zero8(), w = v;
+    typename Epi<D, GATED>::Raw res[1] = {};
+    if (g.e.R && ep.same()) res[0] = ep.residual(0);
+    f32x8 v[1] = {zero8()}, w[1] = {zero8()};
 #pragma unroll 4
     for (int s = 0; s < g.splits; ++s) {
-        v += *(const f32x8*)p;
-        if constexpr (GATED) w += *(const f32x8*)(p + plane);
+        v[0] += *(const f32x8*)p;
+        if constexpr (GATED) w[0] += *(const f32x8*)(p + plane);
         p += planes * plane;
     }
     with_act(g.e.act.kind, [&](auto kind) {
         constexpr int KIND = decltype(kind)::value;
-        ep.template put<KIND>(0, v, w, b0, b1, res);
         if (!ep.whole(0)) {
 #pragma unroll
             for (int x = 0; x < 7; ++x)
-                if (x < ep.valid(0)) ep.template put1<KIND>(0, x, v[x], w[x]);
+                if (x < ep.valid(0)) ep.template put1<KIND>(0, x, v[0][x], w[0][x]);
         }
+        ep.template put<KIND>(0, 0, v, w, b0, b1, res);
     });
 }
 
