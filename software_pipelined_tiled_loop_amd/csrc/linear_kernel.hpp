@@ -95,6 +95,7 @@ struct Opnd {
     static constexpr int ES = Traits<D>::ES, EPC = Traits<D>::EPC, KSTEP = Traits<D>::KSTEP;
     static constexpr int KC = BK * ES / 16, NCH = EXT * ES / 16;
     static constexpr int BYTES = EXT * BK * ES;
+    static constexpr bool along_k = LAY == LAY_K;  // rows in memory run along the contraction
     // LDS reads of one fragment
     static constexpr int READS = LAY == LAY_K ? 1 : (ES == 4 ? 4 : 2);
     static_assert(BYTES % 1024 == 0, "tile must be whole 1-KiB blocks");
@@ -177,18 +178,66 @@ struct Opnd {
         return (int)n;
     }
 
-    // The cut K tile, through registers: blocks [p0, p0 + n) of 1 KiB, chunks
-    // cut at `e_left` / `k_left` completed by element loads, zeros beyond.
-    static __device__ __forceinline__ void load_cut(const char* mem, int64_t ld, int e_left, int k_left,
-                                                    char PGEMM_LDS* tile, int p0, int n, int lane) {
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(mem);
-        for (int p = p0; p < p0 + n; ++p) {
-            int e, k;
-            chunk(p * 1024 + lane * 16, e, k);
-            const int valid = cut_valid(e, k, e_left, k_left);
-            *(i32x4 PGEMM_LDS*)(tile + p * 1024 + lane * 16) =
-                load_chunk_any<ES>(r, mem_off(e, k, ld), valid, valid == EPC);
+    // The cut K tile, through registers: N blocks of 1 KiB from block p0, zeros
+    // beyond the edges.  Where rows hold a chunk or more, a chunk that the edge
+    // cuts is loaded as the 16 bytes that end there and moved down by as many
+    // bytes as lie beyond (`beyond`: the same for every chunk cut, as the edge
+    // is); shorter rows go element by element.  All loads are under way at once:
+    // one after the other the K tile took 16 us.
+    template <int N>
+    static __device__ __forceinline__ void load_cut(const char* mem, int64_t ld, int e_left, int k_left, int row_length,
+                                                    char PGEMM_LDS* tile, int p0, int lane) {
+        if (row_length < EPC) {
+            const __amdgpu_buffer_rsrc_t r = make_rsrc(mem);
+            for (int p = p0; p < p0 + N; ++p) {
+                int e, k;
+                chunk(p * 1024 + lane * 16, e, k);
+                const int valid = cut_valid(e, k, e_left, k_left);
+                *(i32x4 PGEMM_LDS*)(tile + p * 1024 + lane * 16) =
+                    load_chunk_any<ES>(r, mem_off(e, k, ld), valid, valid == EPC);
+            }
+            return;
         }
+        const int beyond = cut_shift(row_length);  // bytes
+        // offsets from 16 bytes before the tile: the chunk cut may begin before it
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(mem - 16);
+        i32x4 v[N];
+        bool cut[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            int e, k;
+            chunk((p0 + q) * 1024 + lane * 16, e, k);
+            const int valid = cut_valid(e, k, e_left, k_left);
+            cut[q] = valid < EPC;
+            const uint32_t off = mem_off(e, k, ld) + 16 - (cut[q] ? beyond : 0);
+            v[q] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, valid > 0 ? off : OOB, 0, 0));
+        }
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            if (beyond) {
+                const i32x4 s = move_down(v[q], beyond);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) v[q][d] = cut[q] ? s[d] : v[q][d];
+            }
+            *(i32x4 PGEMM_LDS*)(tile + (p0 + q) * 1024 + lane * 16) = v[q];
+        }
+    }
+    // Bytes of a row's last chunk beyond the row's end.
+    static PGEMM_HD int cut_shift(int row_length) { return (EPC - row_length % EPC) % EPC * ES; }
+    // The 16 bytes of v from byte `by` (0 < by < 16, uniform) on, then zeros.
+    static __device__ __forceinline__ i32x4 move_down(i32x4 v, int by) {
+        const int w = by >> 2, sh = 8 * (by & 3);
+        uint32_t x[5];
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            x[d] = w == 0 ? (uint32_t)v[d]
+                   : w == 1 ? (d < 3 ? (uint32_t)v[d < 3 ? d + 1 : 3] : 0u)
+                   : w == 2 ? (d < 2 ? (uint32_t)v[d < 2 ? d + 2 : 3] : 0u)
+                            : (d < 1 ? (uint32_t)v[3] : 0u);
+        x[4] = 0;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) v[d] = (int)(uint32_t)((((uint64_t)x[d + 1] << 32) | x[d]) >> sh);
+        return v;
     }
 };
 
@@ -903,10 +952,11 @@ __global__ void __launch_bounds__(C::NT, C::MINW) linear_kernel(LinArgs g) {
         for (int c = 0; c < ncut * g.halves; ++c) {
             const int h = c >= ncut ? 1 : 0, kt = g.nfull + c - h * ncut, k_left = g.K - kt * C::BK;
             drain_barrier();  // every wave has read the stage
-            OA::load_cut((h ? a_half[1] : a_half[0]) + OA::step(g.lda) * kt, g.lda, rows_left, k_left, smem,
-                         wave * C::A_INSTR, C::A_INSTR, lane);
-            OB::load_cut((h ? b_half[1] : b_half[0]) + OB::step(g.ldb) * kt, g.ldb, cols_left, k_left,
-                         smem + C::A_BYTES + panel * OB::BYTES, b_block, C::B_INSTR, lane);
+            OA::template load_cut<C::A_INSTR>((h ? a_half[1] : a_half[0]) + OA::step(g.lda) * kt, g.lda, rows_left,
+                                              k_left, OA::along_k ? g.K : g.e.M, smem, wave * C::A_INSTR, lane);
+            OB::template load_cut<C::B_INSTR>((h ? b_half[1] : b_half[0]) + OB::step(g.ldb) * kt, g.ldb, cols_left,
+                                              k_left, OB::along_k ? g.K : g.e.N,
+                                              smem + C::A_BYTES + panel * OB::BYTES, b_block, lane);
             drain_barrier();
             LinFrags<C> f;
 #pragma unroll
@@ -1082,11 +1132,13 @@ __global__ void __launch_bounds__(C::NT) linear_few(LinArgs g) {
         const int ncut = (g.K + C::BK - 1) / C::BK - g.nfull;
         for (int c = wave; c < ncut * g.halves; c += C::NW) {
             const int h = c >= ncut ? 1 : 0, kt = g.nfull + c - h * ncut, k_left = g.K - kt * C::BK;
-            OA::load_cut((h ? a_half[1] : a_half[0]) + sa * kt, g.lda, rows_left, k_left, ring, 0, C::LPA, lane);
+            OA::template load_cut<C::LPA>((h ? a_half[1] : a_half[0]) + sa * kt, g.lda, rows_left, k_left,
+                                          OA::along_k ? g.K : g.e.M, ring, 0, lane);
 #pragma unroll
             for (int p = 0; p < C::NP; ++p)
-                OB::load_cut((C::NP == 2 ? b_half[p] : h ? b_half[1] : b_half[0]) + sb * kt, g.ldb, cols_left, k_left,
-                             ring + OA::BYTES + p * OB::BYTES, 0, C::LPB, lane);
+                OB::template load_cut<C::LPB>((C::NP == 2 ? b_half[p] : h ? b_half[1] : b_half[0]) + sb * kt, g.ldb,
+                                              cols_left, k_left, OB::along_k ? g.K : g.e.N,
+                                              ring + OA::BYTES + p * OB::BYTES, 0, lane);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             few_multiply<C>(acc, ring, lane);
             lgkm_drain();

@@ -168,8 +168,15 @@ static void check_bounds(int extent, int64_t K, int64_t ld) {
                 } else {
                     n = O::cut_valid(e, k, e_left, k_left);
                     const int64_t at = org + O::mem_off(e, k, ld);
-                    if (n > 0)
+                    const int64_t row = LAY == LAY_K ? K : extent;
+                    if (n > 0 && row >= O::EPC) {
+                        // one 16-byte load, of a chunk cut the one that ends at the edge
+                        const int64_t from = at - (n < O::EPC ? O::cut_shift((int)row) : 0);
+                        EXPECT(from >= 0 && from + 16 <= end, "cut load at %ld of %ld", (long)from, (long)end);
+                        EXPECT(n == O::EPC || (O::EPC - n) * O::ES == O::cut_shift((int)row), "shift");
+                    } else if (n > 0) {
                         EXPECT(at >= 0 && at + n * O::ES <= end, "cut load at %ld of %ld", (long)at, (long)end);
+                    }
                 }
                 for (int x = 0; x < n; ++x) {
                     const int ee = e0 + e + (LAY == LAY_X ? x : 0);
