@@ -128,6 +128,7 @@ Plan search_plan(const Shape& p, int dtype) {
         if (v.lay != p.lay || v.gated != p.gated) continue;
         const int64_t kt = ceil_div(p.K, v.bk) * p.halves;
         const int64_t tiles = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs;
+        if (tiles > 0x1fffff00) continue;  // with their splits, more workgroups than a grid holds
         const int64_t few = v.few ? few_splits(v, p, tiles, kt) : 0;
         const bool must = few > 1 && tiles >= kNumCU;  // the gated block's many workgroups
         for (int64_t s = 1; s <= 32; ++s) {

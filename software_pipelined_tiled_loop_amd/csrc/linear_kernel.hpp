@@ -370,24 +370,28 @@ __device__ __forceinline__ void with_act(int kind, F&& f) {
     }
 }
 
-// act(x) and act'(x) of a smooth activation.  The exponent is held below 2^120
-// so that e p = 1 - p stays finite where p vanishes.
+// act(x) and act'(x) of a smooth activation.  The slope is that at x held to
+// +-64, where it has reached 0 or 1 (so x^3 does not overflow), and its exponent
+// is held below 2^120 so that e p = 1 - p stays finite where p vanishes.
 template <int DEG>
 __device__ __forceinline__ void act_slope(const ActArgs& a, float x, float& y, float& d) {
+    y = act_smooth<DEG>(a, x);
+    x = x > 64.0f ? 64.0f : x < -64.0f ? -64.0f : x;  // NaN stays NaN
     const float t = x * x;
     const float c = DEG == 0 ? a.c[0] : act_poly<DEG>(a, DEG == 6 ? fminf(t, kGeluCap) : t);
     const float e = __builtin_amdgcn_exp2f(fminf(x * c, 120.0f));
     const float p = __builtin_amdgcn_rcpf(1.0f + e);
-    y = x * p;
     if constexpr (DEG == 6) {
         // Phi + x phi, phi(x) = exp2(-t log2(e) / 2) / sqrt(2 pi)
         d = fmaf(x, 0.3989422804f * __builtin_amdgcn_exp2f(-0.7213475204f * t), p);
     } else {
         // d(x P)/dx = P + 2 t P', from the coefficients of -log2(e) P
         const float s = -0.6931471806f * (DEG == 1 ? fmaf(2.0f * t, a.c[1], c) : c);
-        d = fmaf(y * s, e * p, p);
+        d = fmaf(x * p * s, e * p, p);
     }
+    if (x != x) d = x;  // fminf dropped the NaN of the exponent
 }
+
 template <int KIND>
 __device__ __forceinline__ void act_slope8(const ActArgs& a, f32x8 x, f32x8& y, f32x8& d) {
 #pragma unroll

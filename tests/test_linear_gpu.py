@@ -234,7 +234,7 @@ def on_gpu(monkeypatch):
 
 
 #        M     N     K
-LARGE = [(2500, 2310, 200), (4096, 2048, 96), (3001, 2999, 65), (1100, 8200, 130)]
+LARGE = [(2500, 2310, 200), (4096, 2048, 96), (3001, 2999, 65), (1100, 8200, 130), (2304, 2304, 1110)]
 
 
 @pytest.mark.parametrize("order", ["kn", "nk"])
@@ -244,8 +244,8 @@ def test_large_tiles(pg, on_gpu, dtype, order, i):
     """Sizes that fill the GPU, where the planner takes the large tile, in every layout."""
     M, N, K = LARGE[i]
     say("large", dtype, order, (M, N, K))
-    t, act = TYPES[dtype], ref.ACTS[1 + i]
-    m = Maker(500 + i, t, (0, 1, 8, 0)[i], (0, 1, 0, 3)[i])
+    t, act = TYPES[dtype], ref.ACTS[1 + i % 4]
+    m = Maker(500 + i, t, (0, 1, 8, 0, 2)[i], (0, 1, 0, 3, 0)[i])
     X, W, Wu = m.rows(M, K), m.weight(K, N, order), m.weight(K, N, order)
     b, R = m.vector(N), m.rows(M, N)
     Y, Z = m.out(M, N), m.out(M, N)
@@ -269,6 +269,64 @@ def test_large_tiles(pg, on_gpu, dtype, order, i):
     for name, got, want in zip(("dX", "dW", "db"), (dX2, dW2, db), ref.linear_backward(dY, X2, W2, None, "none", t)):
         ref.check(name, got, want)
     m.check_frames()
+
+
+#       M   N      K     few rows: every width of tile, with and without splits, cut K tiles
+FEW = [(1, 4096, 2048), (1, 16384, 520), (3, 33000, 264), (20, 4104, 1000), (40, 4100, 777), (64, 1030, 4001), (17, 300, 9000),
+       (33, 8190, 1500)]
+
+
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("i", range(len(FEW)))
+def test_few_rows(pg, on_gpu, dtype, order, i):
+    M, N, K = FEW[i]
+    say("few", dtype, order, (M, N, K))
+    t, act = TYPES[dtype], ref.ACTS[i % 5]
+    m = Maker(600 + i, t, (0, 1, 8)[i % 3], (0, 3, 1)[i % 3])
+    X, W, Wu, b, R = m.rows(M, K), m.weight(K, N, order), m.weight(K, N, order), m.vector(N), m.rows(M, N)
+    Y, H, U = m.out(M, N), m.out(M, N), m.out(M, N)
+    pg.linear(X, W, Y, bias=b, residual=R, act=act)
+    ref.check("Y", Y, ref.linear(X, W, b, R, act, t)[0])
+    pg.gated(X, W, Wu, H, bias_u=b, act=act, U=U)
+    h, _, u = ref.gated(X, W, Wu, None, b, act, t)
+    ref.check("H", H, h)
+    ref.check("U", U, u)
+    dX = m.out(M, K)
+    pg.gated_backward(R, X, W, Wu, R, U, act=act, dX=dX)
+    ref.check("dX", dX, ref.gated_backward(R, X, W, Wu, R, U, act, t)[0])
+    m.check_frames()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ref.ACTS)
+def test_activations_at_their_ends(pg, dtype, act):
+    """Values whose squares and cubes overflow, infinities and NaN."""
+    say("ends", dtype, act)
+    t, inf, nan = TYPES[dtype], float("inf"), float("nan")
+    x = torch.tensor([3e38, -3e38, 1e20, -1e20, 1e13, -1e13, 1e5, -1e5, 100.0, -100.0, 64.0, -64.0, inf, -inf, nan, 0.0])
+    Z = x.view(1, -1).to(t).cuda()
+    z = Z.double().cpu()[0]
+    eye = torch.eye(16, dtype=t, device="cuda")
+    # a product with the identity would turn 0 * inf into NaN: the bias carries the values
+    Y, X0 = torch.empty(1, 16, dtype=t, device="cuda"), torch.zeros(1, 16, dtype=t, device="cuda")
+    pg.linear(X0, eye, Y, bias=Z[0], act=act)
+    y = Y.double().cpu()[0]
+    want = torch.where(z > 0, z, torch.zeros_like(z)) if act != "none" else z
+    fin = torch.isfinite(z)
+    # beyond +-64 act is x or 0; a smooth act of -64 and -100 is below 1e-25
+    assert bool(((y - want)[fin].abs() <= ref.half_step(t) * want[fin].abs() + 1e-24).all()), y
+    assert y[12] == inf and bool(torch.isnan(y[14]))
+    assert y[13] == (-inf if act == "none" else 0.0) or (act in ("silu", "gelu", "gelu_tanh") and bool(torch.isnan(y[13])))
+    # slopes: 1 and 0
+    one, db = torch.ones(1, 16, dtype=t, device="cuda"), torch.empty(16, dtype=torch.float32, device="cuda")
+    pg.linear_backward(one, X0, eye, Z=Z, act=act, dbias=db)
+    s = db.double().cpu()
+    want = (z > 0).double() if act != "none" else torch.ones(16, dtype=torch.float64)
+    want[15] = {"none": 1.0, "relu": 0.0}.get(act, 0.5)
+    assert bool(((s - want)[:14].abs() <= 1e-6).all()) and abs(float(s[15] - want[15])) <= 1e-6, s
+    if act not in ("none", "relu"):
+        assert bool(torch.isnan(s[14]))
 
 
 def d64(t):
