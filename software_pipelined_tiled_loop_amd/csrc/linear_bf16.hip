@@ -5,7 +5,8 @@ namespace pgemm {
 
 static const LinVariant k_table[] = {
     LIN_CLASS(DT_BF16, 256, 256, 64, 2, 2, 2),  // 4 waves of 128 x 128
-    LIN_CLASS(DT_BF16, 128, 128, 64, 2, 2, 2),  // 4 waves of 64 x 64
+    LIN_CLASS(DT_BF16, 128, 128, 64, 2, 2, 2),  // 4 waves of 64 x 64, two workgroups a CU
+    LIN_CLASS(DT_BF16, 128, 128, 64, 4, 2, 2),  // the same, one a CU, its ring as deep as the loads take
     LIN_FEW_CLASSES(DT_BF16),
 };
 

@@ -558,10 +558,11 @@ struct LinCfg {
     typedef Opnd<D, LA_, BM, BK> OA;
     typedef Opnd<D, LB_, BNP, BK> OB;
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
-    // One wave per SIMD, its 128 x 128 accumulators in all 256 AGPRs.
-    static constexpr bool LONE = BM * BN / NW >= 128 * 128;
-    static constexpr int MINW = LONE ? 1 : 2;  // waves per SIMD
-    static_assert(!LONE || ES == 2, "the fp32 MFMAs of one block depend on each other");
+    // 16-bit types: one wave per SIMD and workgroup, its MFMAs placed by hand
+    // (lone_step), its accumulators in AGPRs: all 256 for a wave of 128 x 128.
+    // (fp32: the four MFMAs of a block depend on each other; left to the compiler.)
+    static constexpr bool LONE = ES == 2 && NW == 4;
+    static constexpr int MINW = BM * BN / NW >= 128 * 128 ? 1 : 2;  // waves per SIMD
     static constexpr int WM = BM / WGM, WNP = BNP / WGN;
     static constexpr int FM = WM / 16, FNP = WNP / 16, FN = FNP * NP;
     static constexpr int A_BYTES = OA::BYTES, B_BYTES = OB::BYTES * NP;
@@ -679,26 +680,29 @@ __device__ __forceinline__ void acc_settle() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// One K step of a lone wave.  Nothing else issues on its SIMD, so what stands
-// between two MFMAs has to fit the 16 clocks that the matrix core is busy with
-// the first: one instruction in each place.  With the sixteen LDS-DMA blocks'
-// three instructions in a row in every second place the core was busy 57 % of
-// the time.  Reads of the next fragments go to places 0, 4, 8 ..; with DMA, each
-// block's M0 and load to the two places behind them; without, the producer's
-// way to the next K tile.  (Every third place instead, which leaves the last
-// quarter of the step free, is 2 % slower, 4 % with inputs in no cache.)
+// One K step of a lone wave.  No other wave of its workgroup issues on its SIMD,
+// so what stands between two MFMAs has to fit the 16 clocks that the matrix core
+// is busy with the first: one instruction in each place, or two where a step has
+// only 16.  (With the sixteen LDS-DMA blocks' three instructions in a row in
+// every second place the core was busy 57 % of the time.)  64 MFMAs a step: reads
+// of the next fragments in places 0, 4, 8 ..; with DMA, each block's M0 and load
+// in the two places behind them; without, the producer's way to the next K tile.
+// (Every third place instead, which leaves the last quarter of the step free, is
+// 2 % slower, 4 % with inputs in no cache.)  16 MFMAs: a read and an M0, then a
+// load, in turns.
 template <class C, bool READS, bool DMA, int M = 0>
 __device__ __forceinline__ void lone_step(f32x4 (&acc)[C::FM][C::FN], const LinFrags<C>& use, LinFrags<C>& nxt,
                                           const char PGEMM_LDS* rstage, int rks, LinSrc<C>& src, uint32_t sa,
                                           uint32_t sb, int wm0, int wnp, int lane) {
-    constexpr int NMF = C::FM * C::FN, NR = C::FM + C::FN, Q = M / 4;
-    static_assert(C::LPS <= NMF / 4 && NR <= NMF / 4, "places");
+    constexpr int NMF = C::FM * C::FN, NR = C::FM + C::FN;
+    constexpr int EVERY = NMF >= 64 ? 4 : 2, Q = M / EVERY, SET = EVERY == 4 ? 1 : 0;
+    static_assert(C::LPS <= NMF / EVERY && NR <= NMF / EVERY, "places");
     if constexpr (M < NMF) {
         mfma_lone<C::Dt>(acc[M / C::FN][M % C::FN], use.a[M / C::FN], use.b[M % C::FN]);
-        if constexpr (READS && M % 4 == 0 && Q < NR) lin_read<C>(rstage, rks, Q, wm0, wnp, lane, nxt);
-        if constexpr (DMA && M % 4 == 1 && Q < C::LPS) src.template place<Q>(sa, sb);
-        if constexpr (DMA && M % 4 == 2 && Q < C::LPS) src.template load<Q>();
-        if constexpr (!DMA && M % 4 == 1 && Q < 4) src.template advance<Q>();
+        if constexpr (READS && M % EVERY == 0 && Q < NR) lin_read<C>(rstage, rks, Q, wm0, wnp, lane, nxt);
+        if constexpr (DMA && M % EVERY == SET && Q < C::LPS) src.template place<Q>(sa, sb);
+        if constexpr (DMA && M % EVERY == SET + 1 && Q < C::LPS) src.template load<Q>();
+        if constexpr (!DMA && M % EVERY == 1 && Q < 4) src.template advance<Q>();
         __builtin_amdgcn_sched_barrier(0);
         lone_step<C, READS, DMA, M + 1>(acc, use, nxt, rstage, rks, src, sa, sb, wm0, wnp, lane);
     }

@@ -245,6 +245,7 @@ int main() {
     classes(LIN_CLASS(DT_BF16, 256, 256, 64, 2, 2, 2));
     classes(LIN_CLASS(DT_F32, 256, 256, 32, 2, 2, 4));
     classes(LIN_CLASS(DT_BF16, 128, 128, 64, 2, 2, 2));
+    classes(LIN_CLASS(DT_BF16, 128, 128, 64, 4, 2, 2));
     classes(LIN_CLASS(DT_F32, 128, 128, 32, 2, 2, 2));
     classes(LIN_FEW_CLASSES(DT_BF16));
     classes(LIN_FEW_CLASSES(DT_F32));

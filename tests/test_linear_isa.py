@@ -73,9 +73,9 @@ def test_no_hazard_around_the_lone_mfmas(unit, tmp_path):
     if not os.path.exists(hipcc):
         pytest.skip("hipcc not available")
     with open(os.path.join(build.CSRC, unit)) as f:
-        tile = re.search(r"LIN_CLASS\(DT_\w+, 256, 256, [^)]*\)", f.read())
+        tiles = re.findall(r"LIN_CLASS\(DT_\w+, [^)]*\)", f.read())
     src, out = tmp_path / "tile.hip", str(tmp_path / "tile.s")
-    src.write_text('#include "linear_variants.hpp"\nnamespace pgemm { LinVariant tile[] = {%s}; }\n' % tile[0])
+    src.write_text('#include "linear_variants.hpp"\nnamespace pgemm { LinVariant tile[] = {%s}; }\n' % ", ".join(tiles))
     subprocess.run([hipcc] + build.HIPCC_FLAGS + ["-I" + build.CSRC, "--cuda-device-only", "-S", str(src), "-o", out],
                    check=True, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     with open(out) as f:
@@ -87,4 +87,4 @@ def test_no_hazard_around_the_lone_mfmas(unit, tmp_path):
         found, count = scan([ln for ln in lines if ln and not ln.startswith(".")])
         assert not found, (name, found[:3])
         kernels += count > 0
-    assert kernels == 5  # the tile in every layout
+    assert kernels == 5 * len(tiles)  # each tile in every layout
