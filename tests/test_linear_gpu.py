@@ -271,6 +271,28 @@ def test_large_tiles(pg, on_gpu, dtype, order, i):
     m.check_frames()
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("M", [8200, 8250])
+def test_gradients_of_many_rows(pg, on_gpu, dtype, M):
+    """Sizes where a workgroup of the slope kernel takes two steps of rows, the last one or both cut."""
+    N, K, t = 1004, 24, TYPES[dtype]
+    for act in ref.ACTS:
+        say("many rows", dtype, M, act)
+        m = Maker(700, t, 1, 1)
+        dY, X, G, U = m.rows(M, N), m.rows(M, K), m.rows(M, N), m.rows(M, N)
+        Wg, Wu = m.weight(K, N, "kn"), m.weight(K, N, "kn")
+        dX, dW, db = m.out(M, K), m.weight_out(K, N, "kn"), m.vector_out(N)
+        pg.linear_backward(dY, X, Wg, Z=G, act=act, dX=dX, dW=dW, dbias=db)
+        for name, got, want in zip(("dX", "dW", "db"), (dX, dW, db), ref.linear_backward(dY, X, Wg, G, act, t)):
+            ref.check(name, got, want)
+        dWu, dbu = m.weight_out(K, N, "kn"), m.vector_out(N)
+        pg.gated_backward(dY, X, Wg, Wu, G, U, act=act, dX=dX, dWg=dW, dWu=dWu, dbias_g=db, dbias_u=dbu)
+        for name, got, want in zip(("dX", "dWg", "dWu", "dbg", "dbu"), (dX, dW, dWu, db, dbu),
+                                   ref.gated_backward(dY, X, Wg, Wu, G, U, act, t)):
+            ref.check(name, got, want)
+        m.check_frames()
+
+
 #       M   N      K     few rows: every width of tile, with and without splits, cut K tiles
 FEW = [(1, 4096, 2048), (1, 16384, 520), (3, 33000, 264), (20, 4104, 1000), (40, 4100, 777), (64, 1030, 4001), (17, 300, 9000),
        (33, 8190, 1500)]
