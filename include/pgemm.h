@@ -23,7 +23,8 @@
  *     integers in int32 range; sums, products and the result wrap modulo 2^32,
  *     with no saturation, so C is the exact result reduced to int32).
  *   - Pointers A, B, C are device pointers owned by the caller.  The library
- *     allocates nothing and keeps no state besides constant tables.
+ *     allocates nothing and keeps no state besides constant tables (and, per
+ *     thread, the plans of recent sizes, which depend on nothing else).
  *   - beta == 0: C is written without being read (NaN/Inf in C do not
  *     propagate).  K == 0: C = beta*C.  M == 0 or N == 0: nothing happens.
  *   - C must not overlap A or B.
@@ -443,8 +444,8 @@ int pgemm_diag_parts(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
  * initialisation; two calls that may run at the same time need one each.
  * Calls enqueue one or more kernels on `stream`, allocate nothing and can be
  * captured in a graph.  Outputs may not overlap inputs, the workspace or each
- * other.  Empty sizes are served: M or N zero computes nothing forward, and
- * gradients over no rows or columns are zeros.
+ * other, except that R may be Y itself.  Empty sizes are served: M or N zero
+ * computes nothing forward, and gradients over no rows or columns are zeros.
  *
  * Errors: UNSUPPORTED_DTYPE; INVALID_ARG (a negative size, a leading dimension
  * too small, a missing or misaligned pointer, an unknown order, activation or

@@ -420,6 +420,8 @@ class _Call:
         for i, bi, j, bj in self.pairs:
             if p[i] < p[j] + bj and p[j] < p[i] + bi:
                 self._overlap(ts, i, j, same)
+        if stream is not None and getattr(stream, "device", self.device) != self.device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, self.device))
         index = self.index
         if self.device.type != "cuda":
             raise ValueError("the tensors must be on a GPU, got %s" % self.device)
@@ -499,6 +501,12 @@ def _act_code(act):
         raise ValueError("unknown activation %r: one of %s" % (act, ", ".join(ACT))) from None
 
 
+def _required(**ts):
+    for name, t in ts.items():
+        if t is None:
+            raise ValueError("%s is needed" % name)
+
+
 def _sizes(X, W, name="W"):
     if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[0]:
         raise ValueError("X is %s and %s is %s: M x K and K x N are needed" % (tuple(X.shape), name, tuple(W.shape)))
@@ -529,6 +537,7 @@ def linear(X, W, Y, bias=None, residual=None, act="none", Z=None, workspace=None
 
 
 def _describe_linear(X, W, Y, bias, residual, Z, act):
+    _required(X=X, W=W, Y=Y)
     M, N, K = _sizes(X, W)
     c = _Call(X)
     t, own = c.dtype, _OWN_TYPE[c.dtype]
@@ -557,6 +566,7 @@ def gated(X, Wg, Wu, H, bias_g=None, bias_u=None, act="silu", G=None, U=None, wo
 
 
 def _describe_gated(X, Wg, Wu, H, bias_g, bias_u, G, U, act):
+    _required(X=X, Wg=Wg, Wu=Wu, H=H)
     M, N, K = _sizes(X, Wg, "Wg")
     c = _Call(X)
     t, own = c.dtype, _OWN_TYPE[c.dtype]
@@ -603,6 +613,7 @@ def linear_backward(dY, X, W, Z=None, act="none", dX=None, dW=None, dbias=None, 
 
 
 def _describe_linear_backward(dY, X, W, Z, dX, dW, dbias, act):
+    _required(dY=dY, X=X, W=W)
     M, N, K = _sizes(X, W)
     c = _Call(X)
     t, own = c.dtype, _OWN_TYPE[c.dtype]
@@ -639,6 +650,7 @@ def gated_backward(dH, X, Wg, Wu, G, U, act="silu", dX=None, dWg=None, dWu=None,
 
 
 def _describe_gated_backward(dH, X, Wg, Wu, G, U, dX, dWg, dWu, dbias_g, dbias_u, act):
+    _required(dH=dH, X=X, Wg=Wg, Wu=Wu, G=G, U=U)
     M, N, K = _sizes(X, Wg, "Wg")
     c = _Call(X)
     t, own = c.dtype, _OWN_TYPE[c.dtype]

@@ -93,8 +93,8 @@ constexpr int lin_lb(int lay) { return lay == LIN_KK ? LAY_K : LAY_X; }
 // 128 KiB a workgroup: measured on one token to 16384 x 4096 gated, two
 // workgroups a CU with short rings stream faster (5.0 TB/s) than one with all
 // of the CU's LDS (4.2 TB/s).  Sixteen columns a tile (W [N][K] only, where they
-// are whole rows) give 256 workgroups at N = 4096 without splitting K: 9.5 us
-// for one token by 4096 x 4096, 12.6 us on 64 columns in four splits.
+// are whole rows) give 256 workgroups at N = 4096 without splitting K: 8.2 us
+// for one token by 4096 x 4096, 11.9 us on 64 columns in four splits.
 #define LIN_FEW_CLASSES(D)                                                                                    \
     LIN_FEW(D, LIN_KK, 0, 1, 16, 8, 3), LIN_FEW(D, LIN_KK, 0, 2, 16, 4, 4), LIN_FEW(D, LIN_KK, 0, 4, 16, 4, 3), \
         LIN_FEW(D, LIN_KK, 0, 1, 64, 4, 2), LIN_FEW(D, LIN_KK, 0, 2, 64, 4, 2),                               \

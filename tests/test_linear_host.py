@@ -191,3 +191,24 @@ def test_wrapper_takes_degenerate_strides():
             lib.linear(e(4, K), W, e(4, N))
     with pytest.raises(ValueError, match="GPU"):
         lib.linear(e(8, 4).t()[:, :1], e(1, 6), e(4, 6))
+
+
+@pytest.mark.parametrize("name,call", [
+    ("Y", lambda: lib.linear(e(4, 8), e(8, 16), None)),
+    ("W", lambda: lib.linear(e(4, 8), None, e(4, 16))),
+    ("H", lambda: lib.gated(e(4, 8), e(8, 16), e(8, 16), None)),
+    ("Wu", lambda: lib.gated(e(4, 8), e(8, 16), None, e(4, 16))),
+    ("dY", lambda: lib.linear_backward(None, e(4, 8), e(8, 16), dX=e(4, 8))),
+    ("U", lambda: lib.gated_backward(e(4, 16), e(4, 8), e(8, 16), e(8, 16), e(4, 16), None, dX=e(4, 8))),
+])
+def test_wrapper_refuses_missing_tensors(name, call):
+    with pytest.raises(ValueError, match="^%s is needed" % name):
+        call()
+
+
+def test_wrapper_refuses_a_stream_of_another_device():
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        lib.linear(e(4, 8), e(8, 16), e(4, 16), stream=Stream())
