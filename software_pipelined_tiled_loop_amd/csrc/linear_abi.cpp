@@ -64,63 +64,52 @@ struct Plan {
     int np8;
 };
 
-// Estimated microseconds of a product with its K tiles split in `splits`, from
-// rates and fixed costs measured on calls back to back (see the notes beside
-// the variants).
+// Estimated microseconds of a product with its K tiles split in `splits`.  The
+// rates and fixed costs are fitted to choose well, on 2000 products of 1 to 8192
+// rows in all layouts and types, each timed on every variant in 1 to 32 splits:
+// the choice takes 1.5 % longer than the best (mean of random sizes), 2.0 % for
+// multiples of 1024, 3.3 % for weights beyond the shared cache.
 //
 // Tiles: the workgroups run in rounds, one or two (128 x 128 with two stages) a
-// CU at a time.  Whole-part rates in TFLOP/s, bf16: 256 x 256 1640; 128 x 128
-// with four stages 1280, with two 955 alone and 1290 where two share a CU
-// (1024 x 4096 x 4096, 256 workgroups: 35 us with four stages, 44 with two; 512
-// workgroups: 70 and 61).
+// CU at a time.  Rates of the whole part in TFLOP/s and us a round, 16-bit
+// types: 256 x 256 1560, 17; 128 x 128 with four stages 820, 6.5, with two 450
+// alone and 763 where two share a CU, 3.4 (1024 x 4096 x 4096, 256 workgroups:
+// 35 us with four stages, 44 with two; 2048 x 4096 x 4096: 70 and 61).
 double est_tiles(const LinVariant& v, const Shape& p, bool f32, int64_t wgs, double kt) {
     const bool large = v.bm == 256, one = v.per_cu == 1;
-    const double alone = (large ? (f32 ? 148e6 : 1640e6) : f32 ? 130e6 : one ? 1280e6 : 955e6) / kNumCU;
-    const double shared = one ? alone : (f32 ? 140e6 : 1290e6) / kNumCU;
+    const double alone = (large ? (f32 ? 159e6 : 1560e6) : f32 ? 138e6 : one ? 820e6 : 450e6) / kNumCU;
+    const double shared = one ? alone : (f32 ? 147e6 : 763e6) / kNumCU;
     const double flop = 2.0 * v.bm * v.bn * v.bk * kt * (p.gated ? 2 : 1);
     const int64_t slots = one ? kNumCU : 2 * kNumCU;
     const int64_t rounds = wgs / slots, rest = wgs % slots;
-    const double round_us = (one ? 1 : 2) * flop / shared, fixed = large ? 12.0 : 6.0;
+    const double round_us = (one ? 1 : 2) * flop / shared, fixed = large ? 17.0 : one ? 6.5 : 3.4;
     double us = rounds * (round_us + fixed);
     if (rest > kNumCU) us += round_us + fixed;
     else if (rest > 0) us += flop / alone + fixed;
-    const double bytes = (double)p.K * p.halves * (f32 ? 4 : 2) * (p.rows + p.cols * (p.gated ? 2.0 : 1.0));
-    const double mem = bytes / 4.9e6 + fixed;
-    return (us > mem ? us : mem) + 2.0;
+    return us;
 }
-// Few rows: a CU streams up to 35 bytes/ns (one token by 4096 x 4096 on 64
-// workgroups: 15.9 us; 1024^3 on 256: 9.9), the inputs arrive at 4.9 TB/s, and
-// each round of workgroups costs 2.5 us.
+// Few rows: the CU with the most workgroups streams 44 bytes/ns or multiplies at
+// 0.87 (fp32: 0.42) TFLOP/s, and each round of workgroups costs 3 us.  W [K][N]
+// in less than 128 bytes of a row at a time streams slower (one token gated to
+// 6144 x 6144, 51.7 us on 32 columns of each weight, 39.1 on 64 in two splits).
 double est_few(const LinVariant& v, const Shape& p, bool f32, int64_t wgs, double kt) {
     const double cols = v.bn * (p.gated ? 2 : 1), es = f32 ? 4 : 2;
     const double kb = kt * v.bk * ((p.rows < v.bm ? p.rows : v.bm) + cols) * es / 1e3;
-    const double load = wgs > kNumCU ? (double)wgs / kNumCU : 1.0;
-    const double bytes = (double)p.K * p.halves * es * (p.rows + p.cols * (p.gated ? 2.0 : 1.0));
-    const double stream = load * kb / 35.0, mfma = load * 2.0 * v.bm * cols * v.bk * kt / (f32 ? 0.33e6 : 2.5e6);
-    double us = bytes / 4.9e6;
-    us = us > stream ? us : stream;
-    us = us > mfma ? us : mfma;
-    return 2.5 * ceil_div(wgs, (int64_t)kNumCU * v.per_cu) + us;
-}
-// Splits of a few-rows product.  Below one workgroup a CU, splitting K up to
-// that fills the CUs (one token by 4096 x 4096 on 64 columns: 15.9 / 13.6 /
-// 11.9 / 12.6 us in 1 / 2 / 4 / 8).  Beyond, it does not pay (16 rows, K =
-// 16384: 32.1 us in 4, 36.0 in 8) but for the gated block with W [N][K], where
-// shorter streams are faster (one token to 16384 x 4096: 61.9 / 66.9 / 52.4 /
-// 55.1 us in 1 / 2 / 4 / 8 with 64 columns a workgroup, 61.5 / 63.1 / 53.7 /
-// 60.9 with 32; W [K][N]: 59.7 / 61.1 / 60.5 in 1 / 2 / 4).
-int64_t few_splits(const LinVariant& v, const Shape& p, int64_t tiles, int64_t kt) {
-    int64_t s = tiles < kNumCU ? kNumCU / tiles : p.gated && p.lay == LIN_KK ? 4 : 1;
-    if (s > kt / v.few) s = kt / v.few;  // a K tile for each wave
-    return s < 1 ? 1 : s > 32 ? 32 : s;
+    const double load = (double)ceil_div(wgs, kNumCU);
+    const double thin = v.lay == LIN_KX && v.bn * es < 128 ? 1.3 : 1.0;
+    const double stream = thin * load * kb / 44.0, mfma = load * 2.0 * v.bm * cols * v.bk * kt / (f32 ? 0.42e6 : 0.87e6);
+    return 3.0 * ceil_div(wgs, (int64_t)kNumCU * v.per_cu) + (stream > mfma ? stream : mfma);
 }
 double est_us(const LinVariant& v, const Shape& p, int dtype, int64_t splits) {
     const bool f32 = dtype == PGEMM_F32;
     const int64_t wgs = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs * splits;
     const double kt = (double)ceil_div(ceil_div(p.K, v.bk) * p.halves, splits);
     double us = v.few ? est_few(v, p, f32, wgs, kt) : est_tiles(v, p, f32, wgs, kt);
+    // inputs from the caches and memory: no variant is faster
+    const double mem = (double)p.K * p.halves * (f32 ? 4 : 2) * (p.rows + p.cols * (p.gated ? 2.0 : 1.0)) / 16e6;
+    if (us < mem) us = mem;
     // the join: a launch, and the partial sums written and read
-    if (splits > 1) us += 4.5 + 2.0 * splits * p.rows * p.cols * (p.gated ? 2 : p.outs) * 4.0 / 4e6;
+    if (splits > 1) us += 5.0 + 0.29 * splits + 2.0 * splits * p.rows * p.cols * (p.gated ? 2 : p.outs) * 4.0 / 4.4e6;
     return us;
 }
 
@@ -135,15 +124,11 @@ Plan search_plan(const Shape& p, int dtype) {
         if (v.lay != p.lay || v.gated != p.gated) continue;
         const int64_t kt = ceil_div(p.K, v.bk) * p.halves;
         const int64_t tiles = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs;
-        // Up to 64 rows the few-rows kernels are as fast as a tile of 128 at its
-        // best splits or faster (16 rows, K = 16384: 32.1 and 32.5 us; 64 rows by
-        // 4096 x 4096: 16.2 and 17.4).
-        if (!v.few && p.rows <= 64 && p.lay != LIN_XX) continue;
+        if (v.bm == 256 && (p.rows <= 64 || p.cols <= 64)) continue;
         if (tiles > 0x1fffff00) continue;  // with their splits, more workgroups than a grid holds
-        const int64_t few = v.few ? few_splits(v, p, tiles, kt) : 0;
-        const bool must = few > 1 && tiles >= kNumCU;  // the gated block's many workgroups
         for (int64_t s = 1; s <= 32; ++s) {
-            if (v.few ? s != few && (s > 1 || must) : s > 1 && (s * 4 > kt || tiles * s > 2 * kNumCU)) continue;
+            // K tiles for each wave, and not more workgroups than splitting is for
+            if (s > 1 && (s * (v.few ? v.few : 4) > kt || tiles * s > (v.few ? 8 : 2) * kNumCU)) break;
             const double us = est_us(v, p, dtype, s);
             if (best.v && us >= best_us) continue;
             best_us = us;
