@@ -1029,8 +1029,8 @@ __global__ void __launch_bounds__(C::NT, C::MINW) linear_kernel(LinArgs g) {
 // order of the waves.
 // Measured, bf16 weights from memory: one token by 4096 x 4096 8.2 us (4.1 TB/s,
 // of which 2 us are the launch and the first loads), 16 by 4096 x 16384 28.6 us
-// (4.7 TB/s) and 4.6 for the join, one token gated to 16384 x 4096 48.3 us (5.6
-// TB/s) and 4.8 for the join; a large copy moves 4.9 TB/s.
+// (4.7 TB/s) and 4.6 for the join, one token gated to 16384 x 4096 50.5 us (5.3
+// TB/s); a large copy moves 4.9 TB/s.
 template <int D, int LA_, int LB_, int FM_, int NCOL_, int NW_, int S_, bool GATED_>
 struct FewCfg {
     static constexpr int Dt = D, FM = FM_, NCOL = NCOL_, NW = NW_, S = S_;
@@ -1121,10 +1121,20 @@ __global__ void __launch_bounds__(C::NT) linear_few(LinArgs g) {
     // This split's K tiles [t0, t1); the wave's are t0 + wave, + NW, ...
     const int64_t total = (int64_t)g.nfull * g.halves;
     const int t0 = (int)(total * split / g.splits), t1 = (int)(total * (split + 1) / g.splits);
+    // Tiles of 64 rows of W [N][K] with the whole contraction begin at one of
+    // eight places of it, and come round: workgroups in step read rows a power of
+    // two apart at the same offset (one token to 16384 x 4096 31.3 -> 28.2 us, gated
+    // 60 -> 52, to 32768 x 8192 110 -> 100; gated to 14336 x 4096 48.3 -> 48.5).  Not
+    // narrower tiles (gated to 8192 x 4096 28 -> 32, 4096 x 4096 8.9 -> 9.3) or
+    // W [K][N] (9460 x 6427 gated 62 -> 74).
+    const int turn = C::NCOLP == 64 && C::OB::along_k && g.splits == 1 && g.halves == 1
+                         ? (int)((int64_t)(t1 - t0) * (tn & 7) >> 3) : 0;
     // Loads K tile t into stage st; past the last one every lane reads zeros.
     const auto issue = [&](int t, int st) {
-        const int h = t >= g.nfull ? 1 : 0, kt = t - h * g.nfull;
         const int range = t < t1 ? (int)0x80000000u : 0;
+        t += turn;  // comes round
+        if (t >= t1) t -= t1 - t0;
+        const int h = t >= g.nfull ? 1 : 0, kt = t - h * g.nfull;
         const uint32_t at = lds0 + (uint32_t)(st * C::STAGE);
         i32x4 r = make_rsrc_sgpr((h ? a_half[1] : a_half[0]) + sa * kt);
         r[2] = range;
