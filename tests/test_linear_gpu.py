@@ -588,3 +588,43 @@ def test_long_leading_dimensions(pg):
     pg.linear_backward(dY, X, W, Z=Y, act="gelu", dX=dX, dW=dW, dbias=db)
     for name, got, want in zip(("dX", "dW", "db"), (dX, dW, db), ref.linear_backward(dY, X, W, Y, "gelu", t)):
         ref.check(name, got, want)
+
+
+def test_offsets_beyond_32_bits(pg):
+    """Outputs and weights of more than 2^31 elements: small integers, so every sum is exact."""
+    big, other, step, t = 70000, 33000, 5000, torch.bfloat16
+
+    def whole(*shape):
+        return torch.randint(-2, 3, shape, dtype=torch.int8, device="cuda").to(t)
+
+    # a large output: Y[big][other], and dW in the other direction
+    X, W = whole(big, 16), whole(16, other)
+    Y = torch.full((big, other), SENTINEL, dtype=torch.float32, device="cuda")
+    say("large output")
+    pg.linear(X, W, Y)
+    for r in range(0, big, step):
+        assert torch.equal(Y[r:r + step].double(), X[r:r + step].double() @ W.double()), r
+    dW, A = Y.fill_(SENTINEL), X.t().contiguous()  # dW = A^T dY
+    say("large weight gradient")
+    pg.linear_backward(W, A, torch.empty(big, other, dtype=t, device="cuda"), dW=dW)
+    for r in range(0, big, step):
+        assert torch.equal(dW[r:r + step].double(), X[r:r + step].double() @ W.double()), r
+    del Y, dW
+
+    # a large weight, each storage order, forward (few rows) and as operand of dX
+    B = whole(big, other)
+    for M in (2, 200):
+        x, dy = whole(M, other), whole(M, big)
+        y, dx = torch.empty(M, big, dtype=torch.float32, device="cuda"), torch.empty(M, other, dtype=t, device="cuda")
+        want = torch.cat([x.double() @ B[r:r + step].double().t() for r in range(0, big, step)], 1)
+        say("large weight", M)
+        pg.linear(x, B.t(), y)  # W[N][K]
+        assert torch.equal(y.double(), want)
+        wantx = sum(dy[:, r:r + step].double() @ B[r:r + step].double() for r in range(0, big, step))
+        pg.linear_backward(dy, x, B.t(), dX=dx)
+        assert torch.equal(dx, wantx.float().to(t))
+        y2, dx2 = torch.empty(M, other, dtype=torch.float32, device="cuda"), torch.empty(M, big, dtype=t, device="cuda")
+        pg.linear(dy, B, y2)  # W[K][N]
+        assert torch.equal(y2.double(), wantx)
+        pg.linear_backward(x, dy, B, dX=dx2)
+        assert torch.equal(dx2, want.float().to(t))
