@@ -554,10 +554,10 @@ struct Epi {
 // Measured, calls back to back on the same inputs:
 //   256 x 256, bf16 4096^3           96.7 us W [N][K], 97.5 W [K][N], dW 97.7
 //                                    (1421 TFLOP/s; eight waves of 128 x 64 101.8)
-//   the same, inputs in no cache     104 us; bias, gelu_tanh, residual 111
-//   gated, 4096 x 8192 x 4096        401 to 413 us with G and U kept (1350 TFLOP/s)
-//   128 x 128 four stages, bf16      1024 x 4096 x 4096 35 us (982 TFLOP/s)
-//   128 x 128 two stages, bf16       512 tiles of K = 4096 61 us
+//   the same, inputs in no cache     99 to 104 us; bias, gelu_tanh, residual 111
+//   gated, 4096 x 8192 x 4096        402 to 413 us with G and U kept (1350 TFLOP/s)
+//   128 x 128 four stages, bf16      1024 x 4096 x 4096 33 us (1040 TFLOP/s)
+//   128 x 128 two stages, bf16       2048 x 4096 x 4096 57 us (1200 TFLOP/s)
 // A tile's fixed cost (first loads, epilogue) is 17 us of a 256 x 256 tile of
 // K = 64; a second workgroup on the CU would hide it, but the accumulators and
 // the ring fill the CU.
@@ -1280,7 +1280,7 @@ __global__ void __launch_bounds__(kJoinCols / 8) linear_join(LinArgs g) {
 // (bias gradients) add the unrounded values.
 //
 // Bound by memory: bf16 reads and writes of 2048 x 8192 gated (168 MB) take
-// 33.5 us, 5.0 TB/s; of 4096 x 4096 (101 MB) 25.7 us, 3.9 TB/s.  256-byte
+// 33.5 us, 5.0 TB/s; of 4096 x 4096 (101 MB) 21.5 to 25.7 us, 4.3 TB/s.  256-byte
 // stretches of a row and two rows under way a thread: stretches of 512 bytes
 // take 22.7 us for the latter but 37 for the former, four rows under way 52.
 struct SlopeArgs {
