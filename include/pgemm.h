@@ -435,7 +435,12 @@ int pgemm_diag_parts(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
  *
  * In the backward passes dZ (dG, dU) is rounded to the operand type before it
  * is multiplied (not where act is none: dZ is dY); the bias gradients sum
- * the unrounded values in fp32.  Nothing depends on the order in which
+ * the unrounded values in fp32.  For fp16, whose range products of fp16 values
+ * leave at both ends, the rounded values are held divided by a power of two for
+ * each row (in dX; of dG and dU together) and each column (in dW), which the fp32
+ * sums are multiplied by: an entry is off by half a step of fp16's 11 bits, or by
+ * 2^-39 of the largest finite entry of its row (column) where that is more.
+ * Nothing depends on the order in which
  * workgroups run: repeated calls give the same bits.
  *
  * Each call takes a workspace: device memory, 16-byte aligned, of at least

@@ -603,7 +603,8 @@ def linear_backward(dY, X, W, Z=None, act="none", dX=None, dW=None, dbias=None, 
     dbias have X's type or float32.  What is None is not computed.  Z is the
     pre-activation that linear wrote (not needed for act "none"); the
     residual's gradient is dY itself.  dZ is rounded to X's type before the two
-    products; dbias sums it unrounded.  Streams, workspace
+    products (float16: scaled by rows and columns, so that it neither overflows nor
+    vanishes there); dbias sums it unrounded.  Streams, workspace
     (pgemm_linear_backward_workspace) and errors as for linear.
     Returns (dX, dW, dbias).
     """

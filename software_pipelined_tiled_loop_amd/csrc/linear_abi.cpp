@@ -20,6 +20,7 @@ namespace {
 constexpr int64_t kMaxDim = 0x7fffff00;
 constexpr int64_t kMaxLd = (int64_t)1 << 21;  // 256 rows of 4-byte elements stay below 2^31 bytes
 constexpr int kNumCU = 256;
+constexpr int64_t kMaxSumGroups = 16384;  // workgroups of linear_colsum, which goes on from there by itself
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -252,11 +253,17 @@ Shape dw_shape(int64_t M, int64_t N, int64_t K, int order, int outs) {
 }
 int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
 
-// Workspace of a backward pass: gradients at the pre-activations, the row
+// Workspace of a backward pass: gradients at the pre-activations (fp16: in two
+// copies, with the largest entries and factors of rows and columns), the row
 // blocks' column sums, the splits' sums (of dX, then of dW).
 struct Backward {
-    int64_t ldd, np8, steps, blocks, dz_bytes, sum_bytes, split_bytes;
-    int64_t total(int planes, bool keeps) const { return (keeps ? planes * dz_bytes : 0) + sum_bytes + split_bytes; }
+    int64_t ldd, np8, steps, blocks, strips;
+    int64_t dz_bytes;                // of one plane of one copy
+    int64_t copies;
+    int64_t row_max, col_max, rows, cols, scale_bytes;  // fp16: offsets behind the copies, and the bytes of all
+    int64_t sum_bytes, split_bytes;
+    int64_t kept(int planes) const { return planes * copies * dz_bytes + scale_bytes; }
+    int64_t total(int planes, bool keeps) const { return (keeps ? kept(planes) : 0) + sum_bytes + split_bytes; }
 };
 Backward backward_layout(int64_t M, int64_t N, int64_t K, int dtype, int planes) {
     Backward b;
@@ -267,7 +274,21 @@ Backward backward_layout(int64_t M, int64_t N, int64_t K, int dtype, int planes)
     // 256 workgroups in two steps: 12 us in one, 17 in two).
     b.steps = ceil_div(M, 2 * kSlopeRows) * ceil_div(N, kSlopeCols) >= 4 * kNumCU ? 2 : 1;
     b.blocks = ceil_div(M, b.steps * kSlopeRows);
+    b.strips = ceil_div(N, kSlopeCols);
     b.dz_bytes = M * b.ldd * elem_size(dtype);  // a multiple of 128
+    b.copies = dtype == PGEMM_F16 ? 2 : 1;
+    b.scale_bytes = 0;
+    if (dtype == PGEMM_F16) {
+        const auto take = [&](int64_t floats) {
+            const int64_t at = b.scale_bytes;
+            b.scale_bytes += round_up(floats * 4, 256);
+            return at;
+        };
+        b.row_max = take(b.strips * M);
+        b.col_max = take(b.blocks * planes * b.np8);
+        b.rows = take(M);
+        b.cols = take(planes * b.np8);
+    }
     b.sum_bytes = round_up(b.blocks * planes * b.np8 * 4, 256);
     b.split_bytes = 0;
     for (int order = 0; order < 2; ++order) {
@@ -290,62 +311,92 @@ int run_backward(int64_t M, int64_t N, int64_t K, const Grad& q, int w_order, in
     const LinKernels k = kernels_for(dtype);
     const Backward b = backward_layout(M, N, K, dtype, planes);
     const bool gated = planes == 2, keeps = gated || act != PGEMM_ACT_NONE;
+    const bool products = q.dX || q.dW[0], bias = q.db[0] || q.db[1];
+    // What stands in the workspace for dZ (dG, dU) as operand of dX and of dW.
+    const bool stored = keeps && products && M > 0 && N > 0, scaled = stored && dtype == PGEMM_F16;
     char* ws = (char*)workspace;
-    void* dz[2] = {ws, ws ? ws + b.dz_bytes : nullptr};
-    char* rest = ws ? ws + (keeps ? planes * b.dz_bytes : 0) : nullptr;
+    const auto plane = [&](int64_t i) -> void* { return ws ? ws + i * b.dz_bytes : nullptr; };
+    char* scales = ws ? ws + planes * b.copies * b.dz_bytes : nullptr;
+    char* rest = ws ? ws + (keeps ? b.kept(planes) : 0) : nullptr;
     float* sums = (float*)rest;
     void* part = rest ? rest + b.sum_bytes : nullptr;
-    const bool products = q.dX || q.dW[0], bias = q.db[0] || q.db[1];
-    if (N == 0) {
-        // no column: dX is all zeros (a product over nothing), the rest is empty
-    } else if (M > 0 && ((keeps && products) || bias)) {
-        SlopeArgs s;
-        std::memset(&s, 0, sizeof(s));
-        s.dY = q.dY;
-        s.ldy = q.lddy;
-        s.Z = q.Z;
-        s.ldz = q.ldz;
-        s.U = q.U;
-        s.ldu = q.ldu;
-        s.dZ = keeps && products ? dz[0] : nullptr;
-        s.dU = gated && products ? dz[1] : nullptr;
-        s.ldd = b.ldd;
-        s.sums = bias ? sums : nullptr;
-        s.np8 = (int)b.np8;
-        s.steps = (int)b.steps;
-        s.M = (int)M;
-        s.N = (int)N;
-        s.act = act_args(act);
-        const hipError_t e = k.slope(s, gated, (int)(ceil_div(N, kSlopeCols) * b.blocks), stream);
-        if (e != hipSuccess) return hip_failed("linear_slope", e);
+    const float* row_factors = scaled ? (const float*)(scales + b.rows) : nullptr;
+    const float* col_factors = scaled ? (const float*)(scales + b.cols) : nullptr;
+    SlopeArgs s;
+    std::memset(&s, 0, sizeof(s));
+    s.dY = q.dY;
+    s.ldy = q.lddy;
+    s.Z = q.Z;
+    s.ldz = q.ldz;
+    s.U = q.U;
+    s.ldu = q.ldu;
+    s.ldd = b.ldd;
+    s.sums = bias ? sums : nullptr;
+    s.np8 = (int)b.np8;
+    s.steps = (int)b.steps;
+    s.M = (int)M;
+    s.N = (int)N;
+    s.act = act_args(act);
+    if (scaled) {
+        s.row_max = (float*)(scales + b.row_max);
+        s.col_max = (float*)(scales + b.col_max);
+    } else if (stored) {
+        for (int p = 0; p < planes; ++p) s.dZ[p] = plane(p);
     }
-    if (bias && N > 0) {
-        SumArgs s;
-        std::memset(&s, 0, sizeof(s));
-        s.sums = sums;
-        s.out[0] = q.db[0];
-        s.out[1] = q.db[1];
-        s.blocks = (int)b.blocks;
-        s.planes = planes;
-        s.np8 = (int)b.np8;
-        s.N = (int)N;
-        s.out_f32 = grad_dtype == PGEMM_F32;
-        const hipError_t e = k.colsum(s, (int)ceil_div(N, 64), stream);
+    const auto slope = [&](int pass) {
+        const hipError_t e = k.slope(s, gated, pass, (int)(b.strips * b.blocks), stream);
+        return e == hipSuccess ? (int)PGEMM_OK : hip_failed("linear_slope", e);
+    };
+    // no column: dX is all zeros (a product over nothing), the rest is empty
+    if (M > 0 && N > 0 && (stored || bias)) PGEMM_TRY(slope(dtype == PGEMM_F16 ? SLOPE_RANGE : SLOPE_PLAIN));
+    if (N > 0 && (bias || scaled)) {
+        SumArgs t;
+        std::memset(&t, 0, sizeof(t));
+        t.sums = sums;
+        t.out[0] = q.db[0];
+        t.out[1] = q.db[1];
+        t.blocks = (int)b.blocks;
+        t.planes = planes;
+        t.np8 = (int)b.np8;
+        t.N = (int)N;
+        t.out_f32 = grad_dtype == PGEMM_F32;
+        if (scaled) {
+            t.row_max = s.row_max;
+            t.col_max = s.col_max;
+            t.rows = (float*)(scales + b.rows);
+            t.cols = (float*)(scales + b.cols);
+            t.M = (int)M;
+            t.strips = (int)b.strips;
+        }
+        const int64_t longest = scaled ? larger(M, b.np8) : N;
+        const int64_t groups = ceil_div(longest, 64);
+        const hipError_t e = k.colsum(t, (int)(groups < kMaxSumGroups ? groups : kMaxSumGroups), stream);
         if (e != hipSuccess) return hip_failed("linear_colsum", e);
     }
-    const void* d[2] = {keeps ? dz[0] : q.dY, gated ? dz[1] : keeps ? dz[0] : q.dY};
+    if (scaled) {
+        s.rows = row_factors;
+        s.cols = col_factors;
+        for (int p = 0; p < planes; ++p) {
+            s.dZ[p] = q.dX ? plane(p) : nullptr;
+            s.dZc[p] = q.dW[0] ? plane(planes + p) : nullptr;
+        }
+        PGEMM_TRY(slope(SLOPE_SCALED));
+    }
+    const void* dx[2] = {keeps ? plane(0) : q.dY, gated ? plane(1) : keeps ? plane(0) : q.dY};
+    const void* dw[2] = {scaled ? plane(planes) : dx[0], scaled ? plane(2 * planes - 1) : dx[1]};
     const int64_t ldd = keeps ? b.ldd : q.lddy;
     if (q.dX) {
         LinArgs a;
         std::memset(&a, 0, sizeof(a));
         for (int h = 0; h < 2; ++h) {
-            a.A[h] = d[h];
+            a.A[h] = dx[h];
             a.B[h] = q.W[h];
         }
         a.lda = ldd;
         a.ldb = q.ldw;
         a.e.Y[0] = a.e.Y[1] = q.dX;
         a.e.ldy = q.lddx;
+        a.e.rows[0] = a.e.rows[1] = row_factors;
         a.e.out_f32 = dtype == PGEMM_F32;
         PGEMM_TRY(run_product(dx_shape(M, N, K, w_order, planes), a, dtype, part, stream));
     }
@@ -353,9 +404,11 @@ int run_backward(int64_t M, int64_t N, int64_t K, const Grad& q, int w_order, in
         LinArgs a;
         std::memset(&a, 0, sizeof(a));
         for (int h = 0; h < 2; ++h) {
-            a.A[h] = dw_order == PGEMM_KN ? q.X : d[h];
-            a.B[h] = dw_order == PGEMM_KN ? d[h] : q.X;
+            a.A[h] = dw_order == PGEMM_KN ? q.X : dw[h];
+            a.B[h] = dw_order == PGEMM_KN ? dw[h] : q.X;
             a.e.Y[h] = q.dW[h];
+            // dZ's columns are dW's columns, or its rows where it lies N x K
+            if (scaled) (dw_order == PGEMM_KN ? a.e.cols : a.e.rows)[h] = col_factors + (gated ? h : 0) * b.np8;
         }
         a.lda = dw_order == PGEMM_KN ? q.ldx : ldd;
         a.ldb = dw_order == PGEMM_KN ? ldd : q.ldx;

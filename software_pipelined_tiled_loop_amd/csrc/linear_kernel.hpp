@@ -68,6 +68,8 @@ struct EpiArgs {
     void* U;              // gated: kept U
     int64_t ldz, ldu;
     const void* bias[2];  // operand type; may be null (gated: bg, bu)
+    const float* rows[2]; // fp16 gradients: factor of each row, or column, of output `out`
+    const float* cols[2]; // (see linear_slope); null: none
     ActArgs act;
     int M, N;
     int out_f32;          // Y and R are fp32 (else the operand type)
@@ -417,8 +419,11 @@ template <int D, bool GATED>
 struct Epi {
     typedef typename Elem<D>::type T;
     static constexpr uint32_t TS = sizeof(T);
+    // the operands of fp16 gradients' products are scaled (linear_slope)
+    static constexpr bool SCALED = D == DT_F16 && !GATED;
     const EpiArgs& e;
     __amdgpu_buffer_rsrc_t y, r, z, u;
+    const float *srow, *scol;
     int n0, row, col, rows, cols;
     uint32_t ys, oy, orr, oz, ou;  // bytes of an element of Y; the lane's offsets
 
@@ -429,6 +434,11 @@ struct Epi {
         r = make_rsrc(e.R ? (const char*)e.R + (m0 * e.ldr + n0) * (int64_t)ys : nullptr);
         z = make_rsrc(e.Z ? (char*)e.Z + (m0 * e.ldz + n0) * (int64_t)TS : nullptr);
         u = make_rsrc(e.U ? (char*)e.U + (m0 * e.ldu + n0) * (int64_t)TS : nullptr);
+        srow = scol = nullptr;
+        if constexpr (SCALED) {
+            if (const float* s = out ? e.rows[1] : e.rows[0]) srow = s + m0;
+            if (const float* s = out ? e.cols[1] : e.cols[0]) scol = s + n0;
+        }
         rows = e.M - m0;
         cols = e.N - n0;
         oy = (uint32_t)(row * (int)e.ldy + col) * ys;
@@ -439,7 +449,10 @@ struct Epi {
     // Columns of the group `by` rows on inside the output (8 or more: all).
     __device__ __forceinline__ int valid(int by) const { return row + by < rows ? cols - col : 0; }
     __device__ __forceinline__ bool same() const { return ys == TS; }  // Y has the operand type
+    // A gradient has no bias: its columns' factors take that place.
     __device__ __forceinline__ f32x8 bias(int which) const {
+        if (SCALED && scol)
+            return cols - col < 8 ? zero8() : load8<float>(make_rsrc(scol), (uint32_t)col * 4u);
         if (!e.bias[which] || cols - col < 8) return zero8();
         return load8<T>(make_rsrc((const T*)e.bias[which] + n0), (uint32_t)col * TS);
     }
@@ -484,7 +497,15 @@ struct Epi {
         const auto to = [&](int q, uint32_t lane, int64_t ld, uint32_t size) {
             return (lane + (uint32_t)((by + q * step) * (int)ld) * size) | o[q];
         };
-        if (e.bias[0]) {
+        if (SCALED && srow) {
+            const __amdgpu_buffer_rsrc_t s = make_rsrc(srow);
+#pragma unroll
+            for (int q = 0; q < U; ++q) v[q] *= load1<float>(s, (uint32_t)(row + by + q * step) * 4u | o[q]);
+        }
+        if (SCALED && scol) {
+#pragma unroll
+            for (int q = 0; q < U; ++q) v[q] *= b0;
+        } else if (e.bias[0]) {
 #pragma unroll
             for (int q = 0; q < U; ++q) v[q] += b0;
         }
@@ -526,6 +547,8 @@ struct Epi {
     template <int KIND>
     __device__ __forceinline__ void put1(int by, int x, float v, float w) const {
         const uint32_t bo = (uint32_t)(col + x) * TS, at = (uint32_t)x * ys;
+        if (SCALED && srow) v *= load1<float>(make_rsrc(srow), (uint32_t)(row + by) * 4u);
+        if (SCALED && scol) v *= load1<float>(make_rsrc(scol), (uint32_t)(col + x) * 4u);
         if (e.bias[0]) v += load1<T>(make_rsrc((const T*)e.bias[0] + n0), bo);
         if (e.Z) store1<T>(z, oz + (uint32_t)(by * (int)e.ldz + x) * TS, v);
         v = act1<KIND>(e.act, v);
@@ -1279,18 +1302,38 @@ __global__ void __launch_bounds__(kJoinCols / 8) linear_join(LinArgs g) {
 // type, as X and W do, and the sums over them stay in fp32.  The column sums
 // (bias gradients) add the unrounded values.
 //
+// bf16 has fp32's range.  fp16 has not: dG of fp16 tensors lies anywhere between
+// 2^-48 and 2^33, with dH = U = 300 already beyond its largest value.  So fp16
+// gradients are held divided by powers of two, which the products' epilogues
+// multiply back in fp32: one factor for each row in the copy that dX contracts,
+// one for each column in the copy that dW contracts (a factor has to stand outside
+// the sum).  Each brings the row's (column's) largest finite entry into [2^14,
+// 2^15), so an entry is rounded to fp16's 11 bits down to 2^-29 of that, and off by
+// at most 2^-39 of it below.  That takes two passes, over inputs that the second
+// finds in the shared cache: SLOPE_RANGE (largest entries, and the column sums),
+// linear_colsum (factors), SLOPE_SCALED (the copies).  Where only bias gradients are
+// asked for, fp16 runs SLOPE_RANGE too, so that they have the same bits.
+//
 // Bound by memory: bf16 reads and writes of 2048 x 8192 gated (168 MB) take
 // 33.5 us, 5.0 TB/s; of 4096 x 4096 (101 MB) 21.5 to 25.7 us, 4.3 TB/s.  256-byte
 // stretches of a row and two rows under way a thread: stretches of 512 bytes
 // take 22.7 us for the latter but 37 for the former, four rows under way 52.
+// fp16, 2048 x 8192 gated: 39 and 41 us in the two passes, 5 for the factors (one
+// pass without factors 37); 1000 x 2003 12, 10 and 5 (one pass 12).
+enum SlopePass : int { SLOPE_PLAIN = 0, SLOPE_RANGE = 1, SLOPE_SCALED = 2 };
+
 struct SlopeArgs {
     const void* dY;
     const void* Z;      // linear: Z; gated: G
     const void* U;      // gated
-    void* dZ;           // gated: dG; null: column sums only
-    void* dU;
+    void* dZ[2];        // linear: dZ; gated: dG, dU (scaled: by rows); null: not stored
+    void* dZc[2];       // scaled: by columns
     int64_t ldy, ldz, ldu, ldd;
     float* sums;        // [row block][planes][np8] column sums; null: none
+    float* row_max;     // range: [strip][M] largest entries of the planes; null: none
+    float* col_max;     // range: [row block][planes][np8]; null: none
+    const float* rows;  // scaled: factors [M]
+    const float* cols;  // scaled: factors [planes][np8]
     int np8;
     int steps;          // of kSlopeRows rows a workgroup
     int M, N;
@@ -1311,7 +1354,24 @@ __device__ __forceinline__ f32x8 load_cut8(__amdgpu_buffer_rsrc_t r, uint32_t of
     return v;
 }
 
-template <int D, bool GATED>
+// The factor of a row or column whose largest entry is m >= 0: 2^(floor(log2 m) - 14),
+// from the exponent's bits, and 1 where there is nothing but zeros.  Entries below
+// 2^-95 need no more (the clamp keeps factor and inverse normal).
+__device__ __forceinline__ float scale_of(float m) {
+    const uint32_t ex = __builtin_bit_cast(uint32_t, m) >> 23;
+    return m == 0.0f ? 1.0f : __builtin_bit_cast(float, (ex < 32u ? 18u : ex - 14u) << 23);
+}
+// 1 / s of a power of two.
+__device__ __forceinline__ float inverse(float s) {
+    return __builtin_bit_cast(float, 0x7f000000u - __builtin_bit_cast(uint32_t, s));
+}
+// |x|, or 0 where x is infinite or NaN (those stay what they are under any factor).
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = __builtin_fabsf(x);
+    return a < __builtin_huge_valf() ? a : 0.0f;
+}
+
+template <int D, bool GATED, int PASS>
 __global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
     typedef typename Elem<D>::type T;
     constexpr int planes = GATED ? 2 : 1;
@@ -1325,10 +1385,19 @@ __global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
     const auto at = [&](const void* p, int64_t ld) {
         return make_rsrc(p ? (const char*)p + (m0 * ld + n0) * (int64_t)sizeof(T) : nullptr);
     };
-    const __amdgpu_buffer_rsrc_t ry = at(g.dY, g.ldy), rz = at(g.Z, g.ldz), ru = at(g.U, g.ldu), rd = at(g.dZ, g.ldd),
-                                 re = at(g.dU, g.ldd);
-    f32x8 s0 = zero8(), s1 = s0;
-    if (valid > 0) {
+    const __amdgpu_buffer_rsrc_t ry = at(g.dY, g.ldy), rz = at(g.Z, g.ldz), ru = at(g.U, g.ldu);
+    f32x8 s[planes], most[planes], down[planes];  // column sums, largest entries; 1 / the columns' factors
+#pragma unroll
+    for (int p = 0; p < planes; ++p) {
+        s[p] = most[p] = zero8();
+        if constexpr (PASS == SLOPE_SCALED) {
+            if (valid <= 0) continue;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) down[p][x] = inverse(g.cols[(int64_t)p * g.np8 + n0 + col + x]);
+        }
+    }
+    // the lanes of a row find its largest entry together: all of them take part
+    if (valid > 0 || PASS == SLOPE_RANGE) {
         with_act(g.act.kind, [&](auto kind) {
             constexpr int KIND = decltype(kind)::value;
 #pragma unroll 1
@@ -1346,49 +1415,84 @@ __global__ void __launch_bounds__(256) linear_slope(SlopeArgs g) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = base + 16 * i;
-                    f32x8 d = dy[i], e = dy[i];
+                    f32x8 d[2] = {dy[i], dy[i]};
                     if constexpr (GATED || KIND != ACTK_NONE) {
                         f32x8 y;
-                        act_slope8<KIND>(g.act, z[i], y, d);
-                        d *= dy[i];
+                        act_slope8<KIND>(g.act, z[i], y, d[0]);
+                        d[0] *= dy[i];
                         if constexpr (GATED) {
-                            d *= u[i];
-                            e = dy[i] * y;
+                            d[0] *= u[i];
+                            d[1] = dy[i] * y;
                         }
                     }
                     if (row >= rows) continue;
-                    s0 += d;
-                    if constexpr (GATED) s1 += e;
-                    if (g.dZ) {  // the workspace's rows are whole groups
-                        const uint32_t o = (uint32_t)(row * (int)g.ldd + col) * sizeof(T);
-                        store8<T>(rd, o, d);
-                        if constexpr (GATED) store8<T>(re, o, e);
+                    if constexpr (PASS == SLOPE_RANGE) {
+                        float largest = 0.0f;
+#pragma unroll
+                        for (int p = 0; p < planes; ++p)
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float a = finite_abs(d[p][x]);
+                                most[p][x] = fmaxf(most[p][x], a);
+                                largest = fmaxf(largest, a);
+                            }
+#pragma unroll
+                        for (int by = 1; by < 16; by *= 2) largest = fmaxf(largest, __shfl_xor(largest, by, 16));
+                        if (col == 0 && g.row_max) g.row_max[(int64_t)strip * g.M + m0 + row] = largest;
+                    }
+                    const uint32_t o = (uint32_t)(row * (int)g.ldd + col) * sizeof(T);
+#pragma unroll
+                    for (int p = 0; p < planes; ++p) {
+                        if constexpr (PASS != SLOPE_SCALED) s[p] += d[p];
+                        // the workspace's rows are whole groups
+                        if constexpr (PASS == SLOPE_PLAIN) {
+                            if (g.dZ[p]) store8<T>(at(g.dZ[p], g.ldd), o, d[p]);
+                        } else if constexpr (PASS == SLOPE_SCALED) {
+                            if (g.dZ[p]) store8<T>(at(g.dZ[p], g.ldd), o, d[p] * inverse(g.rows[m0 + row]));
+                            if (g.dZc[p]) store8<T>(at(g.dZc[p], g.ldd), o, d[p] * down[p]);
+                        }
                     }
                 }
             }
         });
     }
-    if (!g.sums) return;
     // columns of the sixteen row groups, in their order: a thread a column
-    red[0][threadIdx.x] = s0;
-    if constexpr (GATED) red[1][threadIdx.x] = s1;
-    __syncthreads();
     const int c = (int)threadIdx.x % kSlopeCols, p = (int)threadIdx.x / kSlopeCols;
-    if (p >= planes || n0 + c >= g.np8) return;
-    const float* r = (const float*)red[p] + c;
-    float s = r[0];
+    const bool mine = p < planes && n0 + c < g.np8;
+    const int64_t to = ((int64_t)block * planes + p) * g.np8 + n0 + c;
+    const auto gather = [&](const f32x8 (&v)[planes], float* out, auto join) {
 #pragma unroll
-    for (int k = 1; k < 16; ++k) s += r[k * kSlopeCols];
-    g.sums[((int64_t)block * planes + p) * g.np8 + n0 + c] = s;
+        for (int q = 0; q < planes; ++q) red[q][threadIdx.x] = v[q];
+        __syncthreads();
+        if (mine) {
+            const float* r = (const float*)red[p] + c;
+            float x = r[0];
+#pragma unroll
+            for (int k = 1; k < 16; ++k) x = join(x, r[k * kSlopeCols]);
+            out[to] = x;
+        }
+    };
+    if (PASS == SLOPE_RANGE && g.col_max) {
+        gather(most, g.col_max, [](float a, float b) { return fmaxf(a, b); });
+        if (g.sums) __syncthreads();
+    }
+    if (PASS != SLOPE_SCALED && g.sums) gather(s, g.sums, [](float a, float b) { return a + b; });
 }
 
 // Bias gradients: the row blocks' column sums, in a fixed order: sixteen
-// interleaved runs of blocks, then the runs.  Bound by the launch: 64 blocks of
-// 4096 columns (1 MB) 5.2 us, 16 of 1025 3.9.
+// interleaved runs of blocks, then the runs.  The factors of fp16 gradients
+// likewise, of the columns (from the row blocks) and, in one plane more, of the
+// rows (from the strips).  Bound by the launch: 64 blocks of 4096 columns (1 MB)
+// 5.2 us, 16 of 1025 3.9.
 struct SumArgs {
     const float* sums;  // [blocks][planes][np8]
     void* out[2];       // planes; null: none
+    const float* row_max;
+    const float* col_max;
+    float* rows;        // factors [M]; null: none are asked for
+    float* cols;        // factors [planes][np8]
     int blocks, planes, np8, N;
+    int M, strips;
     int out_f32;
 };
 
@@ -1396,21 +1500,45 @@ template <int D>
 __global__ void __launch_bounds__(1024) linear_colsum(SumArgs g) {
     typedef typename Elem<D>::type T;
     __shared__ float red[16][64];
-    const int c = (int)threadIdx.x & 63, run = (int)threadIdx.x >> 6;
-    const int n = (int)blockIdx.x * 64 + c, p = (int)blockIdx.y;
-    float s = 0.0f;
-    if (n < g.N && g.out[p]) {
+    const int c = (int)threadIdx.x & 63, run = (int)threadIdx.x >> 6, p = (int)blockIdx.y;
+    // f(x, next) over the blocks of one column, x of the first run's threads at the end
+    const auto over = [&](const float* from, int64_t step, int count, bool ok, auto f) {
+        float x = 0.0f;
+        if (ok) {
 #pragma unroll 4
-        for (int b = run; b < g.blocks; b += 16) s += g.sums[((int64_t)b * g.planes + p) * g.np8 + n];
+            for (int b = run; b < count; b += 16) x = f(x, from[b * step]);
+        }
+        red[run][c] = x;
+        __syncthreads();
+        if (run == 0)
+            for (int k = 1; k < 16; ++k) x = f(x, red[k][c]);
+        __syncthreads();
+        return x;
+    };
+    if constexpr (D == DT_F16) {
+        const bool of_rows = p == g.planes;
+        const int end = of_rows ? g.M : g.np8;
+        for (int64_t n0 = (int64_t)blockIdx.x * 64; g.rows && n0 < end; n0 += (int64_t)gridDim.x * 64) {
+            const int64_t n = n0 + c;
+            const float m =
+                over(of_rows ? g.row_max + n : g.col_max + (int64_t)p * g.np8 + n,
+                     of_rows ? (int64_t)g.M : (int64_t)g.planes * g.np8, of_rows ? g.strips : g.blocks, n < end,
+                     [](float a, float b) { return fmaxf(a, b); });
+            if (run == 0 && n < end) (of_rows ? g.rows : g.cols + (int64_t)p * g.np8)[n] = scale_of(m);
+        }
+        if (of_rows) return;
     }
-    red[run][c] = s;
-    __syncthreads();
-    if (run != 0 || n >= g.N || !g.out[p]) return;
-    for (int k = 1; k < 16; ++k) s += red[k][c];
-    if (g.out_f32)
-        ((float*)g.out[p])[n] = s;
-    else
-        ((T*)g.out[p])[n] = (T)s;
+    if (!g.out[p]) return;
+    for (int64_t n0 = (int64_t)blockIdx.x * 64; n0 < g.N; n0 += (int64_t)gridDim.x * 64) {
+        const int64_t n = n0 + c;
+        const float s = over(g.sums + (int64_t)p * g.np8 + n, (int64_t)g.planes * g.np8, g.blocks, n < g.N,
+                             [](float a, float b) { return a + b; });
+        if (run != 0 || n >= g.N) continue;
+        if (g.out_f32)
+            ((float*)g.out[p])[n] = s;
+        else
+            ((T*)g.out[p])[n] = (T)s;
+    }
 }
 
 }  // namespace pgemm

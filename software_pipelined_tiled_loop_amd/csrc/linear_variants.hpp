@@ -25,7 +25,7 @@ struct LinKernels {
     const LinVariant* v;
     int n;
     LinLaunch join, join_gated;
-    hipError_t (*slope)(const SlopeArgs&, bool gated, int grid, hipStream_t);
+    hipError_t (*slope)(const SlopeArgs&, bool gated, int pass, int grid, hipStream_t);
     hipError_t (*colsum)(const SumArgs&, int grid, hipStream_t);
 };
 
@@ -53,14 +53,23 @@ template <int D, bool GATED>
 hipError_t lin_launch_join(const LinArgs& a, int grid, hipStream_t s) {
     return lin_launch<LinArgs>(&linear_join<D, GATED>, a, dim3(grid), kJoinCols / 8, s);
 }
+template <int D, int PASS>
+hipError_t lin_launch_pass(const SlopeArgs& a, bool gated, int grid, hipStream_t s) {
+    return gated ? lin_launch<SlopeArgs>(&linear_slope<D, true, PASS>, a, dim3(grid), 256, s)
+                 : lin_launch<SlopeArgs>(&linear_slope<D, false, PASS>, a, dim3(grid), 256, s);
+}
 template <int D>
-hipError_t lin_launch_slope(const SlopeArgs& a, bool gated, int grid, hipStream_t s) {
-    return gated ? lin_launch<SlopeArgs>(&linear_slope<D, true>, a, dim3(grid), 256, s)
-                 : lin_launch<SlopeArgs>(&linear_slope<D, false>, a, dim3(grid), 256, s);
+hipError_t lin_launch_slope(const SlopeArgs& a, bool gated, int pass, int grid, hipStream_t s) {
+    if constexpr (D != DT_F16)  // bf16 and fp32 have the range of the values
+        return lin_launch_pass<D, SLOPE_PLAIN>(a, gated, grid, s);
+    else if (pass == SLOPE_SCALED)
+        return lin_launch_pass<D, SLOPE_SCALED>(a, gated, grid, s);
+    else
+        return lin_launch_pass<D, SLOPE_RANGE>(a, gated, grid, s);
 }
 template <int D>
 hipError_t lin_launch_colsum(const SumArgs& a, int grid, hipStream_t s) {
-    return lin_launch<SumArgs>(&linear_colsum<D>, a, dim3(grid, a.planes), 1024, s);
+    return lin_launch<SumArgs>(&linear_colsum<D>, a, dim3(grid, a.planes + (a.rows ? 1 : 0)), 1024, s);
 }
 
 constexpr int lin_la(int lay) { return lay == LIN_XX ? LAY_X : LAY_K; }
