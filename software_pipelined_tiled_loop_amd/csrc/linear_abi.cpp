@@ -35,15 +35,11 @@ LinKernels kernels_for(int dtype) {
 ActArgs act_args(int act) {
     // -log2(e) * P(t); see ActArgs
     constexpr double kLog2e = 1.4426950408889634;
-    static const double gelu[7] = {1.5957684317138,     0.07266856844868,    -6.6261136489796e-05, -1.1047993311290e-04,
-                                   7.9381600098274e-06, -2.6688873955814e-07, 3.6111307428585e-09};
     ActArgs a;
     std::memset(&a, 0, sizeof(a));
     a.kind = act;
     if (act == PGEMM_ACT_SILU) {
         a.c[0] = (float)-kLog2e;
-    } else if (act == PGEMM_ACT_GELU) {
-        for (int d = 0; d < 7; ++d) a.c[d] = (float)(-kLog2e * gelu[d]);
     } else if (act == PGEMM_ACT_GELU_TANH) {
         const double c = 1.5957691216057308;  // sqrt(8 / pi)
         a.c[0] = (float)(-kLog2e * c);

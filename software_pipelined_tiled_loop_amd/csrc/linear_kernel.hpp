@@ -42,22 +42,21 @@ namespace pgemm {
 enum Lay : int { LAY_K = 0, LAY_X = 1 };
 enum ActKind : int { ACTK_NONE = 0, ACTK_RELU = 1, ACTK_SILU = 2, ACTK_GELU = 3, ACTK_GELU_TANH = 4 };
 
-// Activations silu, gelu and gelu_tanh share one form,
+// Activations silu and gelu_tanh share one form,
 //     act(x) = x * sigmoid(x * P(x^2)):
 //   silu       P = 1
 //   gelu_tanh  P = sqrt(8/pi) (1 + 0.044715 t): (1 + tanh a)/2 = sigmoid(2a)
-//   gelu       P = degree-6 fit of logit(Phi(x)) / x in t = x^2 up to
-//              t = kGeluCap, constant beyond (weighted least squares iterated
-//              towards the minimax of x Phi(x)):
-//              |x sigmoid(x P) - x Phi(x)| < 7e-8 for every x
 // and the slopes
-//     act'(x) = p + x p (1 - p) (P + 2 t P'),  p = sigmoid(x P)
-// (gelu: Phi + x phi, phi(x) = exp(-x^2/2) / sqrt(2 pi)).
+//     act'(x) = p + x p (1 - p) (P + 2 t P'),  p = sigmoid(x P).
+// gelu is x Phi(x), its slope Phi + x phi with phi(x) = exp(-x^2/2) / sqrt(2 pi);
+//     Phi(-y) = exp(-y^2/2) Q(y) for y >= 0,  Phi(y) = 1 - Phi(-y),
+// where Q falls from 1/2 as slowly as 1/y: gelu_q.  Each takes one exponential and
+// one reciprocal, for value and slope together, and stays accurate relative to
+// itself far below zero, down to the smallest numbers of the types.
 struct ActArgs {
     int kind;      // ActKind
-    float c[7];    // coefficients of -log2(e) * P: sigmoid(x P) = 1 / (1 + exp2(x c(t)))
+    float c[2];    // coefficients of -log2(e) * P: sigmoid(x P) = 1 / (1 + exp2(x c(t)))
 };
-constexpr float kGeluCap = 30.25f;
 
 struct EpiArgs {
     void* Y[2];           // output (gated: H); two for a launch with two outputs side by side (dWg, dWu)
@@ -336,8 +335,31 @@ __device__ __forceinline__ float act_poly(const ActArgs& a, float t) {
 
 template <int DEG>
 __device__ __forceinline__ float act_smooth(const ActArgs& a, float x) {
-    const float p = DEG == 0 ? a.c[0] : act_poly<DEG>(a, DEG == 6 ? fminf(x * x, kGeluCap) : x * x);
+    const float p = DEG == 0 ? a.c[0] : act_poly<DEG>(a, x * x);
     return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * p));
+}
+
+// Q(y) = Phi(-y) exp(y^2 / 2), y >= 0, as a polynomial without constant term in
+// s = 1 / (1 + 0.3046 y) (both fall as 1/y): least squares of the relative error,
+// iterated towards its minimax on 0 <= y <= 14, beyond which exp(-y^2 / 2) is zero.
+// 9e-8 relative, 3.7e-7 evaluated in fp32.
+__device__ __forceinline__ float gelu_q(float y) {
+    const float s = __builtin_amdgcn_rcpf(fmaf(0.3046f, y, 1.0f));
+    float q = 0.03676469251513481f;
+    q = fmaf(q, s, -0.15391618013381958f);
+    q = fmaf(q, s, 0.18829947710037231f);
+    q = fmaf(q, s, -0.04002207890152931f);
+    q = fmaf(q, s, 0.12202255427837372f);
+    q = fmaf(q, s, 0.10302632302045822f);
+    q = fmaf(q, s, 0.12234748154878616f);
+    q = fmaf(q, s, 0.12147778272628784f);
+    return q * s;
+}
+// Phi(x); e receives exp(-x^2 / 2).
+__device__ __forceinline__ float gelu_phi(float x, float& e) {
+    e = __builtin_amdgcn_exp2f(-0.7213475204f * (x * x));  // NaN where x is
+    const float w = e * gelu_q(__builtin_fabsf(x));
+    return x > 0.0f ? 1.0f - w : w;
 }
 
 template <int KIND>
@@ -346,7 +368,10 @@ __device__ __forceinline__ float act1(const ActArgs& a, float x) {
     else if constexpr (KIND == ACTK_RELU) return x < 0.0f ? 0.0f : x;  // NaN stays NaN
     else if constexpr (KIND == ACTK_SILU) return act_smooth<0>(a, x);
     else if constexpr (KIND == ACTK_GELU_TANH) return act_smooth<1>(a, x);
-    else return act_smooth<6>(a, x);
+    else {
+        float e;
+        return x * gelu_phi(x, e);
+    }
 }
 template <int KIND>
 __device__ __forceinline__ f32x8 act8(const ActArgs& a, f32x8 x) {
@@ -372,26 +397,27 @@ __device__ __forceinline__ void with_act(int kind, F&& f) {
     }
 }
 
-// act(x) and act'(x) of a smooth activation, from one exponential and one
-// reciprocal (gelu: two).  Beyond |x| = 64 the sigmoid is 0 or 1, so x and t
-// held there leave the slope as it is and keep it finite (x^3 does not overflow,
-// no infinity meets a zero); e is held too, so that e p = 1 - p where p vanishes.
+// act(x) and act'(x) of a smooth activation.  Beyond |x| = 128 exponential and
+// sigmoid are 0 or 1 (gelu_tanh: beyond 12), so x and t held there leave the slope
+// as it is and keep it finite (x^3 does not overflow, no infinity meets a zero); e is
+// held too, so that e p = 1 - p where p vanishes.
 template <int DEG>
 __device__ __forceinline__ void act_slope(const ActArgs& a, float x, float& y, float& d) {
-    const float t = x * x;
-    const float c = DEG == 0 ? a.c[0] : act_poly<DEG>(a, fminf(t, DEG == 6 ? kGeluCap : 4096.0f));
+    const float t = fminf(x * x, 4096.0f);
+    const float c = DEG == 0 ? a.c[0] : act_poly<DEG>(a, t);
     const float e = __builtin_amdgcn_exp2f(x * c);
     const float p = __builtin_amdgcn_rcpf(1.0f + e);  // NaN where x is
-    const float h = __builtin_amdgcn_fmed3f(x, -64.0f, 64.0f);
+    const float h = __builtin_amdgcn_fmed3f(x, -128.0f, 128.0f);
     y = x * p;
-    if constexpr (DEG == 6) {
-        // Phi + x phi, phi(x) = exp2(-t log2(e) / 2) / sqrt(2 pi)
-        d = fmaf(h, 0.3989422804f * __builtin_amdgcn_exp2f(-0.7213475204f * t), p);
-    } else {
-        // d(x P)/dx = P + 2 t P', from the coefficients of -log2(e) P
-        const float s = -0.6931471806f * (DEG == 1 ? fmaf(2.0f * fminf(t, 4096.0f), a.c[1], c) : c);
-        d = fmaf(h * p * s, fminf(e, 0x1p120f) * p, p);
-    }
+    // d(x P)/dx = P + 2 t P', from the coefficients of -log2(e) P
+    const float s = -0.6931471806f * (DEG == 1 ? fmaf(2.0f * t, a.c[1], c) : c);
+    d = fmaf(h * p * s, fminf(e, 0x1p126f) * p, p);
+}
+__device__ __forceinline__ void gelu_slope(float x, float& y, float& d) {
+    float e;
+    const float p = gelu_phi(x, e);
+    y = x * p;
+    d = fmaf(__builtin_amdgcn_fmed3f(x, -128.0f, 128.0f), 0.3989422804f * e, p);
 }
 
 template <int KIND>
@@ -402,8 +428,10 @@ __device__ __forceinline__ void act_slope8(const ActArgs& a, f32x8 x, f32x8& y, 
         if constexpr (KIND == ACTK_RELU) {
             yi = x[i] < 0.0f ? 0.0f : x[i];
             di = x[i] > 0.0f ? 1.0f : 0.0f;
+        } else if constexpr (KIND == ACTK_GELU) {
+            gelu_slope(x[i], yi, di);
         } else if constexpr (KIND != ACTK_NONE) {
-            act_slope<KIND == ACTK_SILU ? 0 : KIND == ACTK_GELU_TANH ? 1 : 6>(a, x[i], yi, di);
+            act_slope<KIND == ACTK_SILU ? 0 : 1>(a, x[i], yi, di);
         }
         y[i] = yi;
         d[i] = di;
