@@ -456,8 +456,10 @@ int pgemm_diag_parts(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
  *
  * Errors: UNSUPPORTED_DTYPE; INVALID_ARG (a negative size, a leading dimension
  * too small, a missing or misaligned pointer, an unknown order, activation or
- * output type, a workspace too small); TOO_LARGE (a size above 2^31 - 256 or a
- * leading dimension of 2^21 or more); HIP for a rejected launch. */
+ * output type, a workspace too small); TOO_LARGE (a size above 2^31 - 256, a
+ * leading dimension of 2^21 or more, or more rows and columns than a launch's
+ * grid of 2^32 threads covers: no matrix of up to 2^35 elements and 2^29 rows is
+ * concerned); HIP for a rejected launch. */
 enum pgemm_act {
     PGEMM_ACT_NONE = 0,
     PGEMM_ACT_RELU = 1,

@@ -20,6 +20,7 @@ namespace {
 constexpr int64_t kMaxDim = 0x7fffff00;
 constexpr int64_t kMaxLd = (int64_t)1 << 21;  // 256 rows of 4-byte elements stay below 2^31 bytes
 constexpr int kNumCU = 256;
+constexpr int64_t kMaxItems = (int64_t)1 << 32;  // a launch has fewer threads than this
 constexpr int64_t kMaxSumGroups = 16384;  // workgroups of linear_colsum, which goes on from there by itself
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -111,7 +112,8 @@ double est_us(const LinVariant& v, const Shape& p, int dtype, int64_t splits) {
 }
 
 // The tile and the splits of a product, from its sizes and type alone (so the
-// workspace functions and the calls agree).
+// workspace functions and the calls agree).  No variant where every one has more
+// threads than a launch holds.
 Plan search_plan(const Shape& p, int dtype) {
     const LinKernels k = kernels_for(dtype);
     Plan best{};
@@ -122,7 +124,7 @@ Plan search_plan(const Shape& p, int dtype) {
         const int64_t kt = ceil_div(p.K, v.bk) * p.halves;
         const int64_t tiles = ceil_div(p.rows, v.bm) * ceil_div(p.cols, v.bn) * p.outs;
         if (v.bm == 256 && (p.rows <= 64 || p.cols <= 64)) continue;
-        if (tiles > 0x1fffff00) continue;  // with their splits, more workgroups than a grid holds
+        if (round_up(tiles, 8) * v.threads >= kMaxItems) continue;  // (split, there are no more than 2048)
         for (int64_t s = 1; s <= 32; ++s) {
             // K tiles for each wave, and not more workgroups than splitting is for
             if (s > 1 && (s * (v.few ? v.few : 4) > kt || tiles * s > (v.few ? 8 : 2) * kNumCU)) break;
@@ -133,6 +135,7 @@ Plan search_plan(const Shape& p, int dtype) {
             best.splits = s;
         }
     }
+    if (!best.v) return best;
     const LinVariant& v = *best.v;
     best.tiles_m = ceil_div(p.rows, v.bm);
     best.tiles_n = ceil_div(p.cols, v.bn);
@@ -165,9 +168,11 @@ Plan plan_product(const Shape& p, int dtype) {
     return s.plan;
 }
 
+// Bytes of the splits' sums, or PGEMM_ERR_TOO_LARGE.
 int64_t part_bytes(const Shape& p, int dtype) {
     if (p.rows == 0 || p.cols == 0) return 0;
-    return round_up(plan_product(p, dtype).part_bytes, 256);
+    const Plan pl = plan_product(p, dtype);
+    return pl.v ? round_up(pl.part_bytes, 256) : PGEMM_ERR_TOO_LARGE;
 }
 
 int hip_failed(const char* what, hipError_t e) {
@@ -180,6 +185,7 @@ int run_product(const Shape& p, LinArgs& a, int dtype, void* part, hipStream_t s
     if (p.rows == 0 || p.cols == 0) return PGEMM_OK;
     const LinKernels k = kernels_for(dtype);
     const Plan pl = plan_product(p, dtype);
+    if (!pl.v) return PGEMM_ERR_TOO_LARGE;  // found out before, with the workspace
     const LinVariant& v = *pl.v;
     a.K = (int)p.K;
     a.halves = p.halves;
@@ -211,6 +217,7 @@ bool grids_fit(int64_t a, int64_t b) { return ceil_div(a, 64) * ceil_div(b, 64) 
 int check_sizes(int64_t M, int64_t N, int64_t K, int dtype) {
     if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
     if (M < 0 || N < 0 || K < 0) return PGEMM_ERR_INVALID_ARG;
+    if (M > 0 && N >= kMaxLd) return PGEMM_ERR_TOO_LARGE;  // every call has a matrix of M rows of N
     if (!in_range(M, N, K) || !grids_fit(M, N) || !grids_fit(M, K) || !grids_fit(K, N) || !grids_fit(N, K))
         return PGEMM_ERR_TOO_LARGE;
     return PGEMM_OK;
@@ -224,6 +231,7 @@ int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t 
 }
 int check_vector(const void* p, int64_t es) { return (uintptr_t)p % es ? PGEMM_ERR_INVALID_ARG : PGEMM_OK; }
 int check_workspace(const void* p, int64_t bytes, int64_t need) {
+    if (need < 0) return (int)need;
     return need > 0 && (!p || (uintptr_t)p % 16 || bytes < need) ? PGEMM_ERR_INVALID_ARG : PGEMM_OK;
 }
 bool known(int order, int act, int out, int dtype) {
@@ -248,6 +256,8 @@ Shape dw_shape(int64_t M, int64_t N, int64_t K, int order, int outs) {
     return order == PGEMM_KN ? Shape{K, N, M, LIN_XX, 0, 1, outs} : Shape{N, K, M, LIN_XX, 0, 1, outs};
 }
 int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
+// The larger of two counts of bytes, or an error among them.
+int64_t both(int64_t a, int64_t b) { return a < 0 ? a : b < 0 ? b : larger(a, b); }
 
 // Workspace of a backward pass: gradients at the pre-activations (fp16: in two
 // copies, with the largest entries and factors of rows and columns), the row
@@ -288,8 +298,8 @@ Backward backward_layout(int64_t M, int64_t N, int64_t K, int dtype, int planes)
     b.sum_bytes = round_up(b.blocks * planes * b.np8 * 4, 256);
     b.split_bytes = 0;
     for (int order = 0; order < 2; ++order) {
-        b.split_bytes = larger(b.split_bytes, part_bytes(dx_shape(M, N, K, order, planes), dtype));
-        b.split_bytes = larger(b.split_bytes, part_bytes(dw_shape(M, N, K, order, planes), dtype));
+        b.split_bytes = both(b.split_bytes, part_bytes(dx_shape(M, N, K, order, planes), dtype));
+        b.split_bytes = both(b.split_bytes, part_bytes(dw_shape(M, N, K, order, planes), dtype));
     }
     return b;
 }
@@ -421,14 +431,16 @@ int check_weight(const void* W, int64_t N, int64_t K, int64_t ldw, int order, in
 
 int64_t forward_workspace(int64_t M, int64_t N, int64_t K, int dtype, int gated) {
     PGEMM_TRY(check_sizes(M, N, K, dtype));
-    return larger(part_bytes(forward_shape(M, N, K, PGEMM_KN, gated), dtype),
-                  part_bytes(forward_shape(M, N, K, PGEMM_NK, gated), dtype));
+    return both(part_bytes(forward_shape(M, N, K, PGEMM_KN, gated), dtype),
+                part_bytes(forward_shape(M, N, K, PGEMM_NK, gated), dtype));
 }
 
 int64_t backward_workspace(int64_t M, int64_t N, int64_t K, int act, int dtype, int planes) {
     PGEMM_TRY(check_sizes(M, N, K, dtype));
     if (act < PGEMM_ACT_NONE || act > PGEMM_ACT_GELU_TANH) return PGEMM_ERR_INVALID_ARG;
-    return backward_layout(M, N, K, dtype, planes).total(planes, planes == 2 || act != PGEMM_ACT_NONE);
+    const Backward b = backward_layout(M, N, K, dtype, planes);
+    if (b.split_bytes < 0 || b.strips * b.blocks * 256 >= kMaxItems) return PGEMM_ERR_TOO_LARGE;
+    return b.total(planes, planes == 2 || act != PGEMM_ACT_NONE);
 }
 
 }  // namespace

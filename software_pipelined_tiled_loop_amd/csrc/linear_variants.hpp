@@ -15,6 +15,7 @@ enum LinLay : int { LIN_KX = 0, LIN_KK = 1, LIN_XX = 2 };
 struct LinVariant {
     int lay, gated;
     int bm, bn, bk;  // bn: output columns of the tile
+    int threads;     // of a workgroup
     int few;         // waves that share the K tiles of a few-rows kernel, else 0
     int per_cu;      // workgroups whose LDS a CU holds
     int (*ring_tiles)(int64_t K, int64_t rows, int64_t lda, int64_t cols, int64_t ldb);
@@ -79,7 +80,8 @@ constexpr int lin_lb(int lay) { return lay == LIN_KK ? LAY_K : LAY_X; }
     LinCfg<D, lin_la(LAY), lin_lb(LAY), BM, BN, BK, S, WGM, WGN, GATED != 0>
 #define LIN_VARIANT(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)                                 \
     LinVariant {                                                                            \
-        LAY, GATED, BM, GATED ? BN / 2 : BN, BK, 0, 163840 / LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)::LDS, \
+        LAY, GATED, BM, GATED ? BN / 2 : BN, BK, 64 * WGM * WGN, 0,                         \
+            163840 / LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)::LDS,                  \
             &lin_ring_tiles<LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)>,               \
             &lin_launch_tile<LIN_CFG(D, LAY, GATED, BM, BN, BK, S, WGM, WGN)>               \
     }
@@ -93,7 +95,7 @@ constexpr int lin_lb(int lay) { return lay == LIN_KK ? LAY_K : LAY_X; }
 #define LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S) FewCfg<D, lin_la(LAY), lin_lb(LAY), FM, NCOL, NW, S, GATED != 0>
 #define LIN_FEW(D, LAY, GATED, FM, NCOL, NW, S)                                                      \
     LinVariant {                                                                                     \
-        LAY, GATED, 16 * FM, GATED ? NCOL / 2 : NCOL, LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)::BK, NW, \
+        LAY, GATED, 16 * FM, GATED ? NCOL / 2 : NCOL, LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)::BK, 64 * NW, NW, \
             163840 / LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)::LDS,                               \
             &lin_ring_tiles<LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)>,                            \
             &lin_launch_few<LIN_FEW_CFG(D, LAY, GATED, FM, NCOL, NW, S)>                             \
