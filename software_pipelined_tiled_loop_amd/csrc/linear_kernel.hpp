@@ -627,11 +627,11 @@ struct LinCfg {
     // (lone_step), its accumulators in AGPRs: all 256 for a wave of 128 x 128.
     // (fp32: the four MFMAs of a block depend on each other; left to the compiler.)
     static constexpr bool LONE = ES == 2 && NW == 4;
-    static constexpr int MINW = BM * BN / NW >= 128 * 128 ? 1 : 2;  // waves per SIMD
     static constexpr int WM = BM / WGM, WNP = BNP / WGN;
     static constexpr int FM = WM / 16, FNP = WNP / 16, FN = FNP * NP;
     static constexpr int A_BYTES = OA::BYTES, B_BYTES = OB::BYTES * NP;
     static constexpr int STAGE = A_BYTES + B_BYTES, LDS = S * STAGE;
+    static constexpr int MINW = 163840 / LDS * NW / 4;  // waves per SIMD, by the CU's LDS
     static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW, LPS = A_INSTR + B_INSTR;
     static constexpr int NKS = BK / T::KSTEP;
     static_assert(NKS == 2, "the loop body is written for two K steps per K tile");
