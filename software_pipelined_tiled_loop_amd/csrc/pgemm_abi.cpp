@@ -439,7 +439,7 @@ const char* pgemm_strerror(int status) {
     }
 }
 
-int pgemm_version(void) { return 10000; }
+int pgemm_version(void) { return 10100; }  // 1.1: the feed-forward operators
 
 int pgemm_num_variants(void) {
     int n = 0;
