@@ -575,8 +575,8 @@ struct Epi {
     template <int KIND>
     __device__ __forceinline__ void put1(int by, int x, float v, float w) const {
         const uint32_t bo = (uint32_t)(col + x) * TS, at = (uint32_t)x * ys;
-        if (SCALED && srow) v *= load1<float>(make_rsrc(srow), (uint32_t)(row + by) * 4u);
-        if (SCALED && scol) v *= load1<float>(make_rsrc(scol), (uint32_t)(col + x) * 4u);
+        if (SCALED && (srow || scol))  // one of them
+            v *= load1<float>(make_rsrc(srow ? srow : scol), (uint32_t)(srow ? row + by : col + x) * 4u);
         if (e.bias[0]) v += load1<T>(make_rsrc((const T*)e.bias[0] + n0), bo);
         if (e.Z) store1<T>(z, oz + (uint32_t)(by * (int)e.ldz + x) * TS, v);
         v = act1<KIND>(e.act, v);
