@@ -64,9 +64,10 @@ struct Plan {
 
 // Estimated microseconds of a product with its K tiles split in `splits`.  The
 // rates and fixed costs are fitted to choose well, on 2000 products of 1 to 8192
-// rows in all layouts and types, each timed on every variant in 1 to 32 splits:
-// the choice takes 1.5 % longer than the best (mean of random sizes), 2.0 % for
-// multiples of 1024, 3.3 % for weights beyond the shared cache.
+// rows in all layouts and types, each timed on every variant in 1 to 32 splits.
+// On 1360 others the choice takes 1.8 % longer than the best (geometric mean of 900
+// random sizes; nine in ten within 7 %, the worst 72 %), 1.8 % for 300 multiples of
+// 1024 and 3.9 % for 160 weights beyond the shared cache.
 //
 // Tiles: the workgroups run in rounds, one or two (128 x 128 with two stages) a
 // CU at a time.  Rates of the whole part in TFLOP/s and us a round, 16-bit
