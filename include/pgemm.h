@@ -431,9 +431,10 @@ int pgemm_diag_parts(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
  *
  * Activations: none, relu, silu z/(1 + exp(-z)), gelu z Phi(z), gelu_tanh
  * (z/2)(1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))).  relu'(0) = 0; a NaN passes
- * through every activation.  The smooth ones and their slopes are accurate
- * relative to themselves also far below zero: to (4 a + 20) 2^-24, where exp(-a) is
- * the exponential in them.
+ * through every activation.  The smooth ones, and each of the two terms of their
+ * slopes, are accurate relative to themselves also far below zero: to
+ * (4 a + 20) 2^-24, where exp(-a) is the exponential in them, down to fp32's
+ * smallest normal number.
  *
  * In the backward passes dZ (dG, dU) is rounded to the operand type before it
  * is multiplied (not where act is none: dZ is dY); the bias gradients sum

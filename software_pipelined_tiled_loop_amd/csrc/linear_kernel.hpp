@@ -52,7 +52,7 @@ enum ActKind : int { ACTK_NONE = 0, ACTK_RELU = 1, ACTK_SILU = 2, ACTK_GELU = 3,
 //     Phi(-y) = exp(-y^2/2) Q(y) for y >= 0,  Phi(y) = 1 - Phi(-y),
 // where Q falls from 1/2 as slowly as 1/y: gelu_q.  Each takes one exponential and
 // one reciprocal, for value and slope together, and stays accurate relative to
-// itself far below zero, down to the smallest numbers of the types.
+// itself far below zero, down to fp32's smallest normal number.
 struct ActArgs {
     int kind;      // ActKind
     float c[2];    // coefficients of -log2(e) * P: sigmoid(x P) = 1 / (1 + exp2(x c(t)))

@@ -18,10 +18,13 @@ def planner(tmp_path_factory):
         pytest.skip("hipcc not available")
     at = tmp_path_factory.mktemp("plans")
     # the planner and the table of variants are host code; the kernels' objects are the library's own
+    sources = [os.path.join(build.CSRC, f) for f in os.listdir(build.CSRC) if f.endswith(".hpp") or f.startswith("linear_")]
+    newest = max(os.path.getmtime(f) for f in sources)
     objs = []
     for name in ("linear_f32.hip", "linear_f16.hip", "linear_bf16.hip"):
         obj = os.path.join(build.BUILD_DIR, name + ".o")
-        objs.append(obj if os.path.exists(obj) else build._compile(os.path.join(build.CSRC, name)))
+        fresh = os.path.exists(obj) and os.path.getmtime(obj) >= newest
+        objs.append(obj if fresh else build._compile(os.path.join(build.CSRC, name)))
     obj, exe = str(at / "plans.o"), str(at / "plans")
     flags = [f for f in build.HIPCC_FLAGS if f != "-O3"] + ["-O1"]
     for cmd in ([hipcc] + flags + ["-x", "hip", "-c", os.path.join(ROOT, "tests", "linear_plans.cpp"), "-o", obj],
