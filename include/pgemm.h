@@ -507,6 +507,96 @@ int pgemm_gated_backward(int64_t M, int64_t N, int64_t K, const void* dH, int64_
                          int64_t lddw, int dw_order, void* dbias_g, void* dbias_u, int grad_dtype, int dtype,
                          void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ---- The norm and the microscaled operators ------------------------------------
+ *
+ * What stands in front of a feed-forward block, and the block's products on
+ * operands of 8 and 4 bits.  Activations are row-major, one row per token; fp32,
+ * fp16 and bf16 values (`dtype`; PGEMM_I8 returns PGEMM_ERR_UNSUPPORTED_DTYPE).
+ *
+ *   rms_norm          h = x + r     y = h w / sqrt(mean(h^2) + eps)
+ *   rms_norm backward, with s = 1 / sqrt(mean(h^2) + eps) and g = dy w:
+ *                     dx = dh + s g - h s^3 mean(g h)     dw = sum over rows of dy h s
+ *                     (x and r have the same gradient dx; dh arrives at h from
+ *                     elsewhere, as down the skip connection)
+ *   mx_quantize       MX blocks of a matrix's rows; mx_dequantize: their values
+ *   mx_linear         Y = act(X W + b) + R
+ *   mx_gated          H = act(X Wg + bg) * (X Wu + bu)
+ *
+ * MX blocks: 32 entries along a row share the scale 2^e.  Entries are e4m3
+ * (PGEMM_MX8, one a byte, at most 448) or e2m1 (PGEMM_MX4, two a byte, the first in
+ * the low half, at most 6); a scale is the byte e + 127, or 255 for NaN.
+ * Quantisation takes the smallest e from -127 on for which no entry rounds beyond
+ * the largest value, and rounds x 2^-e to nearest even; a block that holds an
+ * infinity or a NaN becomes NaN as a whole.  Its gradient is the identity, where
+ * one trains through it.  A row is stored in whole groups of 256 entries, zeros
+ * behind the last one: ceil(K / 256) * 256 codes (half as many bytes in MX4) and
+ * ceil(K / 256) * 8 scales.  Code rows are 16-byte aligned, scale rows 4-byte
+ * aligned (pointers and the leading dimensions ldq and lds, in bytes).  Blocks that
+ * were not written by mx_quantize or rms_norm have to hold zero codes there too.
+ *
+ * The products take activations X in either format and weights in MX4, stored
+ * W[N][K] (row n holds the weights of output column n); products and scales are
+ * exact, sums are fp32, as the matrix cores form them: of MX8 operands they add eight
+ * neighbouring products aligned to the largest, each to 2^-13 of it.  Bias, residual
+ * and output have type `dtype`, and are rounded once.  Activations as for linear.
+ *
+ * The norm adds, squares and sums in fp32 and rounds each output once, from fp32;
+ * rows whose sum of squares leaves fp32's range come out as the formula gives it
+ * with an infinite sum.  MX outputs are taken from the unrounded y.
+ *
+ * Nothing depends on the order in which workgroups run: repeated calls give the
+ * same bits.  Calls enqueue kernels on `stream`, allocate nothing and can be
+ * captured in a graph; workspaces as for the feed-forward operators.  Outputs may
+ * not overlap inputs, the workspace or each other, except that H may be X or R
+ * itself, dX may be dH itself, and R may be Y itself.  Empty sizes are served.
+ *
+ * Errors: UNSUPPORTED_DTYPE; INVALID_ARG (a negative size, a leading dimension too
+ * small, a missing or misaligned pointer, an unknown order, activation, format or
+ * output type, an eps that is negative or not finite, a workspace too small);
+ * TOO_LARGE (rows above 2^31 - 256, a row length or leading dimension of 2^21 or more,
+ * a product of 2^36 outputs or more); HIP for a rejected launch. */
+enum pgemm_mx { PGEMM_MX8 = 0, PGEMM_MX4 = 1 };
+
+/* Bytes of workspace, or a negative pgemm_status. */
+int64_t pgemm_rms_norm_backward_workspace(int64_t M, int64_t N, int dtype);
+int64_t pgemm_mx_linear_workspace(int64_t M, int64_t N, int64_t K, int x_format);
+int64_t pgemm_mx_gated_workspace(int64_t M, int64_t N, int64_t K, int x_format);
+
+/* The norm of M rows of N.  R, weight (null: one), H (receives x + r), Y and the
+ * MX output (Q and S, both or neither, of `format`) may be null; Y has out_dtype:
+ * dtype or PGEMM_F32. */
+int pgemm_rms_norm(int64_t M, int64_t N, const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight,
+                   double eps, void* H, int64_t ldh, void* Y, int64_t ldy, int out_dtype, void* Q, int64_t ldq, void* S,
+                   int64_t lds, int format, int dtype, void* stream);
+
+/* Its gradients, from h.  weight, dH, dX and dweight[N] (grad_dtype: dtype or
+ * PGEMM_F32) may be null; without dweight no workspace is needed. */
+int pgemm_rms_norm_backward(int64_t M, int64_t N, const void* dY, int64_t lddy, const void* H, int64_t ldh,
+                            const void* weight, double eps, const void* dH, int64_t lddh, void* dX, int64_t lddx,
+                            void* dweight, int grad_dtype, int dtype, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+
+/* Blocks of `rows` rows of K entries: X[rows][K] (x_order PGEMM_NK) or
+ * X[K][rows] (PGEMM_KN: the rows are X's columns, as of a weight stored K x N). */
+int pgemm_mx_quantize(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_order, int dtype, void* Q, int64_t ldq,
+                      void* S, int64_t lds, int format, void* stream);
+/* X[rows][K], each value rounded once to dtype. */
+int pgemm_mx_dequantize(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* S, int64_t lds, int format,
+                        void* X, int64_t ldx, int dtype, void* stream);
+
+/* Y[M][N] = act(X W + bias) + R.  bias[N] and R[M][N] may be null. */
+int pgemm_mx_linear(int64_t M, int64_t N, int64_t K, const void* XQ, int64_t ldxq, const void* XS, int64_t ldxs,
+                    int x_format, const void* WQ, int64_t ldwq, const void* WS, int64_t ldws, const void* bias,
+                    const void* R, int64_t ldr, int act, void* Y, int64_t ldy, int dtype, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/* H[M][N] = act(X Wg + bias_g) * (X Wu + bias_u).  Both weights share the leading
+ * dimensions; the biases may be null. */
+int pgemm_mx_gated(int64_t M, int64_t N, int64_t K, const void* XQ, int64_t ldxq, const void* XS, int64_t ldxs,
+                   int x_format, const void* WgQ, const void* WuQ, int64_t ldwq, const void* WgS, const void* WuS,
+                   int64_t ldws, const void* bias_g, const void* bias_u, int act, void* H, int64_t ldh, int dtype,
+                   void* workspace, int64_t workspace_bytes, void* stream);
+
 /* ABI version: major*10000 + minor*100 + patch (a library convention, not
  * from the pages). */
 int pgemm_version(void);

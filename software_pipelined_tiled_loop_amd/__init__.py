@@ -13,7 +13,8 @@ from __future__ import annotations
 import importlib
 
 __all__ = ["binding", "inputs", "build", "pgemm_gemm", "pgemm_gemm_ex", "pgemm_plan",
-           "pgemm_strerror", "gemm", "linear", "linear_backward", "gated", "gated_backward"]
+           "pgemm_strerror", "gemm", "linear", "linear_backward", "gated", "gated_backward",
+           "rms_norm", "rms_norm_backward", "mx_empty", "mx_quantize", "mx_dequantize", "mx_linear", "mx_gated"]
 
 
 def __getattr__(name):
@@ -21,7 +22,8 @@ def __getattr__(name):
         return importlib.import_module("." + name, __name__)
     if name in ("pgemm_gemm", "pgemm_gemm_ex", "pgemm_plan", "pgemm_strerror", "gemm",
                 "pgemm_num_variants", "pgemm_variant_info", "PgemmError", "linear", "linear_backward", "gated",
-                "gated_backward"):
+                "gated_backward", "rms_norm", "rms_norm_backward", "mx_empty", "mx_quantize", "mx_dequantize",
+                "mx_linear", "mx_gated"):
         mod = importlib.import_module(".binding", __name__)
         return getattr(mod, name)
     raise AttributeError(name)

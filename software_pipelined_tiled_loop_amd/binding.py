@@ -119,8 +119,29 @@ _lib.pgemm_gated_backward.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _v
                                       _vp]
 _lib.pgemm_gated_backward.restype = _int
 
+for _f, _a in (
+        ("pgemm_rms_norm", [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _dbl, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64,
+                            _int, _int, _vp]),
+        ("pgemm_rms_norm_backward", [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _dbl, _vp, _i64, _vp, _i64, _vp, _int, _int,
+                                     _vp, _i64, _vp]),
+        ("pgemm_mx_quantize", [_i64, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp, _i64, _int, _vp]),
+        ("pgemm_mx_dequantize", [_i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _int, _vp]),
+        ("pgemm_mx_linear", [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _int, _vp,
+                             _i64, _int, _vp, _i64, _vp]),
+        ("pgemm_mx_gated", [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _int,
+                            _vp, _i64, _int, _vp, _i64, _vp])):
+    getattr(_lib, _f).argtypes = _a
+    getattr(_lib, _f).restype = _int
+for _f, _a in (("pgemm_rms_norm_backward_workspace", [_i64, _i64, _int]),
+               ("pgemm_mx_linear_workspace", [_i64, _i64, _i64, _int]),
+               ("pgemm_mx_gated_workspace", [_i64, _i64, _i64, _int])):
+    getattr(_lib, _f).argtypes = _a
+    getattr(_lib, _f).restype = _i64
+
 ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 ORDER_KN, ORDER_NK = 0, 1
+MX8, MX4 = 0, 1
+MX_FORMAT = {"mx8": MX8, "mx4": MX4}
 
 # Steady-state parts of a parts-ladder build (enum pgemm_part).
 PART_DMA, PART_BARRIER, PART_AREADS, PART_BREADS, PART_ALL = 1, 2, 4, 8, 15
@@ -130,7 +151,10 @@ EXPORTED = ("pgemm_gemm", "pgemm_gemm_ex", "pgemm_plan", "pgemm_strerror", "pgem
             "pgemm_model_global_loads_per_output", "pgemm_model_compute_load_ratio", "pgemm_hazard_copy_reduce",
             "pgemm_diag_mfma_ceiling", "pgemm_diag_lds_stream", "pgemm_diag_wait_profile", "pgemm_diag_parts",
             "pgemm_linear", "pgemm_gated", "pgemm_linear_backward", "pgemm_gated_backward", "pgemm_linear_workspace",
-            "pgemm_gated_workspace", "pgemm_linear_backward_workspace", "pgemm_gated_backward_workspace")
+            "pgemm_gated_workspace", "pgemm_linear_backward_workspace", "pgemm_gated_backward_workspace",
+            "pgemm_rms_norm", "pgemm_rms_norm_backward", "pgemm_rms_norm_backward_workspace", "pgemm_mx_quantize",
+            "pgemm_mx_dequantize", "pgemm_mx_linear", "pgemm_mx_gated", "pgemm_mx_linear_workspace",
+            "pgemm_mx_gated_workspace")
 
 
 class PgemmError(RuntimeError):
@@ -320,7 +344,7 @@ pgemm_gated_backward_workspace = _lib.pgemm_gated_backward_workspace
 
 
 class _Call:
-    """The checks that the four operators share, and their launch.
+    """The checks that the operators share, and their launch.
 
     An operator's checks of types, shapes, strides and devices depend on
     nothing else, so they run once for each combination of them: the operator
@@ -330,10 +354,10 @@ class _Call:
 
     __slots__ = ("dtype", "device", "index", "tensors", "pairs", "args", "need", "function")
 
-    def __init__(self, X):
+    def __init__(self, X, name="X"):
         code = _FLOAT_CODE.get(X.dtype)
         if code is None:
-            raise ValueError("X has unsupported dtype %s: float32, float16 or bfloat16 is needed" % X.dtype)
+            raise ValueError("%s has unsupported dtype %s: float32, float16 or bfloat16 is needed" % (name, X.dtype))
         self.dtype = code
         self.device = X.device
         self.index = X.device.index
@@ -394,6 +418,31 @@ class _Call:
             raise ValueError("%s must be a contiguous vector of %d, got %s" % (name, n, tuple(t.shape)))
         self._place(name, slot, t, dtypes, out)
 
+    def blocks(self, name, slots, Q, S, rows, filled=None, out=False):
+        """(ldq, lds, format, entries of a stored row) of `rows` rows of MX blocks; filled: how many entries those have to be."""
+        if Q is None:
+            return 0, 0, MX8, 0
+        for t, what, ok, align in ((Q, "codes", _CODE_TYPES, 16), (S, "scales", _SCALE_TYPES, 4)):
+            if t.dtype not in ok:
+                raise ValueError("%s: the %s must be %s, got %s" % (name, what, " or ".join(str(d) for d in ok), t.dtype))
+            if t.dim() != 2 or t.shape[0] != rows:
+                raise ValueError("%s: the %s are %s, the call needs %d rows" % (name, what, tuple(t.shape), rows))
+            s0, s1 = t.stride()
+            if t.numel() and ((s1 != 1 and t.shape[1] > 1) or (rows > 1 and (s0 < t.shape[1] or s0 % align))):
+                raise ValueError("%s: the %s must have unit column stride and rows a multiple of %d bytes apart, got "
+                                 "strides %s" % (name, what, align, (s0, s1)))
+        width, scales = Q.shape[1], S.shape[1]
+        entries = scales * 32
+        if scales % 8 or width not in (entries, entries // 2):
+            raise ValueError("%s: rows of %d bytes of codes and %d scales are no whole groups of 256 entries"
+                             % (name, width, scales))
+        if filled is not None and entries != filled:
+            raise ValueError("%s holds rows of %d entries, the call needs %d" % (name, entries, filled))
+        for t, slot in ((Q, slots[0]), (S, slots[1])):
+            self._place(name, slot, t, (t.dtype,), out)
+        return ((Q.stride(0) if rows > 1 else width), (S.stride(0) if rows > 1 else scales),
+                MX8 if width == entries else MX4, entries)
+
     def done(self, function, need, args):
         """`args(pointers)` gives the C function's arguments before the workspace."""
         self.function, self.need, self.args = function, need, args
@@ -404,7 +453,7 @@ class _Call:
     def _overlap(self, ts, i, j, same):
         """Raises unless the matrices at places i and j share no byte (their ranges do)."""
         x, y = ts[i], ts[j]
-        if same == (i, j) and x.data_ptr() == y.data_ptr() and x.stride() == y.stride():
+        if (i, j) in same and x.data_ptr() == y.data_ptr() and x.stride() == y.stride():
             return
         if x.dim() == 2 and y.dim() == 2:
             x, y = _stored_rows(x), _stored_rows(y)
@@ -414,8 +463,8 @@ class _Call:
         raise ValueError("%s and %s overlap: outputs must not share memory with inputs or each other"
                          % (names[i], names[j]))
 
-    def run(self, ts, workspace, stream, same=None):
-        """Launches on the tensors' GPU; `same`: places of an input and an output that may be one matrix."""
+    def run(self, ts, workspace, stream, same=()):
+        """Launches on the tensors' GPU; `same`: pairs of places, of an input and an output that may be one matrix."""
         p = [None if t is None else t.data_ptr() for t in ts]
         for i, bi, j, bj in self.pairs:
             if p[i] < p[j] + bj and p[j] < p[i] + bi:
@@ -488,6 +537,8 @@ try:
     _BY_CODE = {c: t for t, c in _FLOAT_CODE.items()}
     _OUT_TYPES = {c: (t,) if c == PGEMM_F32 else (t, torch.float32) for c, t in _BY_CODE.items()}
     _OWN_TYPE = {c: (t,) for c, t in _BY_CODE.items()}
+    _CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+    _SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
 except NameError:  # without torch only the C entry points above are used
@@ -532,7 +583,7 @@ def linear(X, W, Y, bias=None, residual=None, act="none", Z=None, workspace=None
     launched; a status the library returns raises PgemmError.  Returns Y.
     """
     ts = (X, W, Y, bias, residual, Z)
-    _cached(_describe_linear, ts, act).run(ts, workspace, stream, (2, 4))
+    _cached(_describe_linear, ts, act).run(ts, workspace, stream, ((2, 4),))
     return Y
 
 
@@ -670,6 +721,244 @@ def _describe_gated_backward(dH, X, Wg, Wu, G, U, dX, dWg, dWu, dbias_g, dbias_u
     return c.done(pgemm_gated_backward, pgemm_gated_backward_workspace(M, N, K, t), lambda p: (
         M, N, K, p[0], lddh, p[1], ldx, p[2], p[3], ldw, order, p[4], ldg, p[5], ldu, a, p[6], lddx, p[7], p[8],
         lddw, dorder, p[9], p[10], g, t))
+
+
+# ---- the norm and the microscaled operators ----------------------------------------------
+
+pgemm_rms_norm = _lib.pgemm_rms_norm
+pgemm_rms_norm_backward = _lib.pgemm_rms_norm_backward
+pgemm_rms_norm_backward_workspace = _lib.pgemm_rms_norm_backward_workspace
+pgemm_mx_quantize = _lib.pgemm_mx_quantize
+pgemm_mx_dequantize = _lib.pgemm_mx_dequantize
+pgemm_mx_linear = _lib.pgemm_mx_linear
+pgemm_mx_gated = _lib.pgemm_mx_gated
+pgemm_mx_linear_workspace = _lib.pgemm_mx_linear_workspace
+pgemm_mx_gated_workspace = _lib.pgemm_mx_gated_workspace
+
+
+def mx_empty(rows, K, format="mx4", device=None):
+    """(codes, scales) for `rows` rows of K entries in MX blocks, not yet written.
+
+    A row is stored in whole groups of 256 entries: codes, one a byte ("mx8") or
+    two ("mx4"), and one scale for 32 entries.
+    """
+    if format not in MX_FORMAT:
+        raise ValueError("unknown format %r: one of %s" % (format, ", ".join(MX_FORMAT)))
+    if rows < 0 or K < 0:
+        raise ValueError("sizes are not negative, got %d x %d" % (rows, K))
+    filled = -(-K // 256) * 256
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return (torch.empty(rows, filled if format == "mx8" else filled // 2, dtype=torch.uint8, device=device),
+            torch.empty(rows, filled // 32, dtype=torch.uint8, device=device))
+
+
+def _pair(name, mx, optional=False):
+    """Codes and scales of MX blocks."""
+    if mx is None and optional:
+        return None, None
+    try:
+        Q, S = mx
+    except (TypeError, ValueError):
+        Q = S = None
+    if not isinstance(Q, torch.Tensor) or not isinstance(S, torch.Tensor):
+        raise ValueError("%s must be a pair of tensors, codes and scales" % name)
+    return Q, S
+
+
+def _eps(eps):
+    try:
+        eps = float(eps)
+    except (TypeError, ValueError):
+        eps = -1.0
+    if not 0.0 <= eps <= 3e38:
+        raise ValueError("eps must be a finite number, not negative")
+    return eps
+
+
+def _matrix_sizes(name, t):
+    if t.dim() != 2:
+        raise ValueError("%s is %s: a matrix is needed" % (name, tuple(t.shape)))
+    return t.shape[0], t.shape[1]
+
+
+def rms_norm(X, weight=None, Y=None, residual=None, H=None, mx=None, eps=1e-6, stream=None):
+    """Y = h * weight / sqrt(mean(h * h) + eps) over rows, with h = X + residual.
+
+    X and residual are M x N, row-major with unit column stride, weight N (None:
+    one); float32, float16 or bfloat16, all of one type.  Y has X's type or
+    float32.  H, when given, receives h in X's type, which rms_norm_backward reads;
+    it may be X or residual itself.  mx, when given, is a pair (codes, scales) as of
+    mx_empty(M, N, "mx8" or "mx4") that receives Y in MX blocks, from its unrounded
+    values.  Sums are in fp32; every output is rounded once.
+
+    The call runs on the tensors' GPU, on torch's current stream there unless
+    `stream` is given, and does not synchronise.  Bad arguments raise ValueError
+    before anything is launched; a status the library returns raises PgemmError.
+    Returns Y (mx where Y is None).
+    """
+    ts = (X, weight, Y, residual, H) + _pair("mx", mx, True)
+    _cached(_describe_rms_norm, ts, _eps(eps)).run(ts, None, stream, ((0, 4), (3, 4)))
+    return mx if Y is None else Y
+
+
+def _describe_rms_norm(X, weight, Y, residual, H, Q, S, eps):
+    _required(X=X)
+    M, N = _matrix_sizes("X", X)
+    if Y is None and H is None and Q is None:
+        raise ValueError("one of Y, H and mx is needed")
+    c = _Call(X)
+    t, own = c.dtype, _OWN_TYPE[c.dtype]
+    ldx = c.rows("X", 0, X, (M, N), own)
+    c.vector("weight", 1, weight, N, own)
+    ldy = c.rows("Y", 2, Y, (M, N), _OUT_TYPES[t], True)
+    ldr = c.rows("residual", 3, residual, (M, N), own)
+    ldh = c.rows("H", 4, H, (M, N), own, True)
+    ldq, lds, form, _ = c.blocks("mx", (5, 6), Q, S, M, -(-N // 256) * 256, True)
+    out = t if Y is None else _FLOAT_CODE[Y.dtype]
+    return c.done(lambda *a: pgemm_rms_norm(*a[:-3], a[-1]), 0, lambda p: (
+        M, N, p[0], ldx, p[3], ldr, p[1], eps, p[4], ldh, p[2], ldy, out, p[5], ldq, p[6], lds, form, t))
+
+
+def rms_norm_backward(dY, H, weight=None, dH=None, dX=None, dweight=None, eps=1e-6, workspace=None, stream=None):
+    """Gradients of rms_norm for dY, the gradient at Y, into the tensors given.
+
+    H is what rms_norm wrote (X itself where there was no residual).  dX (M x N, H's
+    type) is the gradient at h, and so X's and the residual's alike; dH, when given,
+    is a gradient that arrives at h from elsewhere, as down the skip connection, and
+    is added to it; dX may be dH itself.  dweight (N) has H's type or float32.  What
+    is None is not computed.  Streams, workspace (pgemm_rms_norm_backward_workspace,
+    where dweight is given) and errors as for linear.  Returns (dX, dweight).
+    """
+    ts = (dY, H, weight, dH, dX, dweight)
+    _cached(_describe_rms_norm_backward, ts, _eps(eps)).run(ts, workspace, stream, ((3, 4),))
+    return dX, dweight
+
+
+def _describe_rms_norm_backward(dY, H, weight, dH, dX, dweight, eps):
+    _required(dY=dY, H=H)
+    M, N = _matrix_sizes("H", H)
+    c = _Call(H, "H")
+    t, own = c.dtype, _OWN_TYPE[c.dtype]
+    lddy = c.rows("dY", 0, dY, (M, N), own)
+    ldh = c.rows("H", 1, H, (M, N), own)
+    c.vector("weight", 2, weight, N, own)
+    lddh = c.rows("dH", 3, dH, (M, N), own)
+    lddx = c.rows("dX", 4, dX, (M, N), own, True)
+    c.vector("dweight", 5, dweight, N, _OUT_TYPES[t], True)
+    g = t if dweight is None else _FLOAT_CODE[dweight.dtype]
+    need = 0 if dweight is None else pgemm_rms_norm_backward_workspace(M, N, t)
+    return c.done(pgemm_rms_norm_backward, need, lambda p: (
+        M, N, p[0], lddy, p[1], ldh, p[2], eps, p[3], lddh, p[4], lddx, p[5], g, t))
+
+
+def mx_quantize(X, mx, stream=None):
+    """MX blocks of X's rows, into mx = (codes, scales) as of mx_empty(*X.shape, ...).
+
+    X is rows x K with unit stride along either axis: row-major, or the transposed
+    view of a K x rows matrix (a weight W stored K x N is quantised as W.t(), and so
+    are the weights of mx_linear laid out).  float32, float16 or bfloat16.  The
+    format follows from the codes' width.  Streams and errors as for rms_norm.
+    Returns mx.
+    """
+    ts = (X,) + _pair("mx", mx)
+    _cached(_describe_mx_quantize, ts, None).run(ts, None, stream)
+    return mx
+
+
+def _describe_mx_quantize(X, Q, S, _):
+    _required(X=X)
+    rows, K = _matrix_sizes("X", X)
+    c = _Call(X)
+    ldx, order = c.weight("X", 0, X, (rows, K), _OWN_TYPE[c.dtype])
+    ldq, lds, form, _ = c.blocks("mx", (1, 2), Q, S, rows, -(-K // 256) * 256, True)
+    # weight() calls rows of X[rows][K] K x N, of which the C entry's NK is the other one
+    order = ORDER_NK if order == ORDER_KN else ORDER_KN
+    return c.done(lambda *a: pgemm_mx_quantize(*a[:-3], a[-1]), 0, lambda p: (
+        rows, K, p[0], ldx, order, c.dtype, p[1], ldq, p[2], lds, form))
+
+
+def mx_dequantize(mx, X, stream=None):
+    """The values of MX blocks, mx = (codes, scales), into X: rows x K, K up to the entries stored.
+
+    X is row-major with unit column stride, float32, float16 or bfloat16; every value
+    is rounded once.  Streams and errors as for rms_norm.  Returns X.
+    """
+    ts = (X,) + _pair("mx", mx)
+    _cached(_describe_mx_dequantize, ts, None).run(ts, None, stream)
+    return X
+
+
+def _describe_mx_dequantize(X, Q, S, _):
+    _required(X=X)
+    rows, K = _matrix_sizes("X", X)
+    c = _Call(X)
+    ldx = c.rows("X", 0, X, (rows, K), _OWN_TYPE[c.dtype], True)
+    ldq, lds, form, _ = c.blocks("mx", (1, 2), Q, S, rows, -(-K // 256) * 256)
+    return c.done(lambda *a: pgemm_mx_dequantize(*a[:-3], a[-1]), 0, lambda p: (
+        rows, K, p[1], ldq, p[2], lds, form, p[0], ldx, c.dtype))
+
+
+def mx_linear(X, W, Y, bias=None, residual=None, act="none", workspace=None, stream=None):
+    """Y = act(X @ W.T + bias) + residual with X and W in MX blocks.
+
+    X is a pair (codes, scales) of M rows in MX8 or MX4, W one of N rows in MX4, both
+    of as many stored entries (as rms_norm and mx_quantize write them, zeros behind
+    the last one).  Y is M x N, row-major with unit column stride, float32, float16
+    or bfloat16; bias (N) and residual (M x N, which may be Y itself) have its type.
+    Activations as for linear.  Sums, bias, activation and residual are in fp32; Y is
+    rounded once.  Streams, workspace (pgemm_mx_linear_workspace) and errors as for
+    linear.  Returns Y.
+    """
+    ts = _pair("X", X) + _pair("W", W) + (Y, bias, residual)
+    _cached(_describe_mx_linear, ts, act).run(ts, workspace, stream, ((4, 6),))
+    return Y
+
+
+def _describe_mx_linear(XQ, XS, WQ, WS, Y, bias, residual, act):
+    _required(Y=Y)
+    M, N = _matrix_sizes("Y", Y)
+    c = _Call(Y, "Y")
+    t, own = c.dtype, _OWN_TYPE[c.dtype]
+    a = _act_code(act)
+    ldxq, ldxs, form, K = c.blocks("X", (0, 1), XQ, XS, M)
+    ldwq, ldws, wform, _ = c.blocks("W", (2, 3), WQ, WS, N, K)
+    if wform != MX4 and K:
+        raise ValueError("W must be in 4-bit blocks")
+    ldy = c.rows("Y", 4, Y, (M, N), own, True)
+    c.vector("bias", 5, bias, N, own)
+    ldr = c.rows("residual", 6, residual, (M, N), own)
+    return c.done(pgemm_mx_linear, pgemm_mx_linear_workspace(M, N, K, form), lambda p: (
+        M, N, K, p[0], ldxq, p[1], ldxs, form, p[2], ldwq, p[3], ldws, p[5], p[6], ldr, a, p[4], ldy, t))
+
+
+def mx_gated(X, Wg, Wu, H, bias_g=None, bias_u=None, act="silu", workspace=None, stream=None):
+    """H = act(X @ Wg.T + bias_g) * (X @ Wu.T + bias_u) with X and the weights in MX blocks.
+
+    As mx_linear, with two weights of the same strides, in one product kernel.
+    Returns H.
+    """
+    ts = _pair("X", X) + _pair("Wg", Wg) + _pair("Wu", Wu) + (H, bias_g, bias_u)
+    _cached(_describe_mx_gated, ts, act).run(ts, workspace, stream)
+    return H
+
+
+def _describe_mx_gated(XQ, XS, WgQ, WgS, WuQ, WuS, H, bias_g, bias_u, act):
+    _required(H=H)
+    M, N = _matrix_sizes("H", H)
+    c = _Call(H, "H")
+    t, own = c.dtype, _OWN_TYPE[c.dtype]
+    a = _act_code(act)
+    ldxq, ldxs, form, K = c.blocks("X", (0, 1), XQ, XS, M)
+    g, u = (c.blocks(n, s, Q, S, N, K) for n, s, Q, S in (("Wg", (2, 3), WgQ, WgS), ("Wu", (4, 5), WuQ, WuS)))
+    if g != u:
+        raise ValueError("Wg and Wu must have the same strides, got %s and %s" % (g[:2], u[:2]))
+    if g[2] != MX4 and K:
+        raise ValueError("Wg and Wu must be in 4-bit blocks")
+    ldh = c.rows("H", 6, H, (M, N), own, True)
+    c.vector("bias_g", 7, bias_g, N, own)
+    c.vector("bias_u", 8, bias_u, N, own)
+    return c.done(pgemm_mx_gated, pgemm_mx_gated_workspace(M, N, K, form), lambda p: (
+        M, N, K, p[0], ldxq, p[1], ldxs, form, p[2], p[4], g[0], p[3], p[5], g[1], p[7], p[8], a, p[6], ldh, t))
 
 
 def pgemm_hazard_copy_reduce(X, rows, cols, ldx, row_sums, reuse_wait, delay_wave=-1, delay_cycles=0, trace=None,

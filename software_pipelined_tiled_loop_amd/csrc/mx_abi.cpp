@@ -1,0 +1,365 @@
+// mx_abi.cpp -- C entry points of the norm and of the microscaled operators:
+// argument checks, the choice of kernels, workspaces and launches.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+
+#include "mx_variants.hpp"
+#include "pgemm.h"
+
+using namespace pgemm;
+
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffff00;
+constexpr int64_t kMaxLd = (int64_t)1 << 21;  // elements; bytes of codes and scales
+constexpr int kNumCU = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+int64_t smaller(int64_t a, int64_t b) { return a < b ? a : b; }
+int64_t elem_size(int dtype) { return dtype == PGEMM_F32 ? 4 : 2; }
+bool float_type(int dtype) { return dtype == PGEMM_F32 || dtype == PGEMM_F16 || dtype == PGEMM_BF16; }
+
+MxKernels kernels_for(int dtype) {
+    return dtype == PGEMM_F32 ? mx_kernels_f32() : dtype == PGEMM_F16 ? mx_kernels_f16() : mx_kernels_bf16();
+}
+
+#define PGEMM_TRY(x)                     \
+    do {                                 \
+        const int r_ = (x);              \
+        if (r_ != PGEMM_OK) return r_;   \
+    } while (0)
+
+int launched(const char* what, hipError_t e) {
+    if (e == hipSuccess) return PGEMM_OK;
+    std::fprintf(stderr, "pgemm: launch of %s failed: %s (%d)\n", what, hipGetErrorString(e), (int)e);
+    return PGEMM_ERR_HIP;
+}
+
+// Types and sizes that every operator checks.
+int check_sizes(int64_t rows, int64_t cols, int dtype) {
+    if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
+    if (rows < 0 || cols < 0) return PGEMM_ERR_INVALID_ARG;
+    return rows > kMaxDim || cols >= kMaxLd ? PGEMM_ERR_TOO_LARGE : PGEMM_OK;
+}
+// A matrix of `rows` rows of `cols` elements: 0, or the error.
+int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t es, bool needed) {
+    if (!p) return needed && rows > 0 && cols > 0 ? PGEMM_ERR_INVALID_ARG : PGEMM_OK;
+    if (ld < (cols > 1 ? cols : 1) || (uintptr_t)p % es) return PGEMM_ERR_INVALID_ARG;
+    return ld >= kMaxLd ? PGEMM_ERR_TOO_LARGE : PGEMM_OK;
+}
+int check_vector(const void* p, int64_t es) { return (uintptr_t)p % es ? PGEMM_ERR_INVALID_ARG : PGEMM_OK; }
+// Codes and scales of `rows` rows of K entries.
+int check_blocks(const void* Q, int64_t ldq, const void* S, int64_t lds, int64_t rows, int64_t K, int format) {
+    if (format != PGEMM_MX8 && format != PGEMM_MX4) return PGEMM_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return PGEMM_OK;
+    if (!Q || !S || (uintptr_t)Q % 16 || (uintptr_t)S % 4 || ldq % 16 || lds % 4) return PGEMM_ERR_INVALID_ARG;
+    if (ldq < mx_code_bytes(K, format) || lds < mx_filled(K) / kMxBlock) return PGEMM_ERR_INVALID_ARG;
+    return ldq >= kMaxLd || lds >= kMaxLd ? PGEMM_ERR_TOO_LARGE : PGEMM_OK;
+}
+int check_workspace(const void* p, int64_t bytes, int64_t need) {
+    if (need < 0) return (int)need;
+    return need > 0 && (!p || (uintptr_t)p % 16 || bytes < need) ? PGEMM_ERR_INVALID_ARG : PGEMM_OK;
+}
+
+// Workgroups for `items`, `per` at a time; kernels go on from there by themselves.
+int grid_for(int64_t items, int64_t per) { return (int)smaller(ceil_div(items, per), 1 << 20); }
+
+// ---- the norm ----------------------------------------------------------------------------------
+
+// The first kernel whose row holds `filled` columns.
+const NormVariant& norm_variant(const MxKernels& k, int64_t filled) {
+    int i = 0;
+    while (i + 1 < k.num_norms && (int64_t)k.norms[i].threads * k.norms[i].groups * 8 < filled) ++i;
+    return k.norms[i];
+}
+int64_t rows_at_once(const NormVariant& v) { return v.threads < 256 ? 256 / v.threads : 1; }
+
+// Blocks of rows of the backward pass: their sums are joined afterwards.
+struct NormBlocks {
+    int64_t rows, blocks, np8;
+};
+NormBlocks norm_blocks(int64_t M, int64_t N, const NormVariant& v) {
+    NormBlocks b;
+    const int64_t at_once = rows_at_once(v), most = 2 * kNumCU;
+    b.rows = round_up(ceil_div(M > 0 ? M : 1, most), at_once);
+    b.blocks = ceil_div(M, b.rows);
+    b.np8 = round_up(N, 8);
+    return b;
+}
+
+// ---- the products -------------------------------------------------------------------------------
+
+ActArgs act_args(int act) {
+    // -log2(e) * P(t); see ActArgs
+    constexpr double kLog2e = 1.4426950408889634;
+    ActArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.kind = act;
+    if (act == PGEMM_ACT_SILU) {
+        a.c[0] = (float)-kLog2e;
+    } else if (act == PGEMM_ACT_GELU_TANH) {
+        const double c = 1.5957691216057308;  // sqrt(8 / pi)
+        a.c[0] = (float)(-kLog2e * c);
+        a.c[1] = (float)(-kLog2e * c * 0.044715);
+    }
+    return a;
+}
+
+int64_t product_workspace(int64_t M, int64_t N, int64_t K, int format, int planes) {
+    (void)planes;
+    if (format != PGEMM_MX8 && format != PGEMM_MX4) return PGEMM_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0) return PGEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || N >= kMaxLd || K >= kMaxLd || ceil_div(M, 32) * ceil_div(N, 32) >= (int64_t)1 << 26) return PGEMM_ERR_TOO_LARGE;
+    return 0;
+}
+
+struct Product {
+    const void *XQ, *XS, *WQ[2], *WS[2];
+    int64_t ldxq, ldxs, ldwq, ldws;
+    const void *bias[2], *R;
+    int64_t ldr;
+    void* Y;
+    int64_t ldy;
+};
+
+int run_product(int64_t M, int64_t N, int64_t K, const Product& q, int format, int act, int dtype, int planes,
+                void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
+    const int64_t need = product_workspace(M, N, K, format, planes), es = elem_size(dtype);
+    if (need < 0) return (int)need;
+    if (act < PGEMM_ACT_NONE || act > PGEMM_ACT_GELU_TANH) return PGEMM_ERR_INVALID_ARG;
+    PGEMM_TRY(check_blocks(q.XQ, q.ldxq, q.XS, q.ldxs, N > 0 ? M : 0, K, format));
+    for (int p = 0; p < planes; ++p) {
+        PGEMM_TRY(check_blocks(q.WQ[p], q.ldwq, q.WS[p], q.ldws, M > 0 ? N : 0, K, PGEMM_MX4));
+        PGEMM_TRY(check_vector(q.bias[p], es));
+    }
+    PGEMM_TRY(check_matrix(q.R, M, N, q.ldr, es, false));
+    PGEMM_TRY(check_matrix(q.Y, M, N, q.ldy, es, true));
+    if (M == 0 || N == 0) return PGEMM_OK;
+    PGEMM_TRY(check_workspace(workspace, workspace_bytes, need));
+    MxArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.A = q.XQ;
+    a.SA = q.XS;
+    for (int p = 0; p < 2; ++p) {
+        a.B[p] = q.WQ[p];
+        a.SB[p] = q.WS[p];
+        a.e.bias[p] = q.bias[p];
+    }
+    a.lda = q.ldxq;
+    a.lsa = q.ldxs;
+    a.ldb = q.ldwq;
+    a.lsb = q.ldws;
+    a.filled = (int)mx_filled(K);
+    a.e.Y[0] = a.e.Y[1] = q.Y;
+    a.e.ldy = q.ldy;
+    a.e.R = q.R;
+    a.e.ldr = q.ldr;
+    a.e.act = act_args(act);
+    a.e.M = (int)M;
+    a.e.N = (int)N;
+    a.e.out_f32 = dtype == PGEMM_F32;
+    return launched("mx_product", kernels_for(dtype).product(a, format, planes == 2, (int)(ceil_div(M, 32) * ceil_div(N, 32)), stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t pgemm_rms_norm_backward_workspace(int64_t M, int64_t N, int dtype) {
+    PGEMM_TRY(check_sizes(M, N, dtype));
+    const NormBlocks b = norm_blocks(M, N, norm_variant(kernels_for(dtype), N));
+    return round_up(b.blocks * b.np8 * 4, 256);
+}
+
+int pgemm_rms_norm(int64_t M, int64_t N, const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight,
+                   double eps, void* H, int64_t ldh, void* Y, int64_t ldy, int out_dtype, void* Q, int64_t ldq, void* S,
+                   int64_t lds, int format, int dtype, void* stream) {
+    PGEMM_TRY(check_sizes(M, N, dtype));
+    if ((out_dtype != dtype && out_dtype != PGEMM_F32) || !(eps >= 0.0 && eps <= 3e38) || !Q != !S) return PGEMM_ERR_INVALID_ARG;
+    const int64_t es = elem_size(dtype);
+    PGEMM_TRY(check_matrix(X, M, N, ldx, es, true));
+    PGEMM_TRY(check_matrix(R, M, N, ldr, es, false));
+    PGEMM_TRY(check_vector(weight, es));
+    PGEMM_TRY(check_matrix(H, M, N, ldh, es, false));
+    PGEMM_TRY(check_matrix(Y, M, N, ldy, elem_size(out_dtype), false));
+    if (Q) PGEMM_TRY(check_blocks(Q, ldq, S, lds, M, N, format));
+    if (M == 0 || N == 0 || (!H && !Y && !Q)) return PGEMM_OK;
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.X = X;
+    a.R = R;
+    a.w = weight;
+    a.H = H;
+    a.Y = Y;
+    a.Q = Q;
+    a.S = S;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldh = ldh;
+    a.ldy = ldy;
+    a.ldq = ldq;
+    a.lds = lds;
+    a.eps = (float)eps;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.filled = (int)(Q ? mx_filled(N) : N);
+    a.y_f32 = out_dtype == PGEMM_F32;
+    a.format = format;
+    const NormVariant& v = norm_variant(kernels_for(dtype), a.filled);
+    return launched("rms_norm", v.norm(a, grid_for(M, rows_at_once(v)), (hipStream_t)stream));
+}
+
+int pgemm_rms_norm_backward(int64_t M, int64_t N, const void* dY, int64_t lddy, const void* H, int64_t ldh,
+                            const void* weight, double eps, const void* dH, int64_t lddh, void* dX, int64_t lddx,
+                            void* dweight, int grad_dtype, int dtype, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+    PGEMM_TRY(check_sizes(M, N, dtype));
+    if ((grad_dtype != dtype && grad_dtype != PGEMM_F32) || !(eps >= 0.0 && eps <= 3e38)) return PGEMM_ERR_INVALID_ARG;
+    const int64_t es = elem_size(dtype);
+    PGEMM_TRY(check_matrix(dY, M, N, lddy, es, dX || dweight));
+    PGEMM_TRY(check_matrix(H, M, N, ldh, es, dX || dweight));
+    PGEMM_TRY(check_vector(weight, es));
+    PGEMM_TRY(check_matrix(dH, M, N, lddh, es, false));
+    PGEMM_TRY(check_matrix(dX, M, N, lddx, es, false));
+    PGEMM_TRY(check_vector(dweight, elem_size(grad_dtype)));
+    if (N == 0 || (!dX && !dweight)) return PGEMM_OK;
+    if (dweight) PGEMM_TRY(check_workspace(workspace, workspace_bytes, pgemm_rms_norm_backward_workspace(M, N, dtype)));
+    const NormVariant& v = norm_variant(kernels_for(dtype), N);
+    const NormBlocks b = norm_blocks(M, N, v);
+    if (M > 0) {
+        NormGradArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.dY = dY;
+        a.H = H;
+        a.w = weight;
+        a.dH = dH;
+        a.dX = dX;
+        a.sums = dweight ? (float*)workspace : nullptr;
+        a.lddy = lddy;
+        a.ldh = ldh;
+        a.lddh = lddh;
+        a.lddx = lddx;
+        a.eps = (float)eps;
+        a.M = (int)M;
+        a.N = (int)N;
+        a.np8 = (int)b.np8;
+        a.rows = (int)b.rows;
+        PGEMM_TRY(launched("rms_norm_grad", v.grad(a, (int)b.blocks, (hipStream_t)stream)));
+    }
+    if (!dweight) return PGEMM_OK;
+    SumArgs t;
+    std::memset(&t, 0, sizeof(t));
+    t.sums = (const float*)workspace;
+    t.out[0] = dweight;
+    t.blocks = (int)b.blocks;
+    t.planes = 1;
+    t.np8 = (int)b.np8;
+    t.N = (int)N;
+    t.out_f32 = grad_dtype == PGEMM_F32;
+    const LinKernels k = dtype == PGEMM_F32 ? linear_kernels_f32() : dtype == PGEMM_F16 ? linear_kernels_f16() : linear_kernels_bf16();
+    return launched("linear_colsum", k.colsum(t, grid_for(N, 64), (hipStream_t)stream));
+}
+
+int pgemm_mx_quantize(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_order, int dtype, void* Q, int64_t ldq,
+                      void* S, int64_t lds, int format, void* stream) {
+    if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
+    if (rows < 0 || K < 0 || (x_order != PGEMM_KN && x_order != PGEMM_NK)) return PGEMM_ERR_INVALID_ARG;
+    if (rows > kMaxDim || K > kMaxDim) return PGEMM_ERR_TOO_LARGE;
+    if (x_order == PGEMM_KN) PGEMM_TRY(check_matrix(X, K, rows, ldx, elem_size(dtype), true));
+    else PGEMM_TRY(check_matrix(X, rows, K, ldx, elem_size(dtype), true));
+    PGEMM_TRY(check_blocks(Q, ldq, S, lds, rows, K, format));
+    if (rows == 0 || K == 0) return PGEMM_OK;
+    MxCopyArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.X = const_cast<void*>(X);
+    a.Q = Q;
+    a.S = S;
+    a.ldx = ldx;
+    a.ldq = ldq;
+    a.lds = lds;
+    a.rows = (int)rows;
+    a.K = (int)K;
+    a.filled = (int)mx_filled(K);
+    const bool columns = x_order == PGEMM_KN;
+    const int grid = columns ? grid_for(ceil_div(rows, 64) * (a.filled / 128), 1) : grid_for(rows * (a.filled / 8), 256);
+    return launched("mx_quantize", kernels_for(dtype).quantize(a, format, columns, grid, (hipStream_t)stream));
+}
+
+int pgemm_mx_dequantize(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* S, int64_t lds, int format,
+                        void* X, int64_t ldx, int dtype, void* stream) {
+    PGEMM_TRY(check_sizes(rows, K, dtype));
+    PGEMM_TRY(check_blocks(Q, ldq, S, lds, rows, K, format));
+    PGEMM_TRY(check_matrix(X, rows, K, ldx, elem_size(dtype), true));
+    if (rows == 0 || K == 0) return PGEMM_OK;
+    MxCopyArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.X = X;
+    a.Q = const_cast<void*>(Q);
+    a.S = const_cast<void*>(S);
+    a.ldx = ldx;
+    a.ldq = ldq;
+    a.lds = lds;
+    a.rows = (int)rows;
+    a.K = (int)K;
+    a.filled = (int)mx_filled(K);
+    return launched("mx_dequantize", kernels_for(dtype).dequantize(a, format, grid_for(rows * ceil_div(K, 8), 256), (hipStream_t)stream));
+}
+
+int64_t pgemm_mx_linear_workspace(int64_t M, int64_t N, int64_t K, int x_format) {
+    return product_workspace(M, N, K, x_format, 1);
+}
+int64_t pgemm_mx_gated_workspace(int64_t M, int64_t N, int64_t K, int x_format) {
+    return product_workspace(M, N, K, x_format, 2);
+}
+
+int pgemm_mx_linear(int64_t M, int64_t N, int64_t K, const void* XQ, int64_t ldxq, const void* XS, int64_t ldxs,
+                    int x_format, const void* WQ, int64_t ldwq, const void* WS, int64_t ldws, const void* bias,
+                    const void* R, int64_t ldr, int act, void* Y, int64_t ldy, int dtype, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+    Product q;
+    std::memset(&q, 0, sizeof(q));
+    q.XQ = XQ;
+    q.XS = XS;
+    q.ldxq = ldxq;
+    q.ldxs = ldxs;
+    q.WQ[0] = q.WQ[1] = WQ;
+    q.WS[0] = q.WS[1] = WS;
+    q.ldwq = ldwq;
+    q.ldws = ldws;
+    q.bias[0] = bias;
+    q.R = R;
+    q.ldr = ldr;
+    q.Y = Y;
+    q.ldy = ldy;
+    return run_product(M, N, K, q, x_format, act, dtype, 1, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+int pgemm_mx_gated(int64_t M, int64_t N, int64_t K, const void* XQ, int64_t ldxq, const void* XS, int64_t ldxs,
+                   int x_format, const void* WgQ, const void* WuQ, int64_t ldwq, const void* WgS, const void* WuS,
+                   int64_t ldws, const void* bias_g, const void* bias_u, int act, void* H, int64_t ldh, int dtype,
+                   void* workspace, int64_t workspace_bytes, void* stream) {
+    Product q;
+    std::memset(&q, 0, sizeof(q));
+    q.XQ = XQ;
+    q.XS = XS;
+    q.ldxq = ldxq;
+    q.ldxs = ldxs;
+    q.WQ[0] = WgQ;
+    q.WQ[1] = WuQ;
+    q.WS[0] = WgS;
+    q.WS[1] = WuS;
+    q.ldwq = ldwq;
+    q.ldws = ldws;
+    q.bias[0] = bias_g;
+    q.bias[1] = bias_u;
+    q.Y = H;
+    q.ldy = ldh;
+    return run_product(M, N, K, q, x_format, act, dtype, 2, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,10 @@
+// mx_f16.hip -- the norm and the microscaled operators on fp16 values.
+#include "mx_variants.hpp"
+
+namespace pgemm {
+
+static const NormVariant k_norms[] = {NORM_VARIANTS(DT_F16)};
+
+MxKernels mx_kernels_f16() { return MX_KERNELS(DT_F16, k_norms); }
+
+}  // namespace pgemm

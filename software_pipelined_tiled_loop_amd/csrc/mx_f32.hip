@@ -1,0 +1,10 @@
+// mx_f32.hip -- the norm and the microscaled operators on fp32 values.
+#include "mx_variants.hpp"
+
+namespace pgemm {
+
+static const NormVariant k_norms[] = {NORM_VARIANTS(DT_F32)};
+
+MxKernels mx_kernels_f32() { return MX_KERNELS(DT_F32, k_norms); }
+
+}  // namespace pgemm

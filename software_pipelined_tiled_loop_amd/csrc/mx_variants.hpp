@@ -1,0 +1,78 @@
+// mx_variants.hpp -- the compiled kernels of the norm and of the microscaled operators (host side).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "linear_variants.hpp"
+#include "mx_kernel.hpp"
+#include "norm_kernel.hpp"
+
+namespace pgemm {
+
+// The norm's kernels by the groups of eight columns that they hold: threads of a row, groups a thread.
+struct NormVariant {
+    int threads, groups;
+    hipError_t (*norm)(const NormArgs&, int grid, hipStream_t);
+    hipError_t (*grad)(const NormGradArgs&, int grid, hipStream_t);
+};
+
+struct MxKernels {
+    const NormVariant* norms;  // by capacity; the last one holds any row
+    int num_norms;
+    hipError_t (*quantize)(const MxCopyArgs&, int format, bool columns, int grid, hipStream_t);
+    hipError_t (*dequantize)(const MxCopyArgs&, int format, int grid, hipStream_t);
+    hipError_t (*product)(const MxArgs&, int format, bool gated, int grid, hipStream_t);
+};
+
+template <int D, int TPR, int CH>
+hipError_t launch_norm(const NormArgs& a, int grid, hipStream_t s) {
+    return lin_launch<NormArgs>(&rms_norm_rows<D, TPR, CH>, a, dim3(grid), norm_threads<TPR>, s);
+}
+template <int D, int TPR, int CH>
+hipError_t launch_norm_grad(const NormGradArgs& a, int grid, hipStream_t s) {
+    return lin_launch<NormGradArgs>(&rms_norm_grad<D, TPR, CH>, a, dim3(grid), norm_threads<TPR>, s);
+}
+template <int D>
+hipError_t launch_norm_long(const NormArgs& a, int grid, hipStream_t s) {
+    return lin_launch<NormArgs>(&rms_norm_long<D>, a, dim3(grid), 1024, s);
+}
+template <int D>
+hipError_t launch_norm_grad_long(const NormGradArgs& a, int grid, hipStream_t s) {
+    return lin_launch<NormGradArgs>(&rms_norm_grad_long<D>, a, dim3(grid), 1024, s);
+}
+template <int D, int F>
+hipError_t launch_quantize(const MxCopyArgs& a, bool columns, int grid, hipStream_t s) {
+    return columns ? lin_launch<MxCopyArgs>(&mx_quantize_columns<D, F>, a, dim3(grid), 256, s)
+                   : lin_launch<MxCopyArgs>(&mx_quantize_rows<D, F>, a, dim3(grid), 256, s);
+}
+template <int D>
+hipError_t launch_quantize_any(const MxCopyArgs& a, int format, bool columns, int grid, hipStream_t s) {
+    return format == MX8 ? launch_quantize<D, MX8>(a, columns, grid, s) : launch_quantize<D, MX4>(a, columns, grid, s);
+}
+template <int D>
+hipError_t launch_dequantize(const MxCopyArgs& a, int format, int grid, hipStream_t s) {
+    return format == MX8 ? lin_launch<MxCopyArgs>(&mx_dequantize_rows<D, MX8>, a, dim3(grid), 256, s)
+                         : lin_launch<MxCopyArgs>(&mx_dequantize_rows<D, MX4>, a, dim3(grid), 256, s);
+}
+template <int D>
+hipError_t launch_product(const MxArgs& a, int format, bool gated, int grid, hipStream_t s) {
+    if (gated)
+        return format == MX8 ? lin_launch<MxArgs>(&mx_simple<D, MX8, true>, a, dim3(grid), 64, s)
+                             : lin_launch<MxArgs>(&mx_simple<D, MX4, true>, a, dim3(grid), 64, s);
+    return format == MX8 ? lin_launch<MxArgs>(&mx_simple<D, MX8, false>, a, dim3(grid), 64, s)
+                         : lin_launch<MxArgs>(&mx_simple<D, MX4, false>, a, dim3(grid), 64, s);
+}
+
+#define NORM_VARIANT(D, TPR, CH) NormVariant{TPR, CH, &launch_norm<D, TPR, CH>, &launch_norm_grad<D, TPR, CH>}
+#define NORM_VARIANTS(D)                                                                                        \
+    NORM_VARIANT(D, 64, 1), NORM_VARIANT(D, 64, 2), NORM_VARIANT(D, 256, 1), NORM_VARIANT(D, 256, 2),           \
+        NORM_VARIANT(D, 1024, 1), NORM_VARIANT(D, 1024, 2), NormVariant{1024, 0, &launch_norm_long<D>, &launch_norm_grad_long<D>}
+#define MX_KERNELS(D, norms)                                                                                    \
+    MxKernels{norms, (int)(sizeof(norms) / sizeof(norms[0])), &launch_quantize_any<D>, &launch_dequantize<D>, &launch_product<D>}
+
+// Per type of the values, each in its own translation unit.
+MxKernels mx_kernels_f32();
+MxKernels mx_kernels_f16();
+MxKernels mx_kernels_bf16();
+
+}  // namespace pgemm
