@@ -109,12 +109,67 @@ ActArgs act_args(int act) {
     return a;
 }
 
+// A product's kernel and the splits of its contraction.
+struct Plan {
+    const MxVariant* v;
+    int64_t tiles_m, tiles_n, splits, np8, part_bytes;
+};
+
+// Estimated microseconds.
+double est_us(const MxVariant& v, int64_t M, int64_t N, int64_t filled, int64_t splits) {
+    const int64_t wgs = ceil_div(M, v.bm) * ceil_div(N, v.bn) * splits;
+    const int planes = v.gated ? 2 : 1;
+    const double kt = (double)ceil_div(filled / v.bk, splits) * v.bk;  // entries of a workgroup
+    double us;
+    if (v.few) {
+        const double bytes = kt * ((M < v.bm ? M : v.bm) * (v.format == MX8 ? 1.0 : 0.5) + v.bn * planes * 0.53);
+        us = 3.0 * ceil_div(wgs, 2 * kNumCU) + (double)ceil_div(wgs, kNumCU) * bytes / 20e3;
+    } else {
+        const bool large = v.bm == 256;
+        const double rate = (v.format == MX8 ? (large ? 2600e6 : 1300e6) : (large ? 5200e6 : 1600e6)) / kNumCU;
+        us = ceil_div(wgs, (int64_t)kNumCU) * (2.0 * v.bm * v.bn * planes * kt / rate + (large ? 17.0 : 6.0));
+    }
+    if (splits > 1) us += 5.0 + 0.29 * splits + 2.0 * splits * M * N * planes * 4.0 / 4.4e6;
+    return us;
+}
+
+// From sizes and format alone, so that the workspace functions and the calls agree.
+Plan plan_product(int64_t M, int64_t N, int64_t K, int format, int gated, int dtype) {
+    const MxKernels k = kernels_for(dtype);
+    const int64_t filled = mx_filled(K);
+    Plan best;
+    std::memset(&best, 0, sizeof(best));
+    double best_us = 0.0;
+    for (int i = 0; i < k.n; ++i) {
+        const MxVariant& v = k.v[i];
+        if (v.format != format || v.gated != gated) continue;
+        const int64_t tiles = ceil_div(M, v.bm) * ceil_div(N, v.bn);
+        if (round_up(tiles, 8) * v.threads >= (int64_t)1 << 32) continue;
+        for (int64_t s = 1; s <= 16; ++s) {
+            if (s > 1 && (s * (v.few ? v.few : 4) * v.bk > filled || tiles * s > 2 * kNumCU)) break;
+            const double us = est_us(v, M, N, filled, s);
+            if (best.v && us >= best_us) continue;
+            best_us = us;
+            best.v = &v;
+            best.splits = s;
+        }
+    }
+    if (!best.v) return best;
+    best.tiles_m = ceil_div(M, best.v->bm);
+    best.tiles_n = ceil_div(N, best.v->bn);
+    best.np8 = round_up(N, 8);
+    best.part_bytes = best.splits > 1 ? best.splits * (gated ? 2 : 1) * M * best.np8 * 4 : 0;
+    return best;
+}
+
 int64_t product_workspace(int64_t M, int64_t N, int64_t K, int format, int planes) {
-    (void)planes;
     if (format != PGEMM_MX8 && format != PGEMM_MX4) return PGEMM_ERR_INVALID_ARG;
     if (M < 0 || N < 0 || K < 0) return PGEMM_ERR_INVALID_ARG;
-    if (M > kMaxDim || N >= kMaxLd || K >= kMaxLd || ceil_div(M, 32) * ceil_div(N, 32) >= (int64_t)1 << 26) return PGEMM_ERR_TOO_LARGE;
-    return 0;
+    if (M > kMaxDim || N >= kMaxLd || K >= kMaxLd || ceil_div(M, 64) * ceil_div(N, 64) >= (int64_t)1 << 24)
+        return PGEMM_ERR_TOO_LARGE;
+    if (M == 0 || N == 0) return 0;
+    const Plan p = plan_product(M, N, K, format, planes == 2, PGEMM_BF16);  // the types have the same kernels
+    return p.v ? round_up(p.part_bytes, 256) : PGEMM_ERR_TOO_LARGE;
 }
 
 struct Product {
@@ -163,7 +218,24 @@ int run_product(int64_t M, int64_t N, int64_t K, const Product& q, int format, i
     a.e.M = (int)M;
     a.e.N = (int)N;
     a.e.out_f32 = dtype == PGEMM_F32;
-    return launched("mx_product", kernels_for(dtype).product(a, format, planes == 2, (int)(ceil_div(M, 32) * ceil_div(N, 32)), stream));
+    const Plan p = plan_product(M, N, K, format, planes == 2, dtype);
+    a.tiles_m = (int)p.tiles_m;
+    a.tiles_n = (int)p.tiles_n;
+    a.group_m = 4;
+    a.splits = (int)p.splits;
+    a.part = p.splits > 1 ? (float*)workspace : nullptr;
+    a.np8 = (int)p.np8;
+    PGEMM_TRY(launched("mx_product", p.v->launch(a, (int)round_up(p.tiles_m * p.tiles_n * p.splits, 8), stream)));
+    if (p.splits == 1) return PGEMM_OK;
+    LinArgs j;
+    std::memset(&j, 0, sizeof(j));
+    j.outs = 1;
+    j.splits = a.splits;
+    j.part = a.part;
+    j.np8 = a.np8;
+    j.e = a.e;
+    const MxKernels k = kernels_for(dtype);
+    return launched("linear_join", (planes == 2 ? k.join_gated : k.join)(j, (int)(ceil_div(N, kJoinCols) * M), stream));
 }
 
 }  // namespace

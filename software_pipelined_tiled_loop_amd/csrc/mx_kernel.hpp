@@ -18,6 +18,8 @@ namespace pgemm {
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
+__device__ __forceinline__ i32x8 two_chunks(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
 struct MxArgs {
     const void* A;      // activations' codes and scales
     const void* SA;
@@ -25,53 +27,667 @@ struct MxArgs {
     const void* SB[2];
     int64_t lda, lsa, ldb, lsb;  // bytes
     int filled;         // entries of a stored row: whole groups
+    int tiles_m, tiles_n, group_m;
+    int splits;         // workgroups that share one output tile's K tiles
+    float* part;        // fp32 sums of each split: [split][plane][M][np8]
+    int np8;
     EpiArgs e;
 };
 
-// e2m1 by F, 32 x 32 x 64.
-template <int F>
-__device__ __forceinline__ void mx_mfma32(f32x16& acc, const i32x8& x, const i32x8& w, int sx, int sw) {
-    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, F == MX8 ? 0 : 4, 0, sw, 0, sx);
+// LDS tile of codes: rows of KC 16-byte chunks.  A fragment is 32 rows at one chunk
+// (two chunks, for the two halves of the wave): the LDS serves the sixteen lanes of
+// a half that have the same parity at a time, so those rows' chunks are spread over
+// all sixteen places of their 256-byte lines.
+template <int KC>
+PGEMM_HD constexpr int mx_off(int row, int kc) {
+    if constexpr (KC == 8) return ((row >> 1) << 8) + ((((row & 1) * 8 + kc) ^ ((row >> 1) & 15)) << 4);
+    else return ((row >> 2) << 8) + ((((row & 3) * 4 + kc) ^ ((row >> 2) & 7)) << 4);
 }
-__device__ __forceinline__ i32x8 two_chunks(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+template <int KC>
+PGEMM_HD void mx_inv(int off, int& row, int& kc) {
+    const int line = off >> 8;
+    if constexpr (KC == 8) {
+        const int u = ((off >> 4) & 15) ^ (line & 15);
+        row = 2 * line + (u >> 3);
+        kc = u & 7;
+    } else {
+        const int u = ((off >> 4) & 15) ^ (line & 7);
+        row = 4 * line + (u >> 2);
+        kc = u & 3;
+    }
+}
 
-// A wave's 32 x 32 outputs, operands straight from memory.
-template <int D, int F, bool GATED>
-__global__ void __launch_bounds__(64) mx_simple(MxArgs g) {
-    const int tiles_n = (g.e.N + 31) / 32;
-    const int m0 = (int)blockIdx.x / tiles_n * 32, n0 = (int)blockIdx.x % tiles_n * 32;
-    const int lane = (int)threadIdx.x, r = lane & 31, half = lane >> 5;
-    const int64_t m = min(m0 + r, g.e.M - 1), n = min(n0 + r, g.e.N - 1);  // rows beyond the edge feed nothing that is stored
-    constexpr int NP = GATED ? 2 : 1;
-    f32x16 acc[NP];
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[p][i] = 0.0f;
-    const char* a = (const char*)g.A + m * g.lda;
-    const uint8_t* sa = (const uint8_t*)g.SA + m * g.lsa;
-    for (int s = 0; s < g.filled / 64; ++s) {
-        i32x8 x;
-        if constexpr (F == MX8) {
-            x = two_chunks(*(const i32x4*)(a + s * 64 + half * 16), *(const i32x4*)(a + s * 64 + 32 + half * 16));
-        } else {
-            x = two_chunks(*(const i32x4*)(a + s * 32 + half * 16), i32x4{0, 0, 0, 0});
-        }
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const i32x8 w = two_chunks(*(const i32x4*)((const char*)g.B[p] + n * g.ldb + s * 32 + half * 16), i32x4{0, 0, 0, 0});
-            mx_mfma32<F>(acc[p], x, w, sa[2 * s + half], ((const uint8_t*)g.SB[p])[n * g.lsb + 2 * s + half]);
+// F: the activations' format.  Tiles of BM rows by BN weights' rows (gated: half of
+// them of each weight), K tiles of 128 bytes of the activations' codes.
+template <int D, int F, int BM_, int BN_, int S_, int WGM_, int WGN_, bool GATED_>
+struct MxCfg {
+    static constexpr int Dt = D, Fmt = F, BM = BM_, BN = BN_, S = S_, WGM = WGM_, WGN = WGN_;
+    static constexpr bool GATED = GATED_;
+    static constexpr int ES = D == DT_F32 ? 4 : 2;  // of a value
+    static constexpr int BK = F == MX8 ? 128 : 256, NKS = BK / 64, Q = BK / 128;  // entries; K steps; dwords of scales a row
+    static constexpr int KCA = 8, KCB = F == MX8 ? 4 : 8;
+    static constexpr int NP = GATED ? 2 : 1, BNP = BN / NP;
+    static constexpr int NW = WGM * WGN, NT = 64 * NW;
+    static constexpr int WM = BM / WGM, WNP = BNP / WGN;
+    static constexpr int FM = WM / 32, FNP = WNP / 32, FN = FNP * NP;
+    static constexpr int A_BYTES = BM * KCA * 16, B_BYTES = BN * KCB * 16;
+    static constexpr int SA_BYTES = BM * Q * 4, SB_BYTES = BN * Q * 4;
+    static constexpr int AT_B = A_BYTES, AT_SA = A_BYTES + B_BYTES, AT_SB = AT_SA + SA_BYTES;
+    static constexpr int STAGE = AT_SB + SB_BYTES, LDS = S * STAGE;
+    static constexpr int MINW = 163840 / LDS * NW / 4;  // waves per SIMD, by the CU's LDS
+    // LDS-DMA pieces of a wave: codes 1 KiB at a time, scales 256 bytes
+    static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW;
+    static constexpr int S_INSTR = (SA_BYTES + SB_BYTES) / 256 / NW, LPS = A_INSTR + B_INSTR + S_INSTR;
+    static constexpr int XCH = F == MX8 ? 2 : 1;  // chunks of an activations' fragment
+    static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0 && NW % 4 == 0, "a wave's pieces lie in one operand");
+    static_assert(SA_BYTES % (256 * S_INSTR) == 0 && SB_BYTES % (256 * S_INSTR * NP) == 0 && BM % 64 == 0 && BNP % 64 == 0,
+                  "scale pieces");
+    static_assert(STAGE % 256 == 0 && LDS <= 163840 && S >= 2 && LPS * (S - 2) <= 63, "ring");
+};
+
+template <class C>
+struct MxFrags {
+    i32x4 a[C::FM][C::XCH];
+    i32x4 b[C::FN];
+};
+template <class C>
+struct MxScales {
+    int a[C::FM], b[C::FN];
+};
+
+// A scaled MFMA with the accumulators in AGPRs, from inline asm (as mfma_lone):
+// weights times activations, byte KS of each side's scales.
+template <class C, int KS>
+__device__ __forceinline__ void mx_mfma(f32x16& acc, const i32x4 (&x)[C::XCH], const i32x4& w, int sx, int sw) {
+    if constexpr (C::Fmt == MX8) {
+        const i32x8 xx = two_chunks(x[0], x[1]);
+        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[%6,%6,0] cbsz:4"
+                     : "+a"(acc)
+                     : "v"(w), "v"(xx), "v"(sw), "v"(sx), "n"(KS & 1), "n"(KS >> 1));
+    } else {
+        asm volatile(
+            "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[%6,%6,0] cbsz:4 blgp:4"
+            : "+a"(acc)
+            : "v"(w), "v"(x[0]), "v"(sw), "v"(sx), "n"(KS & 1), "n"(KS >> 1));
+    }
+}
+
+// Fragment chunk of K step ks that a lane of half g reads.  MX4: block 4 g + ks of
+// the row's eight.  MX8, blocks 0 .. 3, two a step (ks and 2 + ks): the
+// activations' piece g of each, the weights' block 2 g + ks.
+template <class C>
+PGEMM_HD int mx_chunk_a(int ks, int g, int c) { return C::Fmt == MX8 ? 4 * c + 2 * ks + g : 4 * g + ks; }
+template <class C>
+PGEMM_HD int mx_chunk_b(int ks, int g) { return C::Fmt == MX8 ? 2 * g + ks : 4 * g + ks; }
+
+// Reads of a K step's fragments in the order in which its MFMAs need them.
+template <class C, int R>
+__device__ __forceinline__ void mx_read(const char PGEMM_LDS* st, int ks, int wm0, int wn0, int lane, MxFrags<C>& f) {
+    constexpr int XA = C::FM * C::XCH;
+    const int r = lane & 31, g = lane >> 5;
+    // b0, a0 (its chunks), the other b, the other a
+    if constexpr (R == 0 || (R > C::XCH && R < C::XCH + C::FN)) {
+        constexpr int j = R == 0 ? 0 : R - C::XCH;
+        constexpr int panel = j / C::FNP;
+        const int row = panel * C::BNP + wn0 + 32 * (j % C::FNP) + r;
+        f.b[j] = *(const i32x4 PGEMM_LDS*)(st + C::AT_B + mx_off<C::KCB>(row, mx_chunk_b<C>(ks, g)));
+    } else {
+        constexpr int x = R <= C::XCH ? R - 1 : R - C::FN;
+        static_assert(x >= 0 && x < XA, "reads");
+        constexpr int i = x / C::XCH, c = x % C::XCH;
+        f.a[i][c] = *(const i32x4 PGEMM_LDS*)(st + mx_off<C::KCA>(wm0 + 32 * i + r, mx_chunk_a<C>(ks, g, c)));
+    }
+}
+// Scales of a K tile: MX4 the four bytes of blocks 4 g .. 4 g + 3, MX8 those of blocks 2 g, 2 g + 1.
+template <class C, int R>
+__device__ __forceinline__ void mx_read_scale(const char PGEMM_LDS* st, int wm0, int wn0, int lane, MxScales<C>& s) {
+    const int r = lane & 31, g = lane >> 5;
+    const auto get = [&](const char PGEMM_LDS* base, int rows, int row) -> int {
+        if constexpr (C::Fmt == MX8) return *(const unsigned short PGEMM_LDS*)(base + row * 4 + 2 * g);
+        else return *(const int PGEMM_LDS*)(base + (g * rows + row) * 4);
+    };
+    if constexpr (R < C::FN) {
+        constexpr int panel = R / C::FNP;
+        s.b[R] = get(st + C::AT_SB + panel * (C::SB_BYTES / C::NP), C::BNP, wn0 + 32 * (R % C::FNP) + r);
+    } else {
+        s.a[R - C::FN] = get(st + C::AT_SA, C::BM, wm0 + 32 * (R - C::FN) + r);
+    }
+}
+
+// Fragments and scales of the first K tile's first step.
+template <class C, int R = 0>
+__device__ __forceinline__ void mx_first(const char PGEMM_LDS* st, int wm0, int wn0, int lane, MxFrags<C>& f, MxScales<C>& s) {
+    constexpr int NR = C::FM * C::XCH + C::FN;
+    if constexpr (R < NR) mx_read<C, R>(st, 0, wm0, wn0, lane, f);
+    if constexpr (R < C::FM + C::FN) mx_read_scale<C, R>(st, wm0, wn0, lane, s);
+    if constexpr (R < NR) mx_first<C, R + 1>(st, wm0, wn0, lane, f, s);
+}
+
+// The wave's side of the producer.
+template <class C>
+struct MxSrc {
+    i32x4 ra, rb, rs;  // next K tile of the codes, and of the scales that the wave loads
+    int64_t back_a, back_b, back_s;  // from behind the last K tile to the first
+    int turn;          // K tiles until the row's end
+    int left;          // K tiles still to load
+    uint32_t va[C::A_INSTR], vb[C::B_INSTR], vs[C::S_INSTR];
+
+    static __device__ __forceinline__ void move(i32x4& r, int64_t by) {
+        const uint64_t p = (((uint64_t)(uint32_t)r[1] << 32) | (uint32_t)r[0]) + (uint64_t)by;
+        r[0] = (int)(uint32_t)p;
+        r[1] = (int)(uint32_t)(p >> 32);  // the address stays below 2^48: the stride field stays zero
+    }
+    // On to the next K tile; slots past the last one get an empty range: every lane reads zeros.
+    template <int PART>
+    __device__ __forceinline__ void advance() {
+        if constexpr (PART == 0) {
+            --left;
+            ra[2] = rb[2] = rs[2] = left > 0 ? (int)0x80000000u : 0;
+        } else if constexpr (PART == 1) {
+            move(ra, 16 * C::KCA);
+            --turn;
+        } else if constexpr (PART == 2) {
+            move(rb, 16 * C::KCB);
+        } else if constexpr (PART == 3) {
+            move(rs, C::BK / 32);
+        } else if (turn == 0) {
+            move(ra, back_a);
+            move(rb, back_b);
+            move(rs, back_s);
         }
     }
-    const Epi<D, GATED> ep(g.e, m0, n0, 0, r, 0);
-    with_act(g.e.act.kind, [&](auto kind) {
-        constexpr int KIND = decltype(kind)::value;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int c = 8 * (i / 4) + 4 * half + i % 4;
-            if (c < ep.valid(0)) ep.template put1<KIND>(0, c, acc[0][i], acc[NP - 1][i]);
+    static constexpr int PARTS = 5;
+    __device__ __forceinline__ void advance_all() {
+        advance<0>();
+        advance<1>();
+        advance<2>();
+        advance<3>();
+        advance<4>();
+    }
+    // Piece I of the K tile, to LDS: its place (M0), and the load, which needs an instruction between them.
+    template <int I>
+    __device__ __forceinline__ void place(uint32_t a, uint32_t b, uint32_t s) const {
+        constexpr int B0 = C::A_INSTR, S0 = B0 + C::B_INSTR;
+        constexpr uint32_t off = I < B0 ? I * 1024u : I < S0 ? (I - B0) * 1024u : (I - S0) * 256u;
+        asm volatile("s_add_u32 m0, %0, %1" : : "s"(I < B0 ? a : I < S0 ? b : s), "n"(off) : "m0", "scc");
+    }
+    template <int I>
+    __device__ __forceinline__ void load() const {
+        constexpr int B0 = C::A_INSTR, S0 = B0 + C::B_INSTR;
+        if constexpr (I < S0) {
+            asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds"
+                         :
+                         : "v"(I < B0 ? va[I < B0 ? I : 0] : vb[I < B0 ? 0 : I - B0]), "s"(I < B0 ? ra : rb)
+                         : "memory");
+        } else {
+            asm volatile("buffer_load_dword %0, %1, 0 offen lds" : : "v"(vs[I - S0]), "s"(rs) : "memory");
         }
-    });
+    }
+};
+template <class C, int I = 0>
+__device__ __forceinline__ void mx_pieces(const MxSrc<C>& s, uint32_t a, uint32_t b, uint32_t c) {
+    if constexpr (I < C::LPS) {
+        s.template place<I>(a, b, c);
+        asm volatile("s_nop 0");
+        s.template load<I>();
+        mx_pieces<C, I + 1>(s, a, b, c);
+    }
+}
+
+// One K step, with what else is to be done spread evenly between its MFMAs: READS
+// reads of the next step's fragments (of the next K tile's first step: its scales
+// too), with DMA the next K tile's pieces, two instructions each, without it the
+// producer's way to that K tile.
+template <class C, int KS, bool LAST>
+struct MxStep {
+    static constexpr int NMF = C::FM * C::FN, NR = C::FM * C::XCH + C::FN, NS = LAST ? C::FM + C::FN : 0;
+    static constexpr int MORE = LAST ? 2 * C::LPS : KS == 0 ? MxSrc<C>::PARTS : 0, JOBS = NR + NS + MORE;
+    template <int J>
+    static __device__ __forceinline__ void job(const char PGEMM_LDS* st, MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src,
+                                               uint32_t a, uint32_t b, uint32_t s, int wm0, int wn0, int lane) {
+        if constexpr (J < NR) {
+            mx_read<C, J>(st, LAST ? 0 : KS + 1, wm0, wn0, lane, nxt);
+        } else if constexpr (J < NR + NS) {
+            mx_read_scale<C, J - NR>(st, wm0, wn0, lane, sc);
+        } else if constexpr (LAST) {
+            constexpr int P = (J - NR - NS) / 2;
+            if constexpr ((J - NR - NS) % 2 == 0) src.template place<P>(a, b, s);
+            else src.template load<P>();
+        } else {
+            src.template advance<J - NR - NS>();
+        }
+    }
+    template <int J, int END>
+    static __device__ __forceinline__ void jobs(const char PGEMM_LDS* st, MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src,
+                                                uint32_t a, uint32_t b, uint32_t s, int wm0, int wn0, int lane) {
+        if constexpr (J < END) {
+            job<J>(st, nxt, sc, src, a, b, s, wm0, wn0, lane);
+            // (M0 and the load that uses it stand in one place: an instruction between them)
+            if constexpr (LAST && J >= NR + NS && (J - NR - NS) % 2 == 0 && J + 1 < END) asm volatile("s_nop 0");
+            jobs<J + 1, END>(st, nxt, sc, src, a, b, s, wm0, wn0, lane);
+        }
+    }
+    template <int M = 0>
+    static __device__ __forceinline__ void run(f32x16 (&acc)[C::FM][C::FN], const MxFrags<C>& use, const MxScales<C>& us,
+                                               MxFrags<C>& nxt, MxScales<C>& sc, const char PGEMM_LDS* st, MxSrc<C>& src,
+                                               uint32_t a, uint32_t b, uint32_t s, int wm0, int wn0, int lane) {
+        if constexpr (M < NMF) {
+            constexpr int i = M / C::FN, j = M % C::FN;
+            mx_mfma<C, KS>(acc[i][j], use.a[i], use.b[j], us.a[i], us.b[j]);
+            jobs<M * JOBS / NMF, (M + 1) * JOBS / NMF>(st, nxt, sc, src, a, b, s, wm0, wn0, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            run<M + 1>(acc, use, us, nxt, sc, st, src, a, b, s, wm0, wn0, lane);
+        }
+    }
+};
+// All K steps of one K tile, the ready edge of the next one before the last.
+template <class C, int KS = 0>
+__device__ __forceinline__ void mx_tile_steps(f32x16 (&acc)[C::FM][C::FN], MxFrags<C> (&f)[2], const MxScales<C>& us,
+                                              MxScales<C>& sc, const char PGEMM_LDS* cur, const char PGEMM_LDS* next,
+                                              MxSrc<C>& src, uint32_t a, uint32_t b, uint32_t s, int wm0, int wn0,
+                                              int lane) {
+    if constexpr (KS < C::NKS - 1) {
+        MxStep<C, KS, false>::run(acc, f[KS & 1], us, f[(KS & 1) ^ 1], sc, cur, src, 0, 0, 0, wm0, wn0, lane);
+        mx_tile_steps<C, KS + 1>(acc, f, us, sc, cur, next, src, a, b, s, wm0, wn0, lane);
+    } else {
+        wait_barrier<C::LPS*(C::S - 2)>();  // the next K tile is in LDS, this one's stage is free
+        MxStep<C, KS, true>::run(acc, f[KS & 1], us, f[(KS & 1) ^ 1], sc, next, src, a, b, s, wm0, wn0, lane);
+    }
+}
+
+// The epilogue through LDS: as LinOut and lin_epilogue, on blocks of 32 x 32.
+template <class C>
+struct MxOut {
+    static constexpr int WN = C::FN * 32, NCHK = WN / 4;     // sums of a row; in 16-byte chunks
+    static constexpr int AREA = C::LDS / C::NW / 16 * 16;    // bytes of a wave
+    static constexpr int FIT = AREA / (WN * 4) / 32;         // 32-row blocks that fit
+    static constexpr int BLOCKS = FIT < C::FM ? FIT : C::FM;  // of a pass
+    static constexpr int PASSES = C::FM / BLOCKS;
+    static constexpr int LPR = C::WNP / 8;                   // lanes of a row
+    static constexpr int RPI = 64 / LPR;                     // rows at a time
+    static constexpr int STEPS = BLOCKS * 32 / RPI;
+    static constexpr int WANT = C::ES == 4 ? (C::GATED ? 1 : 2) : C::GATED ? 2 : 4;
+    static constexpr int UNROLL = STEPS < WANT ? STEPS : WANT;
+    static_assert(BLOCKS > 0 && PASSES * BLOCKS == C::FM && STEPS % UNROLL == 0 && (NCHK & (NCHK - 1)) == 0, "passes");
+    static PGEMM_HD int at(int row, int chunk) {
+        return (row * NCHK + (chunk & 1) * (NCHK / 2) + ((chunk >> 1) ^ (row & (NCHK / 2 - 1)))) * 16;
+    }
+};
+
+template <class C>
+__device__ __forceinline__ void mx_epilogue(const EpiArgs& e, int m0, int n0, char PGEMM_LDS* smem,
+                                            f32x16 (&acc)[C::FM][C::FN], int wave, int lane, int wm0, int wn0) {
+    typedef MxOut<C> O;
+    typedef Epi<C::Dt, C::GATED> E;
+    const int r0 = lane / O::LPR, c8 = lane % O::LPR;
+    const E ep(e, m0, n0, 0, wm0 + r0, wn0 + 8 * c8);
+    char PGEMM_LDS* area = smem + wave * O::AREA;
+    const f32x8 b0 = ep.bias(0), b1 = C::GATED ? ep.bias(1) : b0;
+    typename E::Raw next[O::UNROLL];
+    const auto fetch = [&](int by) {
+        if (!e.R || !ep.same()) return;
+#pragma unroll
+        for (int q = 0; q < O::UNROLL; ++q) next[q] = ep.residual(by + q * O::RPI);
+    };
+    fetch(0);
+    drain_barrier();  // the ring's memory is free
+#pragma unroll 1
+    for (int pass = 0; pass < O::PASSES; ++pass) {
+#pragma unroll
+        for (int p = 0; p < O::PASSES; ++p) {
+            if (p != pass) continue;
+#pragma unroll
+            for (int i = 0; i < O::BLOCKS; ++i)
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x16& a = acc[p * O::BLOCKS + i][j];
+                        *(f32x4 PGEMM_LDS*)(area + O::at(32 * i + (lane & 31), 8 * j + 2 * q + (lane >> 5))) =
+                            f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+                    }
+        }
+        asm volatile("" ::: "memory");  // a wave's LDS operations stay in order
+        const int down = pass * O::BLOCKS * 32;
+        with_act(e.act.kind, [&](auto kind) {
+            constexpr int KIND = decltype(kind)::value;
+#pragma unroll 1
+            for (int s = 0; s < O::STEPS; s += O::UNROLL) {
+                typename E::Raw res[O::UNROLL];
+                f32x8 v[O::UNROLL], w[C::GATED ? O::UNROLL : 1];
+#pragma unroll
+                for (int q = 0; q < O::UNROLL; ++q) res[q] = next[q];
+                fetch(down + (s + O::UNROLL) * O::RPI);
+#pragma unroll
+                for (int q = 0; q < O::UNROLL; ++q) {
+                    const int row = r0 + (s + q) * O::RPI;
+                    const auto sums = [&](int c) {
+                        return join8(*(const f32x4 PGEMM_LDS*)(area + O::at(row, c)),
+                                     *(const f32x4 PGEMM_LDS*)(area + O::at(row, c + 1)));
+                    };
+                    v[q] = sums(2 * c8);
+                    if constexpr (C::GATED) w[q] = sums(C::WNP / 4 + 2 * c8);
+                }
+                ep.template put<KIND>(down + s * O::RPI, O::RPI, v, w, b0, b1, res);
+            }
+            if (cols_cut(e.N)) {
+#pragma unroll 1
+                for (int s = 0; s < O::STEPS; ++s) {
+                    const int n = ep.valid(down + s * O::RPI);
+#pragma unroll 1
+                    for (int x = 0; x < (n < 8 ? n : 0); ++x) {
+                        const auto one = [&](int c) {
+                            return *(const float PGEMM_LDS*)(area + O::at(r0 + s * O::RPI, c >> 2) + 4 * (c & 3));
+                        };
+                        ep.template put1<KIND>(down + s * O::RPI, x, one(8 * c8 + x),
+                                               C::GATED ? one(C::WNP + 8 * c8 + x) : 0.0f);
+                    }
+                }
+            }
+        });
+        asm volatile("" ::: "memory");
+    }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS];
+    char PGEMM_LDS* smem = (char PGEMM_LDS*)smem_raw;
+
+    const int per_split = g.tiles_m * g.tiles_n;
+    const WgTiles w = wg_tiles_of(per_split * g.splits, (int)blockIdx.x, (int)gridDim.x);
+    if (w.count == 0) return;
+    int L = w.start + w.lb, split = 0;
+    if (g.splits > 1) {
+        split = __builtin_amdgcn_readfirstlane(L / per_split);
+        L -= split * per_split;
+    }
+    int tm, tn;
+    raster(L, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    const int m0 = tm * C::BM, n0 = tn * C::BNP;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm0 = (wave / C::WGN) * C::WM, wn0 = (wave % C::WGN) * C::WNP;
+    const int rows_left = g.e.M - m0, cols_left = g.e.N - n0;
+
+    f32x16 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) acc[i][j][x] = 0.0f;
+    acc_settle();
+
+    // This split's K tiles [t0, t1).
+    const int total = g.filled / C::BK;
+    const int t0 = (int)((int64_t)total * split / g.splits), t1 = (int)((int64_t)total * (split + 1) / g.splits);
+    if (t1 > t0) {
+        MxSrc<C> src;
+        // With the whole contraction in one go the XCDs begin at different places of it (see linear_kernel).
+        const int x = blockIdx.x & 7;
+        const int first = g.splits == 1 ? (int)((int64_t)total * (((x & 6) + 4 * (x & 1)) & 7) >> 3) : t0;
+        src.turn = total - first;
+        src.left = t1 - t0;
+        src.back_a = -(int64_t)total * 16 * C::KCA;
+        src.back_b = -(int64_t)total * 16 * C::KCB;
+        src.back_s = -(int64_t)total * (C::BK / 32);
+        const int panel = C::NP == 2 ? wave / (C::NW / 2) : 0;  // the wave's pieces of B lie in one panel
+        const int b_block = wave * C::B_INSTR - panel * (C::B_BYTES / C::NP / 1024);
+        src.ra = make_rsrc_sgpr((const char*)g.A + m0 * g.lda + first * (16 * C::KCA));
+        src.rb = make_rsrc_sgpr((const char*)(panel ? g.B[1] : g.B[0]) + n0 * g.ldb + first * (16 * C::KCB));
+#pragma unroll
+        for (int q = 0; q < C::A_INSTR; ++q) {
+            int row, kc;
+            mx_inv<C::KCA>((wave * C::A_INSTR + q) * 1024 + lane * 16, row, kc);
+            src.va[q] = row < rows_left ? (uint32_t)(row * (int)g.lda + kc * 16) : OOB;
+        }
+#pragma unroll
+        for (int q = 0; q < C::B_INSTR; ++q) {
+            int row, kc;
+            mx_inv<C::KCB>((b_block + q) * 1024 + lane * 16, row, kc);
+            src.vb[q] = row < cols_left ? (uint32_t)(row * (int)g.ldb + kc * 16) : OOB;
+        }
+        // scales: pieces of 64 rows' dwords, [Q][rows] of the activations, then of each panel of the weights
+        constexpr int A_PIECES = C::SA_BYTES / 256, P_PIECES = C::SB_BYTES / C::NP / 256;
+        const int piece = wave * C::S_INSTR;
+        const bool of_a = piece < A_PIECES;
+        const int s_panel = of_a ? 0 : (piece - A_PIECES) / P_PIECES;
+        src.rs = make_rsrc_sgpr((of_a ? (const char*)g.SA + m0 * g.lsa
+                                      : (const char*)(s_panel ? g.SB[1] : g.SB[0]) + n0 * g.lsb) + first * (C::BK / 32));
+#pragma unroll
+        for (int q = 0; q < C::S_INSTR; ++q) {
+            const int p = (of_a ? piece : piece - A_PIECES - s_panel * P_PIECES) + q, blocks = (of_a ? C::BM : C::BNP) / 64;
+            const int row = p % blocks * 64 + lane, dw = p / blocks;
+            src.vs[q] = row < (of_a ? rows_left : cols_left) ? (uint32_t)(row * (int)(of_a ? g.lsa : g.lsb) + dw * 4) : OOB;
+        }
+
+        const uint32_t lds0 = (uint32_t)(size_t)smem;
+        const uint32_t at_a = wave * C::A_INSTR * 1024, at_b = C::AT_B + wave * C::B_INSTR * 1024;
+        const uint32_t at_s = C::AT_SA + piece * 256;
+        // Prologue: slots 0 .. S-2.
+#pragma unroll
+        for (int p = 0; p < C::S - 1; ++p) {
+            mx_pieces<C>(src, lds0 + p * C::STAGE + at_a, lds0 + p * C::STAGE + at_b, lds0 + p * C::STAGE + at_s);
+            src.advance_all();
+        }
+        wait_barrier<C::LPS*(C::S - 2)>();
+        constexpr uint32_t LASTST = (C::S - 1) * C::STAGE;
+        mx_pieces<C>(src, lds0 + LASTST + at_a, lds0 + LASTST + at_b, lds0 + LASTST + at_s);
+        MxFrags<C> f[2];
+        MxScales<C> sc, next;
+        mx_first<C>(smem, wm0, wn0, lane, f[0], sc);
+        int cur = 0;
+        for (int t = t0; t < t1; ++t) {
+            // the last K step's copies of the scales, two wait states before the first MFMA
+            asm volatile("s_nop 1");
+            const int nst = cur + 1 == C::S ? 0 : cur + 1;
+            const uint32_t freed = lds0 + cur * C::STAGE;
+            mx_tile_steps<C>(acc, f, sc, next, smem + cur * C::STAGE, smem + nst * C::STAGE, src, freed + at_a, freed + at_b,
+                             freed + at_s, wm0, wn0, lane);
+            sc = next;
+            cur = nst;
+        }
+        __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing LDS
+    }
+    acc_settle();
+
+    if (g.part) {
+        // fp32 sums of this split, joined by linear_join in the order of the splits
+        float* base = g.part + (int64_t)split * C::NP * g.e.M * g.np8;
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+            const int row = m0 + wm0 + 32 * i + (lane & 31);
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int col = n0 + wn0 + 32 * (j % C::FNP) + 8 * q + 4 * (lane >> 5);
+                    const f32x16& a = acc[i][j];
+                    if (row < g.e.M && col < g.np8)
+                        *(f32x4*)(base + ((int64_t)(j / C::FNP) * g.e.M + row) * g.np8 + col) =
+                            f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+                }
+        }
+        return;
+    }
+    mx_epilogue<C>(g.e, m0, n0, smem, acc, wave, lane, wm0, wn0);
+}
+
+// ---- few rows -----------------------------------------------------------------------------------
+
+// One token to a few dozen: bound by the weights' bytes.  The waves of a workgroup
+// share its outputs (16 FM rows, 16 FN columns) and deal out the rows' units of 256
+// entries in turn.  A wave takes its operands straight from memory to registers,
+// as the 16 x 16 x 128 instruction wants them: of lane l = 16 g + r, row r, the
+// unit's step j (128 entries) of the weights chunk 4 j + g, of MX8 activations the
+// pieces g and 4 + g of the step's 128 bytes, and the scale byte 4 j + g.  U units are under way: one is
+// fetched anew as soon as it has been multiplied.  At the end the waves' sums are
+// added in LDS, in the order of the waves.
+template <int D, int F, int FM_, int FN_, int NW_, int U_, bool GATED_>
+struct MxFewCfg {
+    static constexpr int Dt = D, Fmt = F, FM = FM_, FNP = FN_, NW = NW_, U = U_;
+    static constexpr bool GATED = GATED_;
+    static constexpr int NP = GATED ? 2 : 1, FN = FNP * NP, NCOLP = 16 * FNP;
+    static constexpr int BM = 16 * FM, NT = 64 * NW, XCH = F == MX8 ? 2 : 1;
+    static constexpr int UA = F == MX8 ? 256 : 128, UB = 128;  // bytes of a unit's row
+    static constexpr int LDS = NW * FM * FN * 1024;
+    static_assert(LDS <= 163840, "sums");
+};
+template <class C>
+struct MxUnit {
+    i32x4 a[C::FM][2][C::XCH], b[C::FN][2];
+    i32x2 sa[C::FM], sb[C::FN];
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
+    __shared__ __attribute__((aligned(16))) char smem_raw[C::LDS];
+    const int per_split = g.tiles_m * g.tiles_n;
+    const WgTiles w = wg_tiles_of(per_split * g.splits, (int)blockIdx.x, (int)gridDim.x);
+    if (w.count == 0) return;
+    int L = w.start + w.lb, split = 0;
+    if (g.splits > 1) {
+        split = __builtin_amdgcn_readfirstlane(L / per_split);
+        L -= split * per_split;
+    }
+    // row tiles of the same columns side by side: they share the weights in L2
+    const int tn = __builtin_amdgcn_readfirstlane(L / g.tiles_m), tm = __builtin_amdgcn_readfirstlane(L - tn * g.tiles_m);
+    const int m0 = tm * C::BM, n0 = tn * C::NCOLP;
+    const int rows_left = g.e.M - m0, cols_left = g.e.N - n0;
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    uint32_t va[C::FM], vsa[C::FM], vb[C::FNP], vsb[C::FNP];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        const int row = 16 * i + r;
+        va[i] = row < rows_left ? (uint32_t)(row * (int)g.lda + q * 16) : OOB;
+        vsa[i] = row < rows_left ? (uint32_t)(row * (int)g.lsa) : OOB;
+    }
+#pragma unroll
+    for (int j = 0; j < C::FNP; ++j) {
+        const int row = 16 * j + r;
+        vb[j] = row < cols_left ? (uint32_t)(row * (int)g.ldb + q * 16) : OOB;
+        vsb[j] = row < cols_left ? (uint32_t)(row * (int)g.lsb) : OOB;
+    }
+    const char* a = (const char*)g.A + m0 * g.lda;
+    const char* sa = (const char*)g.SA + m0 * g.lsa;
+    f32x4 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int total = g.filled / 256;
+    const int t0 = (int)((int64_t)total * split / g.splits), t1 = (int)((int64_t)total * (split + 1) / g.splits);
+    // Unit t, zeros past the last one.
+    const auto fetch = [&](MxUnit<C>& u, int t) {
+        const auto rsrc = [&](const char* p) {
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, t < t1 ? 0x80000000u : 0u, 0x00020000);
+        };
+        const auto get = [](const __amdgpu_buffer_rsrc_t& s, uint32_t v) {
+            return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(s, v, 0, 0));
+        };
+        const auto get2 = [](const __amdgpu_buffer_rsrc_t& s, uint32_t v) {
+            return __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(s, v, 0, 0));
+        };
+#pragma unroll
+        for (int p = 0; p < C::NP; ++p) {
+            const __amdgpu_buffer_rsrc_t rb = rsrc((const char*)g.B[p] + n0 * g.ldb + (int64_t)t * C::UB);
+            const __amdgpu_buffer_rsrc_t rs = rsrc((const char*)g.SB[p] + n0 * g.lsb + (int64_t)t * 8);
+#pragma unroll
+            for (int j = 0; j < C::FNP; ++j) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) u.b[p * C::FNP + j][k] = get(rb, vb[j] + 64 * k);
+                u.sb[p * C::FNP + j] = get2(rs, vsb[j]);
+            }
+        }
+        const __amdgpu_buffer_rsrc_t ra = rsrc(a + (int64_t)t * C::UA), rs = rsrc(sa + (int64_t)t * 8);
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int c = 0; c < C::XCH; ++c) u.a[i][k][c] = get(ra, va[i] + 64 * (k * C::XCH + c));
+            u.sa[i] = get2(rs, vsa[i]);
+        }
+    };
+    const auto multiply = [&](const MxUnit<C>& u) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                const i32x8 x = two_chunks(u.a[i][k][0], C::XCH == 2 ? u.a[i][k][C::XCH - 1] : i32x4{0, 0, 0, 0});
+                const int sx = (int)((uint32_t)u.sa[i][k] >> (8 * q));
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        two_chunks(u.b[j][k], i32x4{0, 0, 0, 0}), x, acc[i][j], 4, C::Fmt == MX8 ? 0 : 4, 0,
+                        (int)((uint32_t)u.sb[j][k] >> (8 * q)), 0, sx);
+            }
+    };
+    int t = t0 + wave;
+    if (t < t1) {
+        MxUnit<C> u[C::U];
+#pragma unroll
+        for (int i = 0; i < C::U; ++i) fetch(u[i], t + i * C::NW);
+        while (true) {
+#pragma unroll
+            for (int i = 0; i < C::U; ++i) {
+                multiply(u[i]);
+                fetch(u[i], t + (i + C::U) * C::NW);
+            }
+            t += C::U * C::NW;
+            if (t >= t1) break;
+        }
+    }
+
+    // The waves' sums.
+    char PGEMM_LDS* own = (char PGEMM_LDS*)smem_raw + wave * (C::FM * C::FN * 1024);
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) *(f32x4 PGEMM_LDS*)(own + ((i * C::FN + j) * 64 + lane) * 16) = acc[i][j];
+    __syncthreads();
+    constexpr int GPR = C::NCOLP / 8, GROUPS = C::BM * GPR;  // groups of eight columns
+    for (int x = (int)threadIdx.x; x < GROUPS; x += C::NT) {
+        const int row = x / GPR, c8 = x % GPR;
+        if (row >= rows_left || 8 * c8 >= cols_left) continue;
+        f32x8 s[C::NP];
+#pragma unroll
+        for (int p = 0; p < C::NP; ++p) {
+            s[p] = zero8();
+            const int block = (row >> 4) * C::FN + p * C::FNP + (c8 >> 1);
+            const char PGEMM_LDS* at = (const char PGEMM_LDS*)smem_raw + (block * 64 + (row & 15) + 32 * (c8 & 1)) * 16;
+#pragma unroll
+            for (int v = 0; v < C::NW; ++v)
+                s[p] += join8(*(const f32x4 PGEMM_LDS*)(at + v * (C::FM * C::FN * 1024)),
+                              *(const f32x4 PGEMM_LDS*)(at + v * (C::FM * C::FN * 1024) + 256));
+        }
+        if (g.part) {
+            float* o = g.part + ((int64_t)split * C::NP * g.e.M + m0 + row) * g.np8 + n0 + 8 * c8;
+#pragma unroll
+            for (int p = 0; p < C::NP; ++p) *(f32x8*)(o + (int64_t)p * g.e.M * g.np8) = s[p];
+            continue;
+        }
+        const Epi<C::Dt, C::GATED> ep(g.e, m0, n0, 0, row, 8 * c8);
+        const f32x8 b0 = ep.bias(0), b1 = C::GATED ? ep.bias(1) : b0;
+        typename Epi<C::Dt, C::GATED>::Raw res[1] = {};
+        if (g.e.R && ep.same()) res[0] = ep.residual(0);
+        f32x8 v[1] = {s[0]}, y[1] = {s[C::NP - 1]};
+        with_act(g.e.act.kind, [&](auto kind) {
+            constexpr int KIND = decltype(kind)::value;
+            ep.template put<KIND>(0, 0, v, y, b0, b1, res);
+            if (!ep.whole(0)) {
+#pragma unroll
+                for (int z = 0; z < 7; ++z)
+                    if (z < ep.valid(0)) ep.template put1<KIND>(0, z, s[0][z], s[C::NP - 1][z]);
+            }
+        });
+    }
 }
 
 }  // namespace pgemm

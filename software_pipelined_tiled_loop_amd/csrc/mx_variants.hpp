@@ -16,12 +16,24 @@ struct NormVariant {
     hipError_t (*grad)(const NormGradArgs&, int grid, hipStream_t);
 };
 
+// A kernel of the products.
+struct MxVariant {
+    int format, gated;
+    int bm, bn, bk;  // bn: output columns of the tile
+    int threads;
+    int few;         // waves that share the contraction of a few-rows kernel, else 0
+    int per_cu;      // workgroups that a CU holds
+    hipError_t (*launch)(const MxArgs&, int grid, hipStream_t);
+};
+
 struct MxKernels {
     const NormVariant* norms;  // by capacity; the last one holds any row
     int num_norms;
     hipError_t (*quantize)(const MxCopyArgs&, int format, bool columns, int grid, hipStream_t);
     hipError_t (*dequantize)(const MxCopyArgs&, int format, int grid, hipStream_t);
-    hipError_t (*product)(const MxArgs&, int format, bool gated, int grid, hipStream_t);
+    const MxVariant* v;
+    int n;
+    LinLaunch join, join_gated;
 };
 
 template <int D, int TPR, int CH>
@@ -54,21 +66,39 @@ hipError_t launch_dequantize(const MxCopyArgs& a, int format, int grid, hipStrea
     return format == MX8 ? lin_launch<MxCopyArgs>(&mx_dequantize_rows<D, MX8>, a, dim3(grid), 256, s)
                          : lin_launch<MxCopyArgs>(&mx_dequantize_rows<D, MX4>, a, dim3(grid), 256, s);
 }
-template <int D>
-hipError_t launch_product(const MxArgs& a, int format, bool gated, int grid, hipStream_t s) {
-    if (gated)
-        return format == MX8 ? lin_launch<MxArgs>(&mx_simple<D, MX8, true>, a, dim3(grid), 64, s)
-                             : lin_launch<MxArgs>(&mx_simple<D, MX4, true>, a, dim3(grid), 64, s);
-    return format == MX8 ? lin_launch<MxArgs>(&mx_simple<D, MX8, false>, a, dim3(grid), 64, s)
-                         : lin_launch<MxArgs>(&mx_simple<D, MX4, false>, a, dim3(grid), 64, s);
+template <class C>
+hipError_t launch_mx_tile(const MxArgs& a, int grid, hipStream_t s) {
+    return lin_launch<MxArgs>(&mx_tile<C>, a, dim3(grid), C::NT, s);
+}
+template <class C>
+hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
+    return lin_launch<MxArgs>(&mx_few<C>, a, dim3(grid), C::NT, s);
 }
 
 #define NORM_VARIANT(D, TPR, CH) NormVariant{TPR, CH, &launch_norm<D, TPR, CH>, &launch_norm_grad<D, TPR, CH>}
 #define NORM_VARIANTS(D)                                                                                        \
     NORM_VARIANT(D, 64, 1), NORM_VARIANT(D, 64, 2), NORM_VARIANT(D, 256, 1), NORM_VARIANT(D, 256, 2),           \
         NORM_VARIANT(D, 1024, 1), NORM_VARIANT(D, 1024, 2), NormVariant{1024, 0, &launch_norm_long<D>, &launch_norm_grad_long<D>}
-#define MX_KERNELS(D, norms)                                                                                    \
-    MxKernels{norms, (int)(sizeof(norms) / sizeof(norms[0])), &launch_quantize_any<D>, &launch_dequantize<D>, &launch_product<D>}
+#define MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN) MxCfg<D, F, BM, BN, S, WGM, WGN, GATED != 0>
+#define MX_TILE(D, F, GATED, BM, BN, S, WGM, WGN)                                                               \
+    MxVariant {                                                                                                 \
+        F, GATED, BM, GATED ? BN / 2 : BN, F == MX8 ? 128 : 256, 64 * WGM * WGN, 0,                             \
+            163840 / MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN)::LDS,                                        \
+            &launch_mx_tile<MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN)>                                      \
+    }
+#define MX_FEW(D, F, GATED, FM, FN, NW, U)                                                                      \
+    MxVariant {                                                                                                 \
+        F, GATED, 16 * FM, 16 * FN, 256, 64 * NW, NW, 2, &launch_mx_few<MxFewCfg<D, F, FM, FN, NW, U, GATED != 0>> \
+    }
+#define MX_CLASS(D, F, GATED, DEEP)                                                                             \
+    MX_TILE(D, F, GATED, 256, 256, (F == MX8 ? 3 : 2), 2, 2), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2),        \
+        MX_FEW(D, F, GATED, 1, 1, 8, 2), MX_FEW(D, F, GATED, 2, 1, 8, 2), MX_FEW(D, F, GATED, 4, 1, 8, 2)
+#define MX_VARIANTS(D) MX_CLASS(D, MX8, 0, 3), MX_CLASS(D, MX8, 1, 3), MX_CLASS(D, MX4, 0, 2), MX_CLASS(D, MX4, 1, 2)
+#define MX_KERNELS(D, norms, table)                                                                             \
+    MxKernels {                                                                                                 \
+        norms, (int)(sizeof(norms) / sizeof(norms[0])), &launch_quantize_any<D>, &launch_dequantize<D>, table,  \
+            (int)(sizeof(table) / sizeof(table[0])), &lin_launch_join<D, false>, &lin_launch_join<D, true>      \
+    }
 
 // Per type of the values, each in its own translation unit.
 MxKernels mx_kernels_f32();
