@@ -57,6 +57,11 @@ PGEMM_HD void mx_inv(int off, int& row, int& kc) {
     }
 }
 
+// Scales go to LDS for 512 entries at a time, 16 bytes of a row, in a ring of their
+// own: four bytes a row with every 128 entries made as many requests to the cache as
+// the codes (4096^3 in 4 bits 46 us instead of @).
+constexpr int kScaleGroup = 512;
+
 // F: the activations' format.  Tiles of BM rows by BN weights' rows (gated: half of
 // them of each weight), K tiles of 128 bytes of the activations' codes.
 template <int D, int F, int BM_, int BN_, int S_, int WGM_, int WGN_, bool GATED_>
@@ -64,25 +69,24 @@ struct MxCfg {
     static constexpr int Dt = D, Fmt = F, BM = BM_, BN = BN_, S = S_, WGM = WGM_, WGN = WGN_;
     static constexpr bool GATED = GATED_;
     static constexpr int ES = D == DT_F32 ? 4 : 2;  // of a value
-    static constexpr int BK = F == MX8 ? 128 : 256, NKS = BK / 64, Q = BK / 128;  // entries; K steps; dwords of scales a row
+    static constexpr int BK = F == MX8 ? 128 : 256, NKS = BK / 64;  // entries; K steps
+    static constexpr int G = kScaleGroup / BK;                      // K tiles of a group of scales
     static constexpr int KCA = 8, KCB = F == MX8 ? 4 : 8;
     static constexpr int NP = GATED ? 2 : 1, BNP = BN / NP;
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
     static constexpr int WM = BM / WGM, WNP = BNP / WGN;
     static constexpr int FM = WM / 32, FNP = WNP / 32, FN = FNP * NP;
     static constexpr int A_BYTES = BM * KCA * 16, B_BYTES = BN * KCB * 16;
-    static constexpr int SA_BYTES = BM * Q * 4, SB_BYTES = BN * Q * 4;
-    static constexpr int AT_B = A_BYTES, AT_SA = A_BYTES + B_BYTES, AT_SB = AT_SA + SA_BYTES;
-    static constexpr int STAGE = AT_SB + SB_BYTES, LDS = S * STAGE;
+    static constexpr int SA_BYTES = BM * 16, S_STAGE = (BM + BN) * 16;  // scales: two stages behind the ring
+    static constexpr int STAGE = A_BYTES + B_BYTES, AT_S = S * STAGE, LDS = AT_S + 2 * S_STAGE;
     static constexpr int MINW = 163840 / LDS * NW / 4;  // waves per SIMD, by the CU's LDS
-    // LDS-DMA pieces of a wave: codes 1 KiB at a time, scales 256 bytes
+    // LDS-DMA pieces of a wave, 1 KiB each
     static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW;
-    static constexpr int S_INSTR = (SA_BYTES + SB_BYTES) / 256 / NW, LPS = A_INSTR + B_INSTR + S_INSTR;
+    static constexpr int LPS = A_INSTR + B_INSTR, S_INSTR = S_STAGE / 1024 / NW;
     static constexpr int XCH = F == MX8 ? 2 : 1;  // chunks of an activations' fragment
     static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0 && NW % 4 == 0, "a wave's pieces lie in one operand");
-    static_assert(SA_BYTES % (256 * S_INSTR) == 0 && SB_BYTES % (256 * S_INSTR * NP) == 0 && BM % 64 == 0 && BNP % 64 == 0,
-                  "scale pieces");
-    static_assert(STAGE % 256 == 0 && LDS <= 163840 && S >= 2 && LPS * (S - 2) <= 63, "ring");
+    static_assert(S_INSTR * NW * 64 == BM + BN && BM % (64 * S_INSTR) == 0 && BNP % (64 * S_INSTR) == 0, "scale pieces");
+    static_assert(LDS <= 163840 && S >= 2 && LPS * (S - 2) <= 63, "ring");
 };
 
 template <class C>
@@ -130,7 +134,7 @@ __device__ __forceinline__ void mx_read(const char PGEMM_LDS* st, int ks, int wm
         constexpr int j = R == 0 ? 0 : R - C::XCH;
         constexpr int panel = j / C::FNP;
         const int row = panel * C::BNP + wn0 + 32 * (j % C::FNP) + r;
-        f.b[j] = *(const i32x4 PGEMM_LDS*)(st + C::AT_B + mx_off<C::KCB>(row, mx_chunk_b<C>(ks, g)));
+        f.b[j] = *(const i32x4 PGEMM_LDS*)(st + C::A_BYTES + mx_off<C::KCB>(row, mx_chunk_b<C>(ks, g)));
     } else {
         constexpr int x = R <= C::XCH ? R - 1 : R - C::FN;
         static_assert(x >= 0 && x < XA, "reads");
@@ -138,38 +142,37 @@ __device__ __forceinline__ void mx_read(const char PGEMM_LDS* st, int ks, int wm
         f.a[i][c] = *(const i32x4 PGEMM_LDS*)(st + mx_off<C::KCA>(wm0 + 32 * i + r, mx_chunk_a<C>(ks, g, c)));
     }
 }
-// Scales of a K tile: MX4 the four bytes of blocks 4 g .. 4 g + 3, MX8 those of blocks 2 g, 2 g + 1.
+// Scales of K tile u of a group: MX4 the four bytes of its blocks 4 g .. 4 g + 3, MX8 those of its blocks 2 g, 2 g + 1.
 template <class C, int R>
-__device__ __forceinline__ void mx_read_scale(const char PGEMM_LDS* st, int wm0, int wn0, int lane, MxScales<C>& s) {
+__device__ __forceinline__ void mx_read_scale(const char PGEMM_LDS* st, int u, int wm0, int wn0, int lane, MxScales<C>& s) {
     const int r = lane & 31, g = lane >> 5;
-    const auto get = [&](const char PGEMM_LDS* base, int rows, int row) -> int {
-        if constexpr (C::Fmt == MX8) return *(const unsigned short PGEMM_LDS*)(base + row * 4 + 2 * g);
-        else return *(const int PGEMM_LDS*)(base + (g * rows + row) * 4);
+    const auto get = [&](int row) -> int {
+        const char PGEMM_LDS* p = st + row * 16;
+        if constexpr (C::Fmt == MX8) return *(const unsigned short PGEMM_LDS*)(p + 4 * u + 2 * g);
+        else return *(const int PGEMM_LDS*)(p + 8 * u + 4 * g);
     };
-    if constexpr (R < C::FN) {
-        constexpr int panel = R / C::FNP;
-        s.b[R] = get(st + C::AT_SB + panel * (C::SB_BYTES / C::NP), C::BNP, wn0 + 32 * (R % C::FNP) + r);
-    } else {
-        s.a[R - C::FN] = get(st + C::AT_SA, C::BM, wm0 + 32 * (R - C::FN) + r);
-    }
+    if constexpr (R < C::FN) s.b[R] = get(C::BM + R / C::FNP * C::BNP + wn0 + 32 * (R % C::FNP) + r);
+    else s.a[R - C::FN] = get(wm0 + 32 * (R - C::FN) + r);
 }
 
 // Fragments and scales of the first K tile's first step.
 template <class C, int R = 0>
-__device__ __forceinline__ void mx_first(const char PGEMM_LDS* st, int wm0, int wn0, int lane, MxFrags<C>& f, MxScales<C>& s) {
+__device__ __forceinline__ void mx_first(const char PGEMM_LDS* st, const char PGEMM_LDS* ss, int wm0, int wn0, int lane,
+                                         MxFrags<C>& f, MxScales<C>& s) {
     constexpr int NR = C::FM * C::XCH + C::FN;
     if constexpr (R < NR) mx_read<C, R>(st, 0, wm0, wn0, lane, f);
-    if constexpr (R < C::FM + C::FN) mx_read_scale<C, R>(st, wm0, wn0, lane, s);
-    if constexpr (R < NR) mx_first<C, R + 1>(st, wm0, wn0, lane, f, s);
+    if constexpr (R < C::FM + C::FN) mx_read_scale<C, R>(ss, 0, wm0, wn0, lane, s);
+    if constexpr (R < NR) mx_first<C, R + 1>(st, ss, wm0, wn0, lane, f, s);
 }
 
 // The wave's side of the producer.
 template <class C>
 struct MxSrc {
-    i32x4 ra, rb, rs;  // next K tile of the codes, and of the scales that the wave loads
-    int64_t back_a, back_b, back_s;  // from behind the last K tile to the first
-    int turn;          // K tiles until the row's end
-    int left;          // K tiles still to load
+    i32x4 ra, rb, rs;  // next K tile of the codes, next group of the scales that the wave loads
+    int64_t back_a, back_b;      // from behind the last K tile to the first
+    int turn, s_turn;            // K tiles, groups until the row's end
+    int left, s_left;            // K tiles, groups still to load
+    int s_bytes, s_groups;       // bytes from rs's address to the end of the last row; groups of a row
     uint32_t va[C::A_INSTR], vb[C::B_INSTR], vs[C::S_INSTR];
 
     static __device__ __forceinline__ void move(i32x4& r, int64_t by) {
@@ -182,116 +185,128 @@ struct MxSrc {
     __device__ __forceinline__ void advance() {
         if constexpr (PART == 0) {
             --left;
-            ra[2] = rb[2] = rs[2] = left > 0 ? (int)0x80000000u : 0;
+            ra[2] = rb[2] = left > 0 ? (int)0x80000000u : 0;
         } else if constexpr (PART == 1) {
             move(ra, 16 * C::KCA);
             --turn;
         } else if constexpr (PART == 2) {
             move(rb, 16 * C::KCB);
-        } else if constexpr (PART == 3) {
-            move(rs, C::BK / 32);
         } else if (turn == 0) {
             move(ra, back_a);
             move(rb, back_b);
-            move(rs, back_s);
         }
     }
-    static constexpr int PARTS = 5;
+    static constexpr int PARTS = 4;
     __device__ __forceinline__ void advance_all() {
         advance<0>();
         advance<1>();
         advance<2>();
         advance<3>();
-        advance<4>();
+    }
+    // The next group of scales, to LDS.  The last one of a row may be half a group: its
+    // other half is the next row's first bytes, or beyond the range, and not read.
+    __device__ __forceinline__ void scales(uint32_t at) {
+        rs[2] = s_left > 0 ? s_bytes : 0;
+#pragma unroll
+        for (int q = 0; q < C::S_INSTR; ++q) dma16(rs, vs[q], at + q * 1024u);
+        --s_left;
+        int by = 16;
+        if (--s_turn == 0) by -= 16 * s_groups;
+        move(rs, by);
+        s_bytes -= by;
     }
     // Piece I of the K tile, to LDS: its place (M0), and the load, which needs an instruction between them.
     template <int I>
-    __device__ __forceinline__ void place(uint32_t a, uint32_t b, uint32_t s) const {
-        constexpr int B0 = C::A_INSTR, S0 = B0 + C::B_INSTR;
-        constexpr uint32_t off = I < B0 ? I * 1024u : I < S0 ? (I - B0) * 1024u : (I - S0) * 256u;
-        asm volatile("s_add_u32 m0, %0, %1" : : "s"(I < B0 ? a : I < S0 ? b : s), "n"(off) : "m0", "scc");
+    __device__ __forceinline__ void place(uint32_t a, uint32_t b) const {
+        constexpr uint32_t off = (I < C::A_INSTR ? I : I - C::A_INSTR) * 1024u;
+        asm volatile("s_add_u32 m0, %0, %1" : : "s"(I < C::A_INSTR ? a : b), "n"(off) : "m0", "scc");
     }
     template <int I>
     __device__ __forceinline__ void load() const {
-        constexpr int B0 = C::A_INSTR, S0 = B0 + C::B_INSTR;
-        if constexpr (I < S0) {
-            asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds"
-                         :
-                         : "v"(I < B0 ? va[I < B0 ? I : 0] : vb[I < B0 ? 0 : I - B0]), "s"(I < B0 ? ra : rb)
-                         : "memory");
-        } else {
-            asm volatile("buffer_load_dword %0, %1, 0 offen lds" : : "v"(vs[I - S0]), "s"(rs) : "memory");
-        }
+        asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds"
+                     :
+                     : "v"(I < C::A_INSTR ? va[I < C::A_INSTR ? I : 0] : vb[I < C::A_INSTR ? 0 : I - C::A_INSTR]),
+                       "s"(I < C::A_INSTR ? ra : rb)
+                     : "memory");
     }
 };
 template <class C, int I = 0>
-__device__ __forceinline__ void mx_pieces(const MxSrc<C>& s, uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ void mx_pieces(const MxSrc<C>& s, uint32_t a, uint32_t b) {
     if constexpr (I < C::LPS) {
-        s.template place<I>(a, b, c);
+        s.template place<I>(a, b);
         asm volatile("s_nop 0");
         s.template load<I>();
-        mx_pieces<C, I + 1>(s, a, b, c);
+        mx_pieces<C, I + 1>(s, a, b);
     }
 }
 
-// One K step, with what else is to be done spread evenly between its MFMAs: READS
-// reads of the next step's fragments (of the next K tile's first step: its scales
-// too), with DMA the next K tile's pieces, two instructions each, without it the
-// producer's way to that K tile.
+// Where a K tile's steps read and load.
+struct MxAt {
+    const char PGEMM_LDS* cur;   // the K tile's stage
+    const char PGEMM_LDS* next;  // the next one's
+    const char PGEMM_LDS* scales;  // the next K tile's group of scales, and its place there
+    int u;
+    uint32_t a, b;               // where the wave's pieces of the freed stage go
+    uint32_t s;                  // and of the freed stage of scales; 0: none is free
+    int wm0, wn0, lane;
+};
+
+// One K step, with what else is to be done spread evenly between its MFMAs: the
+// reads of the next step's fragments; in a K tile's last step those are of the next
+// K tile, with its scales, and the pieces of the stage that has become free follow,
+// two instructions each; in its first step the producer's way to the next K tile.
 template <class C, int KS, bool LAST>
 struct MxStep {
     static constexpr int NMF = C::FM * C::FN, NR = C::FM * C::XCH + C::FN, NS = LAST ? C::FM + C::FN : 0;
     static constexpr int MORE = LAST ? 2 * C::LPS : KS == 0 ? MxSrc<C>::PARTS : 0, JOBS = NR + NS + MORE;
     template <int J>
-    static __device__ __forceinline__ void job(const char PGEMM_LDS* st, MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src,
-                                               uint32_t a, uint32_t b, uint32_t s, int wm0, int wn0, int lane) {
+    static __device__ __forceinline__ void job(const MxAt& at, MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src) {
         if constexpr (J < NR) {
-            mx_read<C, J>(st, LAST ? 0 : KS + 1, wm0, wn0, lane, nxt);
+            mx_read<C, J>(LAST ? at.next : at.cur, LAST ? 0 : KS + 1, at.wm0, at.wn0, at.lane, nxt);
         } else if constexpr (J < NR + NS) {
-            mx_read_scale<C, J - NR>(st, wm0, wn0, lane, sc);
+            mx_read_scale<C, J - NR>(at.scales, at.u, at.wm0, at.wn0, at.lane, sc);
         } else if constexpr (LAST) {
             constexpr int P = (J - NR - NS) / 2;
-            if constexpr ((J - NR - NS) % 2 == 0) src.template place<P>(a, b, s);
+            if constexpr ((J - NR - NS) % 2 == 0) src.template place<P>(at.a, at.b);
             else src.template load<P>();
         } else {
             src.template advance<J - NR - NS>();
         }
     }
     template <int J, int END>
-    static __device__ __forceinline__ void jobs(const char PGEMM_LDS* st, MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src,
-                                                uint32_t a, uint32_t b, uint32_t s, int wm0, int wn0, int lane) {
+    static __device__ __forceinline__ void jobs(const MxAt& at, MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src) {
         if constexpr (J < END) {
-            job<J>(st, nxt, sc, src, a, b, s, wm0, wn0, lane);
-            // (M0 and the load that uses it stand in one place: an instruction between them)
+            job<J>(at, nxt, sc, src);
+            // M0 and the load that uses it stand in one place: an instruction between them
             if constexpr (LAST && J >= NR + NS && (J - NR - NS) % 2 == 0 && J + 1 < END) asm volatile("s_nop 0");
-            jobs<J + 1, END>(st, nxt, sc, src, a, b, s, wm0, wn0, lane);
+            jobs<J + 1, END>(at, nxt, sc, src);
         }
     }
     template <int M = 0>
     static __device__ __forceinline__ void run(f32x16 (&acc)[C::FM][C::FN], const MxFrags<C>& use, const MxScales<C>& us,
-                                               MxFrags<C>& nxt, MxScales<C>& sc, const char PGEMM_LDS* st, MxSrc<C>& src,
-                                               uint32_t a, uint32_t b, uint32_t s, int wm0, int wn0, int lane) {
+                                               MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src, const MxAt& at) {
         if constexpr (M < NMF) {
             constexpr int i = M / C::FN, j = M % C::FN;
             mx_mfma<C, KS>(acc[i][j], use.a[i], use.b[j], us.a[i], us.b[j]);
-            jobs<M * JOBS / NMF, (M + 1) * JOBS / NMF>(st, nxt, sc, src, a, b, s, wm0, wn0, lane);
+            jobs<M * JOBS / NMF, (M + 1) * JOBS / NMF>(at, nxt, sc, src);
             __builtin_amdgcn_sched_barrier(0);
-            run<M + 1>(acc, use, us, nxt, sc, st, src, a, b, s, wm0, wn0, lane);
+            run<M + 1>(acc, use, us, nxt, sc, src, at);
         }
     }
 };
 // All K steps of one K tile, the ready edge of the next one before the last.
 template <class C, int KS = 0>
 __device__ __forceinline__ void mx_tile_steps(f32x16 (&acc)[C::FM][C::FN], MxFrags<C> (&f)[2], const MxScales<C>& us,
-                                              MxScales<C>& sc, const char PGEMM_LDS* cur, const char PGEMM_LDS* next,
-                                              MxSrc<C>& src, uint32_t a, uint32_t b, uint32_t s, int wm0, int wn0,
-                                              int lane) {
+                                              MxScales<C>& sc, MxSrc<C>& src, const MxAt& at) {
     if constexpr (KS < C::NKS - 1) {
-        MxStep<C, KS, false>::run(acc, f[KS & 1], us, f[(KS & 1) ^ 1], sc, cur, src, 0, 0, 0, wm0, wn0, lane);
-        mx_tile_steps<C, KS + 1>(acc, f, us, sc, cur, next, src, a, b, s, wm0, wn0, lane);
+        MxStep<C, KS, false>::run(acc, f[KS & 1], us, f[(KS & 1) ^ 1], sc, src, at);
+        mx_tile_steps<C, KS + 1>(acc, f, us, sc, src, at);
     } else {
-        wait_barrier<C::LPS*(C::S - 2)>();  // the next K tile is in LDS, this one's stage is free
-        MxStep<C, KS, true>::run(acc, f[KS & 1], us, f[(KS & 1) ^ 1], sc, next, src, a, b, s, wm0, wn0, lane);
+        // The next K tile is in LDS (and the scales, which are older than the codes
+        // that may be under way), this one's stage is free.
+        wait_barrier<C::LPS*(C::S - 2)>();
+        if (at.s) src.scales(at.s);
+        MxStep<C, KS, true>::run(acc, f[KS & 1], us, f[(KS & 1) ^ 1], sc, src, at);
     }
 }
 
@@ -421,19 +436,23 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
             for (int x = 0; x < 16; ++x) acc[i][j][x] = 0.0f;
     acc_settle();
 
-    // This split's K tiles [t0, t1).
-    const int total = g.filled / C::BK;
-    const int t0 = (int)((int64_t)total * split / g.splits), t1 = (int)((int64_t)total * (split + 1) / g.splits);
+    // This split's K tiles [t0, t1): whole groups of scales.
+    const int total = g.filled / C::BK, groups = (total + C::G - 1) / C::G;
+    const int g0 = (int)((int64_t)groups * split / g.splits), g1 = (int)((int64_t)groups * (split + 1) / g.splits);
+    const int t0 = g0 * C::G, t1 = min(g1 * C::G, total);
     if (t1 > t0) {
         MxSrc<C> src;
         // With the whole contraction in one go the XCDs begin at different places of it (see linear_kernel).
         const int x = blockIdx.x & 7;
-        const int first = g.splits == 1 ? (int)((int64_t)total * (((x & 6) + 4 * (x & 1)) & 7) >> 3) : t0;
+        const int begin = g.splits == 1 ? (int)((int64_t)groups * (((x & 6) + 4 * (x & 1)) & 7) >> 3) : g0;
+        const int first = begin * C::G;
         src.turn = total - first;
         src.left = t1 - t0;
+        src.s_turn = groups - begin;
+        src.s_left = g1 - g0;
+        src.s_groups = groups;
         src.back_a = -(int64_t)total * 16 * C::KCA;
         src.back_b = -(int64_t)total * 16 * C::KCB;
-        src.back_s = -(int64_t)total * (C::BK / 32);
         const int panel = C::NP == 2 ? wave / (C::NW / 2) : 0;  // the wave's pieces of B lie in one panel
         const int b_block = wave * C::B_INSTR - panel * (C::B_BYTES / C::NP / 1024);
         src.ra = make_rsrc_sgpr((const char*)g.A + m0 * g.lda + first * (16 * C::KCA));
@@ -450,43 +469,62 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
             mx_inv<C::KCB>((b_block + q) * 1024 + lane * 16, row, kc);
             src.vb[q] = row < cols_left ? (uint32_t)(row * (int)g.ldb + kc * 16) : OOB;
         }
-        // scales: pieces of 64 rows' dwords, [Q][rows] of the activations, then of each panel of the weights
-        constexpr int A_PIECES = C::SA_BYTES / 256, P_PIECES = C::SB_BYTES / C::NP / 256;
-        const int piece = wave * C::S_INSTR;
-        const bool of_a = piece < A_PIECES;
-        const int s_panel = of_a ? 0 : (piece - A_PIECES) / P_PIECES;
-        src.rs = make_rsrc_sgpr((of_a ? (const char*)g.SA + m0 * g.lsa
-                                      : (const char*)(s_panel ? g.SB[1] : g.SB[0]) + n0 * g.lsb) + first * (C::BK / 32));
+        // scales: rows of the activations, then of each panel of the weights
+        const int s_row = wave * C::S_INSTR * 64;
+        const bool of_a = s_row < C::BM;
+        const int s_panel = of_a ? 0 : (s_row - C::BM) / C::BNP, s_first = of_a ? s_row : s_row - C::BM - s_panel * C::BNP;
+        const int s_rows = of_a ? min(rows_left, C::BM) : min(cols_left, C::BNP);
+        const int64_t ls = of_a ? g.lsa : g.lsb;
+        src.rs = make_rsrc_sgpr((of_a ? (const char*)g.SA + m0 * ls : (const char*)(s_panel ? g.SB[1] : g.SB[0]) + n0 * ls) +
+                                begin * 16);
+        src.s_bytes = __builtin_amdgcn_readfirstlane((s_rows - 1) * (int)ls + g.filled / 32 - begin * 16);
 #pragma unroll
         for (int q = 0; q < C::S_INSTR; ++q) {
-            const int p = (of_a ? piece : piece - A_PIECES - s_panel * P_PIECES) + q, blocks = (of_a ? C::BM : C::BNP) / 64;
-            const int row = p % blocks * 64 + lane, dw = p / blocks;
-            src.vs[q] = row < (of_a ? rows_left : cols_left) ? (uint32_t)(row * (int)(of_a ? g.lsa : g.lsb) + dw * 4) : OOB;
+            const int row = s_first + q * 64 + lane;
+            src.vs[q] = row < s_rows ? (uint32_t)(row * (int)ls) : OOB;
         }
 
         const uint32_t lds0 = (uint32_t)(size_t)smem;
-        const uint32_t at_a = wave * C::A_INSTR * 1024, at_b = C::AT_B + wave * C::B_INSTR * 1024;
-        const uint32_t at_s = C::AT_SA + piece * 256;
-        // Prologue: slots 0 .. S-2.
+        const uint32_t at_a = wave * C::A_INSTR * 1024, at_b = C::A_BYTES + wave * C::B_INSTR * 1024;
+        const uint32_t at_s = lds0 + C::AT_S + s_row * 16;
+        // Prologue: two groups of scales, slots 0 .. S-2.
+        src.scales(at_s);
+        src.scales(at_s + C::S_STAGE);
 #pragma unroll
         for (int p = 0; p < C::S - 1; ++p) {
-            mx_pieces<C>(src, lds0 + p * C::STAGE + at_a, lds0 + p * C::STAGE + at_b, lds0 + p * C::STAGE + at_s);
+            mx_pieces<C>(src, lds0 + p * C::STAGE + at_a, lds0 + p * C::STAGE + at_b);
             src.advance_all();
         }
         wait_barrier<C::LPS*(C::S - 2)>();
         constexpr uint32_t LASTST = (C::S - 1) * C::STAGE;
-        mx_pieces<C>(src, lds0 + LASTST + at_a, lds0 + LASTST + at_b, lds0 + LASTST + at_s);
+        mx_pieces<C>(src, lds0 + LASTST + at_a, lds0 + LASTST + at_b);
         MxFrags<C> f[2];
         MxScales<C> sc, next;
-        mx_first<C>(smem, wm0, wn0, lane, f[0], sc);
-        int cur = 0;
+        mx_first<C>(smem, smem + C::AT_S, wm0, wn0, lane, f[0], sc);
+        int cur = 0, u = 0, sst = 0, row_left = total - first;
         for (int t = t0; t < t1; ++t) {
             // the last K step's copies of the scales, two wait states before the first MFMA
             asm volatile("s_nop 1");
             const int nst = cur + 1 == C::S ? 0 : cur + 1;
-            const uint32_t freed = lds0 + cur * C::STAGE;
-            mx_tile_steps<C>(acc, f, sc, next, smem + cur * C::STAGE, smem + nst * C::STAGE, src, freed + at_a, freed + at_b,
-                             freed + at_s, wm0, wn0, lane);
+            // the next K tile's scales: of this group, or the next one where the group or the row ends
+            --row_left;
+            const bool ends = ++u == C::G || row_left == 0;
+            MxAt at;
+            at.cur = smem + cur * C::STAGE;
+            at.next = smem + nst * C::STAGE;
+            at.a = lds0 + cur * C::STAGE + at_a;
+            at.b = lds0 + cur * C::STAGE + at_b;
+            at.s = ends ? at_s + sst * C::S_STAGE : 0;
+            if (ends) {
+                u = 0;
+                sst ^= 1;
+            }
+            at.scales = smem + C::AT_S + sst * C::S_STAGE;
+            at.u = u;
+            at.wm0 = wm0;
+            at.wn0 = wn0;
+            at.lane = lane;
+            mx_tile_steps<C>(acc, f, sc, next, src, at);
             sc = next;
             cur = nst;
         }
