@@ -63,15 +63,14 @@ PGEMM_HD void mx_inv(int off, int& row, int& kc) {
 constexpr int kScaleGroup = 512;
 
 // F: the activations' format.  Tiles of BM rows by BN weights' rows (gated: half of
-// them of each weight), K tiles of 128 bytes of the activations' codes.
+// them of each weight), K tiles of 128 entries.
 template <int D, int F, int BM_, int BN_, int S_, int WGM_, int WGN_, bool GATED_>
 struct MxCfg {
     static constexpr int Dt = D, Fmt = F, BM = BM_, BN = BN_, S = S_, WGM = WGM_, WGN = WGN_;
     static constexpr bool GATED = GATED_;
     static constexpr int ES = D == DT_F32 ? 4 : 2;  // of a value
-    static constexpr int BK = F == MX8 ? 128 : 256, NKS = BK / 64;  // entries; K steps
-    static constexpr int G = kScaleGroup / BK;                      // K tiles of a group of scales
-    static constexpr int KCA = 8, KCB = F == MX8 ? 4 : 8;
+    static constexpr int BK = 128, NKS = 2, G = kScaleGroup / BK;  // entries; K steps; K tiles of a group of scales
+    static constexpr int KCA = F == MX8 ? 8 : 4, KCB = 4;          // 16-byte chunks of a row
     static constexpr int NP = GATED ? 2 : 1, BNP = BN / NP;
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
     static constexpr int WM = BM / WGM, WNP = BNP / WGN;
@@ -100,29 +99,29 @@ struct MxScales {
 };
 
 // A scaled MFMA with the accumulators in AGPRs, from inline asm (as mfma_lone):
-// weights times activations, byte KS of each side's scales.
+// weights times activations, byte KS (0 or 1) of each side's scales.
 template <class C, int KS>
 __device__ __forceinline__ void mx_mfma(f32x16& acc, const i32x4 (&x)[C::XCH], const i32x4& w, int sx, int sw) {
     if constexpr (C::Fmt == MX8) {
         const i32x8 xx = two_chunks(x[0], x[1]);
-        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[%6,%6,0] cbsz:4"
+        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4"
                      : "+a"(acc)
-                     : "v"(w), "v"(xx), "v"(sw), "v"(sx), "n"(KS & 1), "n"(KS >> 1));
+                     : "v"(w), "v"(xx), "v"(sw), "v"(sx), "n"(KS));
     } else {
         asm volatile(
-            "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[%6,%6,0] cbsz:4 blgp:4"
+            "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
             : "+a"(acc)
-            : "v"(w), "v"(x[0]), "v"(sw), "v"(sx), "n"(KS & 1), "n"(KS >> 1));
+            : "v"(w), "v"(x[0]), "v"(sw), "v"(sx), "n"(KS));
     }
 }
 
-// Fragment chunk of K step ks that a lane of half g reads.  MX4: block 4 g + ks of
-// the row's eight.  MX8, blocks 0 .. 3, two a step (ks and 2 + ks): the
-// activations' piece g of each, the weights' block 2 g + ks.
+// Of a K tile's four blocks, K step ks takes ks and 2 + ks, so that a lane's scales
+// of both steps lie side by side.  A lane of half g reads block 2 g + ks of e2m1,
+// piece g of each of the two blocks of e4m3.
 template <class C>
-PGEMM_HD int mx_chunk_a(int ks, int g, int c) { return C::Fmt == MX8 ? 4 * c + 2 * ks + g : 4 * g + ks; }
+PGEMM_HD int mx_chunk_a(int ks, int g, int c) { return C::Fmt == MX8 ? 4 * c + 2 * ks + g : 2 * g + ks; }
 template <class C>
-PGEMM_HD int mx_chunk_b(int ks, int g) { return C::Fmt == MX8 ? 2 * g + ks : 4 * g + ks; }
+PGEMM_HD int mx_chunk_b(int ks, int g) { return 2 * g + ks; }
 
 // Reads of a K step's fragments in the order in which its MFMAs need them.
 template <class C, int R>
@@ -142,15 +141,11 @@ __device__ __forceinline__ void mx_read(const char PGEMM_LDS* st, int ks, int wm
         f.a[i][c] = *(const i32x4 PGEMM_LDS*)(st + mx_off<C::KCA>(wm0 + 32 * i + r, mx_chunk_a<C>(ks, g, c)));
     }
 }
-// Scales of K tile u of a group: MX4 the four bytes of its blocks 4 g .. 4 g + 3, MX8 those of its blocks 2 g, 2 g + 1.
+// Scales of a K tile, from its place in the group on: the two bytes of blocks 2 g and 2 g + 1.
 template <class C, int R>
-__device__ __forceinline__ void mx_read_scale(const char PGEMM_LDS* st, int u, int wm0, int wn0, int lane, MxScales<C>& s) {
+__device__ __forceinline__ void mx_read_scale(const char PGEMM_LDS* st, int wm0, int wn0, int lane, MxScales<C>& s) {
     const int r = lane & 31, g = lane >> 5;
-    const auto get = [&](int row) -> int {
-        const char PGEMM_LDS* p = st + row * 16;
-        if constexpr (C::Fmt == MX8) return *(const unsigned short PGEMM_LDS*)(p + 4 * u + 2 * g);
-        else return *(const int PGEMM_LDS*)(p + 8 * u + 4 * g);
-    };
+    const auto get = [&](int row) -> int { return *(const unsigned short PGEMM_LDS*)(st + row * 16 + 2 * g); };
     if constexpr (R < C::FN) s.b[R] = get(C::BM + R / C::FNP * C::BNP + wn0 + 32 * (R % C::FNP) + r);
     else s.a[R - C::FN] = get(wm0 + 32 * (R - C::FN) + r);
 }
@@ -161,58 +156,41 @@ __device__ __forceinline__ void mx_first(const char PGEMM_LDS* st, const char PG
                                          MxFrags<C>& f, MxScales<C>& s) {
     constexpr int NR = C::FM * C::XCH + C::FN;
     if constexpr (R < NR) mx_read<C, R>(st, 0, wm0, wn0, lane, f);
-    if constexpr (R < C::FM + C::FN) mx_read_scale<C, R>(ss, 0, wm0, wn0, lane, s);
+    if constexpr (R < C::FM + C::FN) mx_read_scale<C, R>(ss, wm0, wn0, lane, s);
     if constexpr (R < NR) mx_first<C, R + 1>(st, ss, wm0, wn0, lane, f, s);
 }
 
-// The wave's side of the producer.
+// The wave's side of the producer.  A K tile's place in the rows goes into the loads
+// as their scalar offset; behind the rows' end it comes round to their beginning,
+// also for the slots past the last K tile, which nobody reads.
 template <class C>
 struct MxSrc {
-    i32x4 ra, rb, rs;  // next K tile of the codes, next group of the scales that the wave loads
-    int64_t back_a, back_b;      // from behind the last K tile to the first
-    int turn, s_turn;            // K tiles, groups until the row's end
-    int left, s_left;            // K tiles, groups still to load
+    i32x4 ra, rb, rs;            // the codes' rows; the next group of the scales that the wave loads
+    uint32_t k, k_end;           // bytes in the weights' rows: the next K tile, the rows' end
+    int s_turn, s_left;          // groups until the row's end, groups still to load
     int s_bytes, s_groups;       // bytes from rs's address to the end of the last row; groups of a row
     uint32_t va[C::A_INSTR], vb[C::B_INSTR], vs[C::S_INSTR];
 
-    static __device__ __forceinline__ void move(i32x4& r, int64_t by) {
-        const uint64_t p = (((uint64_t)(uint32_t)r[1] << 32) | (uint32_t)r[0]) + (uint64_t)by;
-        r[0] = (int)(uint32_t)p;
-        r[1] = (int)(uint32_t)(p >> 32);  // the address stays below 2^48: the stride field stays zero
-    }
-    // On to the next K tile; slots past the last one get an empty range: every lane reads zeros.
     template <int PART>
     __device__ __forceinline__ void advance() {
-        if constexpr (PART == 0) {
-            --left;
-            ra[2] = rb[2] = left > 0 ? (int)0x80000000u : 0;
-        } else if constexpr (PART == 1) {
-            move(ra, 16 * C::KCA);
-            --turn;
-        } else if constexpr (PART == 2) {
-            move(rb, 16 * C::KCB);
-        } else if (turn == 0) {
-            move(ra, back_a);
-            move(rb, back_b);
-        }
-    }
-    static constexpr int PARTS = 4;
-    __device__ __forceinline__ void advance_all() {
-        advance<0>();
-        advance<1>();
-        advance<2>();
-        advance<3>();
+        if constexpr (PART == 0) k += 16 * C::KCB;
+        else k = k == k_end ? 0 : k;
     }
     // The next group of scales, to LDS.  The last one of a row may be half a group: its
     // other half is the next row's first bytes, or beyond the range, and not read.
     __device__ __forceinline__ void scales(uint32_t at) {
         rs[2] = s_left > 0 ? s_bytes : 0;
+        i32x4 r;
 #pragma unroll
-        for (int q = 0; q < C::S_INSTR; ++q) dma16(rs, vs[q], at + q * 1024u);
+        for (int d = 0; d < 4; ++d) r[d] = __builtin_amdgcn_readfirstlane(rs[d]);
+#pragma unroll
+        for (int q = 0; q < C::S_INSTR; ++q) dma16(r, vs[q], at + q * 1024u);
         --s_left;
         int by = 16;
         if (--s_turn == 0) by -= 16 * s_groups;
-        move(rs, by);
+        const uint64_t p = (((uint64_t)(uint32_t)rs[1] << 32) | (uint32_t)rs[0]) + (int64_t)by;
+        rs[0] = (int)(uint32_t)p;
+        rs[1] = (int)(uint32_t)(p >> 32);  // the address stays below 2^48: the stride field stays zero
         s_bytes -= by;
     }
     // Piece I of the K tile, to LDS: its place (M0), and the load, which needs an instruction between them.
@@ -223,62 +201,73 @@ struct MxSrc {
     }
     template <int I>
     __device__ __forceinline__ void load() const {
-        asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds"
+        asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds"
                      :
                      : "v"(I < C::A_INSTR ? va[I < C::A_INSTR ? I : 0] : vb[I < C::A_INSTR ? 0 : I - C::A_INSTR]),
-                       "s"(I < C::A_INSTR ? ra : rb)
+                       "s"(I < C::A_INSTR ? ra : rb), "s"(I < C::A_INSTR ? k * (C::KCA / C::KCB) : k)
                      : "memory");
     }
 };
-template <class C, int I = 0>
+template <class C, int END, int I = 0>
 __device__ __forceinline__ void mx_pieces(const MxSrc<C>& s, uint32_t a, uint32_t b) {
-    if constexpr (I < C::LPS) {
+    if constexpr (I < END) {
         s.template place<I>(a, b);
         asm volatile("s_nop 0");
         s.template load<I>();
-        mx_pieces<C, I + 1>(s, a, b);
+        mx_pieces<C, END, I + 1>(s, a, b);
     }
 }
 
-// Where a K tile's steps read and load.
+// Where a step reads and loads.
 struct MxAt {
-    const char PGEMM_LDS* cur;   // the K tile's stage
-    const char PGEMM_LDS* next;  // the next one's
-    const char PGEMM_LDS* scales;  // the next K tile's group of scales, and its place there
-    int u;
-    uint32_t a, b;               // where the wave's pieces of the freed stage go
-    uint32_t s;                  // and of the freed stage of scales; 0: none is free
+    const char PGEMM_LDS* codes;   // the stage of the fragments that it reads
+    const char PGEMM_LDS* scales;  // the next K tile's scales in their group
+    uint32_t a, b;                 // where the wave's pieces of the free stage go
     int wm0, wn0, lane;
 };
 
-// One K step, with what else is to be done spread evenly between its MFMAs: the
-// reads of the next step's fragments; in a K tile's last step those are of the next
-// K tile, with its scales, and the pieces of the stage that has become free follow,
-// two instructions each; in its first step the producer's way to the next K tile.
-template <class C, int KS, bool LAST>
+// One K step, with what else is to be done spread between its MFMAs: reads of the
+// next step's fragments (behind the ready edge the next K tile's, its scales first)
+// and, in turns with them, half of a K tile's pieces, M0 first and the load an
+// instruction later.  A K tile's pieces begin in the step behind the ready edge that
+// frees their stage and end in the one that follows, so that they come at an even
+// pace: the address path takes 16 clocks a piece and CU.
+template <class C, bool LAST>
 struct MxStep {
     static constexpr int NMF = C::FM * C::FN, NR = C::FM * C::XCH + C::FN, NS = LAST ? C::FM + C::FN : 0;
-    static constexpr int MORE = LAST ? 2 * C::LPS : KS == 0 ? MxSrc<C>::PARTS : 0, JOBS = NR + NS + MORE;
+    static constexpr int HALF = C::LPS / 2, P0 = LAST ? 0 : HALF, NP = LAST ? HALF : C::LPS - HALF;
+    static constexpr int READS = NS + NR, PIECES = 2 * NP, ADV = LAST ? 0 : 2;
+    static constexpr int PAIRS = READS < PIECES ? READS : PIECES, JOBS = READS + PIECES + ADV;
+    template <int J>
+    static __device__ __forceinline__ void read(const MxAt& at, MxFrags<C>& nxt, MxScales<C>& sc) {
+        if constexpr (J < NS) mx_read_scale<C, J>(at.scales, at.wm0, at.wn0, at.lane, sc);
+        else mx_read<C, J - NS>(at.codes, LAST ? 0 : 1, at.wm0, at.wn0, at.lane, nxt);
+    }
+    template <int J, bool NOP>
+    static __device__ __forceinline__ void piece(const MxAt& at, const MxSrc<C>& src) {
+        if constexpr (J % 2 == 0) {
+            src.template place<P0 + J / 2>(at.a, at.b);
+            if constexpr (NOP) asm volatile("s_nop 0");
+        } else {
+            src.template load<P0 + J / 2>();
+        }
+    }
     template <int J>
     static __device__ __forceinline__ void job(const MxAt& at, MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src) {
-        if constexpr (J < NR) {
-            mx_read<C, J>(LAST ? at.next : at.cur, LAST ? 0 : KS + 1, at.wm0, at.wn0, at.lane, nxt);
-        } else if constexpr (J < NR + NS) {
-            mx_read_scale<C, J - NR>(at.scales, at.u, at.wm0, at.wn0, at.lane, sc);
-        } else if constexpr (LAST) {
-            constexpr int P = (J - NR - NS) / 2;
-            if constexpr ((J - NR - NS) % 2 == 0) src.template place<P>(at.a, at.b);
-            else src.template load<P>();
+        if constexpr (J < 2 * PAIRS) {
+            if constexpr (J % 2 == 0) read<J / 2>(at, nxt, sc);
+            else piece<J / 2, false>(at, src);
+        } else if constexpr (J < READS + PIECES) {
+            if constexpr (READS > PIECES) read<J - PIECES>(at, nxt, sc);
+            else piece<J - READS, true>(at, src);
         } else {
-            src.template advance<J - NR - NS>();
+            src.template advance<J - READS - PIECES>();
         }
     }
     template <int J, int END>
     static __device__ __forceinline__ void jobs(const MxAt& at, MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src) {
         if constexpr (J < END) {
             job<J>(at, nxt, sc, src);
-            // M0 and the load that uses it stand in one place: an instruction between them
-            if constexpr (LAST && J >= NR + NS && (J - NR - NS) % 2 == 0 && J + 1 < END) asm volatile("s_nop 0");
             jobs<J + 1, END>(at, nxt, sc, src);
         }
     }
@@ -287,28 +276,13 @@ struct MxStep {
                                                MxFrags<C>& nxt, MxScales<C>& sc, MxSrc<C>& src, const MxAt& at) {
         if constexpr (M < NMF) {
             constexpr int i = M / C::FN, j = M % C::FN;
-            mx_mfma<C, KS>(acc[i][j], use.a[i], use.b[j], us.a[i], us.b[j]);
+            mx_mfma<C, LAST ? 1 : 0>(acc[i][j], use.a[i], use.b[j], us.a[i], us.b[j]);
             jobs<M * JOBS / NMF, (M + 1) * JOBS / NMF>(at, nxt, sc, src);
             __builtin_amdgcn_sched_barrier(0);
             run<M + 1>(acc, use, us, nxt, sc, src, at);
         }
     }
 };
-// All K steps of one K tile, the ready edge of the next one before the last.
-template <class C, int KS = 0>
-__device__ __forceinline__ void mx_tile_steps(f32x16 (&acc)[C::FM][C::FN], MxFrags<C> (&f)[2], const MxScales<C>& us,
-                                              MxScales<C>& sc, MxSrc<C>& src, const MxAt& at) {
-    if constexpr (KS < C::NKS - 1) {
-        MxStep<C, KS, false>::run(acc, f[KS & 1], us, f[(KS & 1) ^ 1], sc, src, at);
-        mx_tile_steps<C, KS + 1>(acc, f, us, sc, src, at);
-    } else {
-        // The next K tile is in LDS (and the scales, which are older than the codes
-        // that may be under way), this one's stage is free.
-        wait_barrier<C::LPS*(C::S - 2)>();
-        if (at.s) src.scales(at.s);
-        MxStep<C, KS, true>::run(acc, f[KS & 1], us, f[(KS & 1) ^ 1], sc, src, at);
-    }
-}
 
 // The epilogue through LDS: as LinOut and lin_epilogue, on blocks of 32 x 32.
 template <class C>
@@ -446,17 +420,15 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
         const int x = blockIdx.x & 7;
         const int begin = g.splits == 1 ? (int)((int64_t)groups * (((x & 6) + 4 * (x & 1)) & 7) >> 3) : g0;
         const int first = begin * C::G;
-        src.turn = total - first;
-        src.left = t1 - t0;
+        src.k = first * (16 * C::KCB);
+        src.k_end = total * (16 * C::KCB);
         src.s_turn = groups - begin;
         src.s_left = g1 - g0;
         src.s_groups = groups;
-        src.back_a = -(int64_t)total * 16 * C::KCA;
-        src.back_b = -(int64_t)total * 16 * C::KCB;
         const int panel = C::NP == 2 ? wave / (C::NW / 2) : 0;  // the wave's pieces of B lie in one panel
         const int b_block = wave * C::B_INSTR - panel * (C::B_BYTES / C::NP / 1024);
-        src.ra = make_rsrc_sgpr((const char*)g.A + m0 * g.lda + first * (16 * C::KCA));
-        src.rb = make_rsrc_sgpr((const char*)(panel ? g.B[1] : g.B[0]) + n0 * g.ldb + first * (16 * C::KCB));
+        src.ra = make_rsrc_sgpr((const char*)g.A + m0 * g.lda);
+        src.rb = make_rsrc_sgpr((const char*)(panel ? g.B[1] : g.B[0]) + n0 * g.ldb);
 #pragma unroll
         for (int q = 0; q < C::A_INSTR; ++q) {
             int row, kc;
@@ -492,41 +464,51 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
         src.scales(at_s + C::S_STAGE);
 #pragma unroll
         for (int p = 0; p < C::S - 1; ++p) {
-            mx_pieces<C>(src, lds0 + p * C::STAGE + at_a, lds0 + p * C::STAGE + at_b);
-            src.advance_all();
+            mx_pieces<C, C::LPS>(src, lds0 + p * C::STAGE + at_a, lds0 + p * C::STAGE + at_b);
+            src.template advance<0>();
+            src.template advance<1>();
         }
         wait_barrier<C::LPS*(C::S - 2)>();
         constexpr uint32_t LASTST = (C::S - 1) * C::STAGE;
-        mx_pieces<C>(src, lds0 + LASTST + at_a, lds0 + LASTST + at_b);
+        mx_pieces<C, C::LPS / 2>(src, lds0 + LASTST + at_a, lds0 + LASTST + at_b);
         MxFrags<C> f[2];
-        MxScales<C> sc, next;
-        mx_first<C>(smem, smem + C::AT_S, wm0, wn0, lane, f[0], sc);
-        int cur = 0, u = 0, sst = 0, row_left = total - first;
-        for (int t = t0; t < t1; ++t) {
-            // the last K step's copies of the scales, two wait states before the first MFMA
-            asm volatile("s_nop 1");
-            const int nst = cur + 1 == C::S ? 0 : cur + 1;
-            // the next K tile's scales: of this group, or the next one where the group or the row ends
-            --row_left;
-            const bool ends = ++u == C::G || row_left == 0;
+        MxScales<C> sc[2];
+        mx_first<C>(smem, smem + C::AT_S, wm0, wn0, lane, f[0], sc[0]);
+        // Stages as bytes from the ring's beginning; the scales of the next K tile.
+        uint32_t cur = 0, prev = LASTST, scale = C::AT_S;
+        int row_left = (total - first) / 2, odd = 0;
+        const auto tile = [&](const MxScales<C>& us, MxScales<C>& next, uint32_t next_scale, uint32_t free_scales) {
+            const uint32_t nxt = cur == LASTST ? 0 : cur + C::STAGE;
             MxAt at;
-            at.cur = smem + cur * C::STAGE;
-            at.next = smem + nst * C::STAGE;
-            at.a = lds0 + cur * C::STAGE + at_a;
-            at.b = lds0 + cur * C::STAGE + at_b;
-            at.s = ends ? at_s + sst * C::S_STAGE : 0;
-            if (ends) {
-                u = 0;
-                sst ^= 1;
-            }
-            at.scales = smem + C::AT_S + sst * C::S_STAGE;
-            at.u = u;
             at.wm0 = wm0;
             at.wn0 = wn0;
             at.lane = lane;
-            mx_tile_steps<C>(acc, f, sc, next, src, at);
-            sc = next;
-            cur = nst;
+            at.scales = smem + next_scale;
+            at.codes = smem + cur;
+            at.a = lds0 + prev + at_a;
+            at.b = lds0 + prev + at_b;
+            MxStep<C, false>::run(acc, f[0], us, f[1], next, src, at);
+            // The next K tile is in LDS (and the scales, which are older than the codes
+            // that may be under way), this one's stage is free.
+            wait_barrier<C::LPS*(C::S - 2)>();
+            if (free_scales) src.scales(free_scales);
+            at.codes = smem + nxt;
+            at.a = lds0 + cur + at_a;
+            at.b = lds0 + cur + at_b;
+            MxStep<C, true>::run(acc, f[1], us, f[0], next, src, at);
+            prev = cur;
+            cur = nxt;
+        };
+        // K tiles come in pairs, half a group of scales; a row ends with a pair.
+        for (int t = t0; t < t1; t += 2) {
+            tile(sc[0], sc[1], scale + 4, 0);
+            const uint32_t stage = scale & ~15u;  // (places in a group are 0 and 8)
+            odd ^= 1;
+            const bool ends = --row_left == 0 || odd == 0;
+            const uint32_t other = (uint32_t)(2 * C::AT_S + C::S_STAGE) - stage;
+            odd = ends ? 0 : 1;
+            scale = ends ? other : stage + 8;
+            tile(sc[1], sc[0], scale, ends ? at_s + (stage - C::AT_S) : 0);
         }
         __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing LDS
     }

@@ -82,7 +82,7 @@ hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
 #define MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN) MxCfg<D, F, BM, BN, S, WGM, WGN, GATED != 0>
 #define MX_TILE(D, F, GATED, BM, BN, S, WGM, WGN)                                                               \
     MxVariant {                                                                                                 \
-        F, GATED, BM, GATED ? BN / 2 : BN, F == MX8 ? 128 : 256, 64 * WGM * WGN, 0,                             \
+        F, GATED, BM, GATED ? BN / 2 : BN, 128, 64 * WGM * WGN, 0,                                              \
             163840 / MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN)::LDS,                                        \
             &launch_mx_tile<MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN)>                                      \
     }
@@ -91,9 +91,9 @@ hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
         F, GATED, 16 * FM, 16 * FN, 256, 64 * NW, NW, 2, &launch_mx_few<MxFewCfg<D, F, FM, FN, NW, U, GATED != 0>> \
     }
 #define MX_CLASS(D, F, GATED, DEEP)                                                                             \
-    MX_TILE(D, F, GATED, 256, 256, (F == MX8 ? 3 : 2), 2, 2), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2),        \
+    MX_TILE(D, F, GATED, 256, 256, (F == MX8 ? 3 : 4), 2, 2), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2),        \
         MX_FEW(D, F, GATED, 1, 1, 8, 2), MX_FEW(D, F, GATED, 2, 1, 8, 2), MX_FEW(D, F, GATED, 4, 1, 8, 2)
-#define MX_VARIANTS(D) MX_CLASS(D, MX8, 0, 3), MX_CLASS(D, MX8, 1, 3), MX_CLASS(D, MX4, 0, 2), MX_CLASS(D, MX4, 1, 2)
+#define MX_VARIANTS(D) MX_CLASS(D, MX8, 0, 3), MX_CLASS(D, MX8, 1, 3), MX_CLASS(D, MX4, 0, 4), MX_CLASS(D, MX4, 1, 4)
 #define MX_KERNELS(D, norms, table)                                                                             \
     MxKernels {                                                                                                 \
         norms, (int)(sizeof(norms) / sizeof(norms[0])), &launch_quantize_any<D>, &launch_dequantize<D>, table,  \
