@@ -352,7 +352,7 @@ class _Call:
     depends on addresses (overlaps, the workspace) is checked at every call.
     """
 
-    __slots__ = ("dtype", "device", "index", "tensors", "pairs", "args", "need", "function")
+    __slots__ = ("dtype", "device", "index", "on_gpu", "tensors", "pairs", "near", "args", "need", "function", "bare")
 
     def __init__(self, X, name="X"):
         code = _FLOAT_CODE.get(X.dtype)
@@ -361,6 +361,7 @@ class _Call:
         self.dtype = code
         self.device = X.device
         self.index = X.device.index
+        self.on_gpu = X.device.type == "cuda"
         self.tensors = []  # (name, tensor's place among the operator's, bytes from first to last, written)
 
     def _place(self, name, slot, t, dtypes, out):
@@ -443,11 +444,14 @@ class _Call:
         return ((Q.stride(0) if rows > 1 else width), (S.stride(0) if rows > 1 else scales),
                 MX8 if width == entries else MX4, entries)
 
-    def done(self, function, need, args):
-        """`args(pointers)` gives the C function's arguments before the workspace."""
-        self.function, self.need, self.args = function, need, args
+    def done(self, function, need, args, bare=False):
+        """`args(pointers)` gives the C function's arguments before the workspace (bare: it takes none) and the stream."""
+        self.function, self.need, self.args, self.bare = function, need, args, bare
         self.pairs = [(i, bi, j, bj) for x, (_, i, bi, oi) in enumerate(self.tensors)
                       for _, j, bj, oj in self.tensors[x + 1:] if oi or oj]
+        # whether the byte ranges of any of them meet, written out: a third of the loop's time
+        self.near = eval("lambda p: " + (" or ".join("p[%d] < p[%d] + %d and p[%d] < p[%d] + %d" % (i, j, bj, j, i, bi)
+                                                     for i, bi, j, bj in self.pairs) or "False"))
         return self
 
     def _overlap(self, ts, i, j, same):
@@ -466,18 +470,19 @@ class _Call:
     def run(self, ts, workspace, stream, same=()):
         """Launches on the tensors' GPU; `same`: pairs of places, of an input and an output that may be one matrix."""
         p = [None if t is None else t.data_ptr() for t in ts]
-        for i, bi, j, bj in self.pairs:
-            if p[i] < p[j] + bj and p[j] < p[i] + bi:
-                self._overlap(ts, i, j, same)
+        if self.near(p):
+            for i, bi, j, bj in self.pairs:
+                if p[i] < p[j] + bj and p[j] < p[i] + bi:
+                    self._overlap(ts, i, j, same)
         if stream is not None and getattr(stream, "device", self.device) != self.device:
             raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, self.device))
         index = self.index
-        if self.device.type != "cuda":
+        if not self.on_gpu:
             raise ValueError("the tensors must be on a GPU, got %s" % self.device)
         need = self.need
         if need < 0:
             raise PgemmError(need)
-        if index != torch.cuda.current_device():
+        if index != _current_device():
             with torch.cuda.device(index):
                 return self.run(ts, workspace, stream, same)
         if workspace is not None:
@@ -494,7 +499,8 @@ class _Call:
                                    torch.cuda.ExternalStream(stream, device=self.device)):
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
             w, n = workspace.data_ptr(), need
-        r = self.function(*self.args(p), w, n, _raw_stream(index) if stream is None else _stream(stream))
+        s = _raw_stream(index) if stream is None else _stream(stream)
+        r = self.function(*self.args(p), s) if self.bare else self.function(*self.args(p), w, n, s)
         if r != 0:
             raise PgemmError(r)
 
@@ -516,7 +522,7 @@ _CALLS = {}
 def _cached(describe, ts, act):
     """The checked call of these types, shapes, strides and devices."""
     try:
-        key = (describe, act) + tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in ts])
+        key = (describe, act, *[None if t is None else (t.shape, t.stride(), t.dtype, t.get_device()) for t in ts])
         c = _CALLS.get(key)
     except TypeError:  # an activation that is no name
         raise ValueError("unknown activation %r: one of %s" % (act, ", ".join(ACT))) from None
@@ -539,6 +545,7 @@ try:
     _OWN_TYPE = {c: (t,) for c, t in _BY_CODE.items()}
     _CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
     _SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
 except NameError:  # without torch only the C entry points above are used
@@ -815,8 +822,8 @@ def _describe_rms_norm(X, weight, Y, residual, H, Q, S, eps):
     ldh = c.rows("H", 4, H, (M, N), own, True)
     ldq, lds, form, _ = c.blocks("mx", (5, 6), Q, S, M, -(-N // 256) * 256, True)
     out = t if Y is None else _FLOAT_CODE[Y.dtype]
-    return c.done(lambda *a: pgemm_rms_norm(*a[:-3], a[-1]), 0, lambda p: (
-        M, N, p[0], ldx, p[3], ldr, p[1], eps, p[4], ldh, p[2], ldy, out, p[5], ldq, p[6], lds, form, t))
+    return c.done(pgemm_rms_norm, 0, lambda p: (
+        M, N, p[0], ldx, p[3], ldr, p[1], eps, p[4], ldh, p[2], ldy, out, p[5], ldq, p[6], lds, form, t), True)
 
 
 def rms_norm_backward(dY, H, weight=None, dH=None, dX=None, dweight=None, eps=1e-6, workspace=None, stream=None):
@@ -873,8 +880,8 @@ def _describe_mx_quantize(X, Q, S, _):
     ldq, lds, form, _ = c.blocks("mx", (1, 2), Q, S, rows, -(-K // 256) * 256, True)
     # weight() calls rows of X[rows][K] K x N, of which the C entry's NK is the other one
     order = ORDER_NK if order == ORDER_KN else ORDER_KN
-    return c.done(lambda *a: pgemm_mx_quantize(*a[:-3], a[-1]), 0, lambda p: (
-        rows, K, p[0], ldx, order, c.dtype, p[1], ldq, p[2], lds, form))
+    return c.done(pgemm_mx_quantize, 0, lambda p: (
+        rows, K, p[0], ldx, order, c.dtype, p[1], ldq, p[2], lds, form), True)
 
 
 def mx_dequantize(mx, X, stream=None):
@@ -894,8 +901,8 @@ def _describe_mx_dequantize(X, Q, S, _):
     c = _Call(X)
     ldx = c.rows("X", 0, X, (rows, K), _OWN_TYPE[c.dtype], True)
     ldq, lds, form, _ = c.blocks("mx", (1, 2), Q, S, rows, -(-K // 256) * 256)
-    return c.done(lambda *a: pgemm_mx_dequantize(*a[:-3], a[-1]), 0, lambda p: (
-        rows, K, p[1], ldq, p[2], lds, form, p[0], ldx, c.dtype))
+    return c.done(pgemm_mx_dequantize, 0, lambda p: (
+        rows, K, p[1], ldq, p[2], lds, form, p[0], ldx, c.dtype), True)
 
 
 def mx_linear(X, W, Y, bias=None, residual=None, act="none", workspace=None, stream=None):

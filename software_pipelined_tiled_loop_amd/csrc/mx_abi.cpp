@@ -68,24 +68,34 @@ int check_workspace(const void* p, int64_t bytes, int64_t need) {
 // Workgroups for `items`, `per` at a time; kernels go on from there by themselves.
 int grid_for(int64_t items, int64_t per) { return (int)smaller(ceil_div(items, per), 1 << 20); }
 
+// How the threads of mx_quantize_rows and mx_dequantize_rows share rows of `groups` groups of eight; returns the grid.
+int share_rows(MxCopyArgs& a, int64_t groups) {
+    a.shift = 5;
+    while (a.shift < 8 && ((int64_t)kRun << a.shift) < groups) ++a.shift;
+    a.stretches = (int)ceil_div(groups, (int64_t)kRun << a.shift);
+    return grid_for(ceil_div(a.rows, 256 >> a.shift) * a.stretches, 1);
+}
+
 // ---- the norm ----------------------------------------------------------------------------------
 
 // The first kernel whose row holds `filled` columns.
-const NormVariant& norm_variant(const MxKernels& k, int64_t filled) {
+template <class Args>
+const NormVariant<Args>& norm_variant(const NormTable<Args>& t, int64_t filled) {
     int i = 0;
-    while (i + 1 < k.num_norms && (int64_t)k.norms[i].threads * k.norms[i].groups * 8 < filled) ++i;
-    return k.norms[i];
+    while (i + 1 < t.n && (int64_t)t.v[i].threads * t.v[i].groups * 8 < filled) ++i;
+    return t.v[i];
 }
-int64_t rows_at_once(const NormVariant& v) { return v.threads < 256 ? 256 / v.threads : 1; }
 
-// Blocks of rows of the backward pass: their sums are joined afterwards.
+// Blocks of rows of the backward pass, one a CU; their sums are joined afterwards.
 struct NormBlocks {
     int64_t rows, blocks, np8;
 };
-NormBlocks norm_blocks(int64_t M, int64_t N, const NormVariant& v) {
+NormBlocks norm_blocks(int64_t M, int64_t N, const NormVariant<NormGradArgs>& v) {
     NormBlocks b;
-    const int64_t at_once = rows_at_once(v), most = 2 * kNumCU;
-    b.rows = round_up(ceil_div(M > 0 ? M : 1, most), at_once);
+    const int64_t at_once = v.groups ? kNormGradThreads / v.threads : 1, steps = ceil_div(M, at_once);
+    // up to four steps stay in one block, which writes the sums itself
+    b.rows = (steps <= 4 ? steps : ceil_div(steps, kNumCU)) * at_once;
+    if (b.rows == 0) b.rows = at_once;
     b.blocks = ceil_div(M, b.rows);
     b.np8 = round_up(N, 8);
     return b;
@@ -244,8 +254,9 @@ extern "C" {
 
 int64_t pgemm_rms_norm_backward_workspace(int64_t M, int64_t N, int dtype) {
     PGEMM_TRY(check_sizes(M, N, dtype));
-    const NormBlocks b = norm_blocks(M, N, norm_variant(kernels_for(dtype), N));
-    return round_up(b.blocks * b.np8 * 4, 256);
+    const NormVariant<NormGradArgs>& v = norm_variant(kernels_for(dtype).norm_grad, N);
+    const NormBlocks b = norm_blocks(M, N, v);
+    return b.blocks > 1 || (v.groups == 0 && M > 0) ? round_up(b.blocks * b.np8 * 4, 256) : 0;
 }
 
 int pgemm_rms_norm(int64_t M, int64_t N, const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight,
@@ -282,8 +293,8 @@ int pgemm_rms_norm(int64_t M, int64_t N, const void* X, int64_t ldx, const void*
     a.filled = (int)(Q ? mx_filled(N) : N);
     a.y_f32 = out_dtype == PGEMM_F32;
     a.format = format;
-    const NormVariant& v = norm_variant(kernels_for(dtype), a.filled);
-    return launched("rms_norm", v.norm(a, grid_for(M, rows_at_once(v)), (hipStream_t)stream));
+    const NormVariant<NormArgs>& v = norm_variant(kernels_for(dtype).norm, a.filled);
+    return launched("rms_norm", v.launch(a, grid_for(M, v.threads < 256 ? 256 / v.threads : 1), (hipStream_t)stream));
 }
 
 int pgemm_rms_norm_backward(int64_t M, int64_t N, const void* dY, int64_t lddy, const void* H, int64_t ldh,
@@ -301,8 +312,10 @@ int pgemm_rms_norm_backward(int64_t M, int64_t N, const void* dY, int64_t lddy, 
     PGEMM_TRY(check_vector(dweight, elem_size(grad_dtype)));
     if (N == 0 || (!dX && !dweight)) return PGEMM_OK;
     if (dweight) PGEMM_TRY(check_workspace(workspace, workspace_bytes, pgemm_rms_norm_backward_workspace(M, N, dtype)));
-    const NormVariant& v = norm_variant(kernels_for(dtype), N);
+    const MxKernels k = kernels_for(dtype);
+    const NormVariant<NormGradArgs>& v = norm_variant(k.norm_grad, N);
     const NormBlocks b = norm_blocks(M, N, v);
+    const bool joined = b.blocks != 1 || v.groups == 0;
     if (M > 0) {
         NormGradArgs a;
         std::memset(&a, 0, sizeof(a));
@@ -311,7 +324,9 @@ int pgemm_rms_norm_backward(int64_t M, int64_t N, const void* dY, int64_t lddy, 
         a.w = weight;
         a.dH = dH;
         a.dX = dX;
-        a.sums = dweight ? (float*)workspace : nullptr;
+        if (joined) a.sums = dweight ? (float*)workspace : nullptr;
+        else a.dw = dweight;
+        a.dw_f32 = grad_dtype == PGEMM_F32;
         a.lddy = lddy;
         a.ldh = ldh;
         a.lddh = lddh;
@@ -321,20 +336,18 @@ int pgemm_rms_norm_backward(int64_t M, int64_t N, const void* dY, int64_t lddy, 
         a.N = (int)N;
         a.np8 = (int)b.np8;
         a.rows = (int)b.rows;
-        PGEMM_TRY(launched("rms_norm_grad", v.grad(a, (int)b.blocks, (hipStream_t)stream)));
+        PGEMM_TRY(launched("rms_norm_grad", v.launch(a, (int)b.blocks, (hipStream_t)stream)));
     }
-    if (!dweight) return PGEMM_OK;
-    SumArgs t;
+    if (!dweight || !joined) return PGEMM_OK;
+    NormSumArgs t;
     std::memset(&t, 0, sizeof(t));
     t.sums = (const float*)workspace;
-    t.out[0] = dweight;
+    t.out = dweight;
     t.blocks = (int)b.blocks;
-    t.planes = 1;
     t.np8 = (int)b.np8;
     t.N = (int)N;
     t.out_f32 = grad_dtype == PGEMM_F32;
-    const LinKernels k = dtype == PGEMM_F32 ? linear_kernels_f32() : dtype == PGEMM_F16 ? linear_kernels_f16() : linear_kernels_bf16();
-    return launched("linear_colsum", k.colsum(t, grid_for(N, 64), (hipStream_t)stream));
+    return launched("rms_norm_join", k.norm_join(t, grid_for(N, 16), (hipStream_t)stream));
 }
 
 int pgemm_mx_quantize(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_order, int dtype, void* Q, int64_t ldq,
@@ -358,7 +371,7 @@ int pgemm_mx_quantize(int64_t rows, int64_t K, const void* X, int64_t ldx, int x
     a.K = (int)K;
     a.filled = (int)mx_filled(K);
     const bool columns = x_order == PGEMM_KN;
-    const int grid = columns ? grid_for(ceil_div(rows, 64) * (a.filled / 128), 1) : grid_for(rows * (a.filled / 8), 256);
+    const int grid = columns ? grid_for(ceil_div(rows, 256) * (a.filled / 256), 1) : share_rows(a, a.filled / 8);
     return launched("mx_quantize", kernels_for(dtype).quantize(a, format, columns, grid, (hipStream_t)stream));
 }
 
@@ -379,7 +392,8 @@ int pgemm_mx_dequantize(int64_t rows, int64_t K, const void* Q, int64_t ldq, con
     a.rows = (int)rows;
     a.K = (int)K;
     a.filled = (int)mx_filled(K);
-    return launched("mx_dequantize", kernels_for(dtype).dequantize(a, format, grid_for(rows * ceil_div(K, 8), 256), (hipStream_t)stream));
+    const int grid = share_rows(a, ceil_div(K, 8));
+    return launched("mx_dequantize", kernels_for(dtype).dequantize(a, format, grid, (hipStream_t)stream));
 }
 
 int64_t pgemm_mx_linear_workspace(int64_t M, int64_t N, int64_t K, int x_format) {

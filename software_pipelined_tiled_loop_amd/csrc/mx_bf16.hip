@@ -3,9 +3,10 @@
 
 namespace pgemm {
 
-static const NormVariant k_norms[] = {NORM_VARIANTS(DT_BF16)};
+static const NormVariant<NormArgs> k_norms[] = {NORM_VARIANTS(DT_BF16)};
+static const NormVariant<NormGradArgs> k_grads[] = {NORM_GRAD_VARIANTS(DT_BF16)};
 static const MxVariant k_table[] = {MX_VARIANTS(DT_BF16)};
 
-MxKernels mx_kernels_bf16() { return MX_KERNELS(DT_BF16, k_norms, k_table); }
+MxKernels mx_kernels_bf16() { return MX_KERNELS(DT_BF16, k_norms, k_grads, k_table); }
 
 }  // namespace pgemm

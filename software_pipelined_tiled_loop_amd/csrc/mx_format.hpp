@@ -110,7 +110,13 @@ struct MxCopyArgs {
     int64_t ldx, ldq, lds;  // elements; bytes
     int rows, K;
     int filled;     // entries of a stored row
+    int shift;      // log2 of the threads that share a row's stretch
+    int stretches;  // of a row
 };
+
+// Rows of eight entries a thread: a workgroup has 256 >> shift rows (a row's stretch
+// of 256 kRun groups of eight where rows are longer).
+constexpr int kRun = 2;
 
 template <class T>
 struct __attribute__((packed, aligned(sizeof(T)))) Packed8 {
@@ -154,66 +160,138 @@ __device__ __forceinline__ void mx_put8(char* q, uint8_t* s, int k, const f32x8&
     if ((k & 31) == 0) s[k >> 5] = (uint8_t)byte;
 }
 
+// Where a thread of a workgroup stands: its row, and its first entry; the following ones are `step` further on.
+struct MxPlace {
+    int64_t row;
+    int k, step;
+};
+__device__ __forceinline__ MxPlace mx_place(const MxCopyArgs& g, int64_t b) {
+    const int64_t lot = g.stretches == 1 ? b : b / g.stretches;
+    const int stretch = (int)(b - lot * g.stretches), t = (int)threadIdx.x & ((1 << g.shift) - 1);
+    return MxPlace{(lot << (8 - g.shift)) + ((int)threadIdx.x >> g.shift), (stretch * (kRun << g.shift) + t) * 8, 8 << g.shift};
+}
+
 // Rows whose entries lie side by side: a lane has eight of them, four lanes a block.
+// Bound by memory.
 template <int D, int F>
 __global__ void __launch_bounds__(256) mx_quantize_rows(MxCopyArgs g) {
     typedef typename Elem<D>::type T;
-    const int per_row = g.filled / 8;
-    const int64_t total = (int64_t)g.rows * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / per_row;
-        const int k = (int)(i - row * per_row) * 8;
-        const f32x8 v = load8_at((const T*)g.X + row * g.ldx + k, g.K - k);
-        mx_put8<F>((char*)g.Q + row * g.ldq, (uint8_t*)g.S + row * g.lds, k, v);
-    }
-}
-
-// Rows that are columns in memory (a weight stored K x N): a thread has one row's block.
-template <int D, int F>
-__global__ void __launch_bounds__(256) mx_quantize_columns(MxCopyArgs g) {
-    typedef typename Elem<D>::type T;
-    const int blocks = g.filled / 32;
-    const int64_t strips = ((int64_t)g.rows + 63) / 64, total = strips * (blocks / 4);
-    for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-        const int64_t row = i % strips * 64 + (threadIdx.x & 63);
-        const int b = (int)(i / strips) * 4 + (int)(threadIdx.x >> 6);
-        if (row >= g.rows) continue;
-        const T* x = (const T*)g.X + (int64_t)b * 32 * g.ldx + row;
-        f32x8 v[4];
-        uint32_t most = 0;
+    const int64_t lots = ((int64_t)g.rows + (256 >> g.shift) - 1) >> (8 - g.shift);
+    for (int64_t b = blockIdx.x; b < lots * g.stretches; b += gridDim.x) {
+        const MxPlace p = mx_place(g, b);
+        if (p.row >= g.rows) continue;
+        f32x8 v[kRun];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j / 8][j % 8] = b * 32 + j < g.K ? (float)x[j * g.ldx] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) most = max(most, largest8(v[j]));
-        const uint32_t byte = mx_scale_byte<F>(most);
-        i32x2 c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = mx_codes<F>(v[j], byte);
-        char* q = (char*)g.Q + row * g.ldq + b * (F == MX8 ? 32 : 16);
-        if constexpr (F == MX8) {
-            *(i32x4*)q = i32x4{c[0][0], c[0][1], c[1][0], c[1][1]};
-            *(i32x4*)(q + 16) = i32x4{c[2][0], c[2][1], c[3][0], c[3][1]};
-        } else {
-            *(i32x4*)q = i32x4{c[0][0], c[1][0], c[2][0], c[3][0]};
+        for (int i = 0; i < kRun; ++i) {
+            const int k = p.k + i * p.step;
+            v[i] = load8_at((const T*)g.X + p.row * g.ldx + k, g.K - k);
         }
-        ((uint8_t*)g.S)[row * g.lds + b] = (uint8_t)byte;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const int k = p.k + i * p.step;
+            if (k < g.filled) mx_put8<F>((char*)g.Q + p.row * g.ldq, (uint8_t*)g.S + p.row * g.lds, k, v[i]);
+        }
     }
 }
 
 template <int D, int F>
 __global__ void __launch_bounds__(256) mx_dequantize_rows(MxCopyArgs g) {
     typedef typename Elem<D>::type T;
-    const int per_row = (g.K + 7) / 8;
-    const int64_t total = (int64_t)g.rows * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / per_row;
-        const int k = (int)(i - row * per_row) * 8;
-        const char* q = (const char*)g.Q + row * g.ldq;
-        i32x2 c = {0, 0};
-        if constexpr (F == MX8) c = *(const i32x2*)(q + k);
-        else c[0] = *(const int*)(q + k / 2);
-        const f32x8 v = mx_values<F>(c, ((const uint8_t*)g.S)[row * g.lds + (k >> 5)]);
-        store8_at((T*)g.X + row * g.ldx + k, v, g.K - k);
+    const int64_t lots = ((int64_t)g.rows + (256 >> g.shift) - 1) >> (8 - g.shift);
+    for (int64_t b = blockIdx.x; b < lots * g.stretches; b += gridDim.x) {
+        const MxPlace p = mx_place(g, b);
+        if (p.row >= g.rows) continue;
+        const char* q = (const char*)g.Q + p.row * g.ldq;
+        i32x2 c[kRun];
+        uint32_t s[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const int k = p.k + i * p.step;
+            c[i] = i32x2{0, 0};
+            s[i] = 0;
+            if (k >= g.K) continue;
+            if constexpr (F == MX8) c[i] = *(const i32x2*)(q + k);
+            else c[i][0] = *(const int*)(q + k / 2);
+            s[i] = ((const uint8_t*)g.S)[p.row * g.lds + (k >> 5)];
+        }
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const int k = p.k + i * p.step;
+            store8_at((T*)g.X + p.row * g.ldx + k, mx_values<F>(c[i], s[i]), g.K - k);
+        }
+    }
+}
+
+template <class T>
+struct __attribute__((packed, aligned(sizeof(T)))) Packed4 {
+    T v[4];
+};
+// Rows that are columns in memory (a weight stored K x N).  A workgroup has 256
+// rows by 256 entries: a wave the rows' blocks of 32, a thread four rows' block,
+// loaded in 32 stretches of four elements that lie side by side over the lanes.
+// Codes and scales go through LDS, so that rows are written in whole lines.
+template <int D, int F>
+__global__ void __launch_bounds__(512) mx_quantize_columns(MxCopyArgs g) {
+    typedef typename Elem<D>::type T;
+    constexpr int CB = F == MX8 ? 32 : 16, RB = 8 * CB, CHUNKS = RB / 16;  // bytes of a block's codes, of a row's; its chunks
+    __shared__ __attribute__((aligned(16))) char codes[256 * RB];
+    __shared__ __attribute__((aligned(8))) uint8_t scales[256 * 8];
+    const int lane = (int)threadIdx.x & 63, blk = (int)threadIdx.x >> 6;
+    const int64_t strips = ((int64_t)g.rows + 255) / 256, total = strips * (g.filled / 256);
+    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+        const int64_t row0 = b % strips * 256;
+        const int k0 = (int)(b / strips) * 256, kb = k0 + 32 * blk;
+        const int64_t row = row0 + 4 * lane;
+        const int valid = (int)(g.rows - row < 4 ? g.rows - row : 4);
+        const T* x = (const T*)g.X + (int64_t)kb * g.ldx + row;
+        Packed4<T> raw[32];
+        if (row0 + 256 <= g.rows && kb + 32 <= g.K) {  // all of the workgroup's rows: no branch between the loads
+#pragma unroll
+            for (int j = 0; j < 32; ++j) raw[j] = *(const Packed4<T>*)(x + j * g.ldx);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) raw[j].v[e] = kb + j < g.K && e < valid ? x[j * g.ldx + e] : (T)0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f32x8 v[4];
+            uint32_t most = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j / 8][j % 8] = (float)raw[j].v[e];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) most = max(most, largest8(v[j]));
+            const uint32_t byte = mx_scale_byte<F>(most);
+            i32x2 c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = mx_codes<F>(v[j], byte);
+            const int r = 4 * lane + e;
+            // chunks of a row XOR-swizzled by the lane against bank conflicts
+            const auto put = [&](int chunk, i32x4 q) { *(i32x4*)(codes + r * RB + ((chunk ^ (lane & 7)) << 4)) = q; };
+            if constexpr (F == MX8) {
+                put(2 * blk, i32x4{c[0][0], c[0][1], c[1][0], c[1][1]});
+                put(2 * blk + 1, i32x4{c[2][0], c[2][1], c[3][0], c[3][1]});
+            } else {
+                put(blk, i32x4{c[0][0], c[1][0], c[2][0], c[3][0]});
+            }
+            scales[r * 8 + blk] = (uint8_t)byte;
+        }
+        __syncthreads();
+        const int64_t left = g.rows - row0;
+        for (int i = (int)threadIdx.x; i < 256 * CHUNKS; i += 512) {
+            const int r = i / CHUNKS, chunk = i % CHUNKS;
+            if (r < left)
+                *(i32x4*)((char*)g.Q + (row0 + r) * g.ldq + (int64_t)k0 * CB / 32 + chunk * 16) =
+                    *(const i32x4*)(codes + r * RB + ((chunk ^ ((r >> 2) & 7)) << 4));
+        }
+        if (threadIdx.x < 256 && (int)threadIdx.x < left) {
+            // (rows of scales are 4-byte aligned)
+            int* s = (int*)((uint8_t*)g.S + (row0 + threadIdx.x) * g.lds + k0 / 32);
+            s[0] = *(const int*)(scales + threadIdx.x * 8);
+            s[1] = *(const int*)(scales + threadIdx.x * 8 + 4);
+        }
+        __syncthreads();
     }
 }
 

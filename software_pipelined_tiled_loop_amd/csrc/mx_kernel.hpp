@@ -603,10 +603,11 @@ __global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
 
     const int total = g.filled / 256;
     const int t0 = (int)((int64_t)total * split / g.splits), t1 = (int)((int64_t)total * (split + 1) / g.splits);
-    // Unit t, zeros past the last one.
+    // The wave's stretch of them, in a row, so that a line of scales serves several; unit t, zeros past the last one.
+    const int first = t0 + (t1 - t0) * wave / C::NW, end = t0 + (t1 - t0) * (wave + 1) / C::NW;
     const auto fetch = [&](MxUnit<C>& u, int t) {
         const auto rsrc = [&](const char* p) {
-            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, t < t1 ? 0x80000000u : 0u, 0x00020000);
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, t < end ? 0x80000000u : 0u, 0x00020000);
         };
         const auto get = [](const __amdgpu_buffer_rsrc_t& s, uint32_t v) {
             return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(s, v, 0, 0));
@@ -649,20 +650,19 @@ __global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
                         (int)((uint32_t)u.sb[j][k] >> (8 * q)), 0, sx);
             }
     };
-    int t = t0 + wave;
-    if (t < t1) {
+    if (first < end) {
         MxUnit<C> u[C::U];
 #pragma unroll
-        for (int i = 0; i < C::U; ++i) fetch(u[i], t + i * C::NW);
-        while (true) {
+        for (int i = 0; i < C::U; ++i) fetch(u[i], first + i);
+        for (int t = first + C::U; t < end; t += C::U) {
 #pragma unroll
             for (int i = 0; i < C::U; ++i) {
                 multiply(u[i]);
-                fetch(u[i], t + (i + C::U) * C::NW);
+                fetch(u[i], t + i);
             }
-            t += C::U * C::NW;
-            if (t >= t1) break;
         }
+#pragma unroll
+        for (int i = 0; i < C::U; ++i) multiply(u[i]);
     }
 
     // The waves' sums.

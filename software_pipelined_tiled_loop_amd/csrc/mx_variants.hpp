@@ -10,10 +10,15 @@
 namespace pgemm {
 
 // The norm's kernels by the groups of eight columns that they hold: threads of a row, groups a thread.
+template <class Args>
 struct NormVariant {
-    int threads, groups;
-    hipError_t (*norm)(const NormArgs&, int grid, hipStream_t);
-    hipError_t (*grad)(const NormGradArgs&, int grid, hipStream_t);
+    int threads, groups;  // no groups: rows of any length
+    hipError_t (*launch)(const Args&, int grid, hipStream_t);
+};
+template <class Args>
+struct NormTable {
+    const NormVariant<Args>* v;  // by what they hold
+    int n;
 };
 
 // A kernel of the products.
@@ -27,8 +32,9 @@ struct MxVariant {
 };
 
 struct MxKernels {
-    const NormVariant* norms;  // by capacity; the last one holds any row
-    int num_norms;
+    NormTable<NormArgs> norm;
+    NormTable<NormGradArgs> norm_grad;
+    hipError_t (*norm_join)(const NormSumArgs&, int grid, hipStream_t);
     hipError_t (*quantize)(const MxCopyArgs&, int format, bool columns, int grid, hipStream_t);
     hipError_t (*dequantize)(const MxCopyArgs&, int format, int grid, hipStream_t);
     const MxVariant* v;
@@ -42,7 +48,11 @@ hipError_t launch_norm(const NormArgs& a, int grid, hipStream_t s) {
 }
 template <int D, int TPR, int CH>
 hipError_t launch_norm_grad(const NormGradArgs& a, int grid, hipStream_t s) {
-    return lin_launch<NormGradArgs>(&rms_norm_grad<D, TPR, CH>, a, dim3(grid), norm_threads<TPR>, s);
+    return lin_launch<NormGradArgs>(&rms_norm_grad<D, TPR, CH>, a, dim3(grid), kNormGradThreads, s);
+}
+template <int D>
+hipError_t launch_norm_join(const NormSumArgs& a, int grid, hipStream_t s) {
+    return lin_launch<NormSumArgs>(&rms_norm_join<D>, a, dim3(grid), 256, s);
 }
 template <int D>
 hipError_t launch_norm_long(const NormArgs& a, int grid, hipStream_t s) {
@@ -54,7 +64,7 @@ hipError_t launch_norm_grad_long(const NormGradArgs& a, int grid, hipStream_t s)
 }
 template <int D, int F>
 hipError_t launch_quantize(const MxCopyArgs& a, bool columns, int grid, hipStream_t s) {
-    return columns ? lin_launch<MxCopyArgs>(&mx_quantize_columns<D, F>, a, dim3(grid), 256, s)
+    return columns ? lin_launch<MxCopyArgs>(&mx_quantize_columns<D, F>, a, dim3(grid), 512, s)
                    : lin_launch<MxCopyArgs>(&mx_quantize_rows<D, F>, a, dim3(grid), 256, s);
 }
 template <int D>
@@ -75,10 +85,15 @@ hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
     return lin_launch<MxArgs>(&mx_few<C>, a, dim3(grid), C::NT, s);
 }
 
-#define NORM_VARIANT(D, TPR, CH) NormVariant{TPR, CH, &launch_norm<D, TPR, CH>, &launch_norm_grad<D, TPR, CH>}
-#define NORM_VARIANTS(D)                                                                                        \
-    NORM_VARIANT(D, 64, 1), NORM_VARIANT(D, 64, 2), NORM_VARIANT(D, 256, 1), NORM_VARIANT(D, 256, 2),           \
-        NORM_VARIANT(D, 1024, 1), NORM_VARIANT(D, 1024, 2), NormVariant{1024, 0, &launch_norm_long<D>, &launch_norm_grad_long<D>}
+#define NORM_VARIANT(D, TPR, CH) NormVariant<NormArgs>{TPR, CH, &launch_norm<D, TPR, CH>}
+#define NORM_VARIANTS(D)                                                                                  \
+    NORM_VARIANT(D, 64, 1), NORM_VARIANT(D, 64, 2), NORM_VARIANT(D, 256, 1), NORM_VARIANT(D, 256, 2),     \
+        NORM_VARIANT(D, 1024, 1), NORM_VARIANT(D, 1024, 2), NormVariant<NormArgs>{1024, 0, &launch_norm_long<D>}
+#define NORM_GRAD_VARIANT(D, TPR, CH) NormVariant<NormGradArgs>{TPR, CH, &launch_norm_grad<D, TPR, CH>}
+#define NORM_GRAD_VARIANTS(D)                                                                             \
+    NORM_GRAD_VARIANT(D, 64, 1), NORM_GRAD_VARIANT(D, 128, 1), NORM_GRAD_VARIANT(D, 256, 1),              \
+        NORM_GRAD_VARIANT(D, 512, 1), NORM_GRAD_VARIANT(D, 1024, 1), NORM_GRAD_VARIANT(D, 1024, 2),       \
+        NormVariant<NormGradArgs>{1024, 0, &launch_norm_grad_long<D>}
 #define MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN) MxCfg<D, F, BM, BN, S, WGM, WGN, GATED != 0>
 #define MX_TILE(D, F, GATED, BM, BN, S, WGM, WGN)                                                               \
     MxVariant {                                                                                                 \
@@ -94,9 +109,10 @@ hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
     MX_TILE(D, F, GATED, 256, 256, (F == MX8 ? 3 : 4), 2, 2), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2),        \
         MX_FEW(D, F, GATED, 1, 1, 8, 2), MX_FEW(D, F, GATED, 2, 1, 8, 2), MX_FEW(D, F, GATED, 4, 1, 8, 2)
 #define MX_VARIANTS(D) MX_CLASS(D, MX8, 0, 3), MX_CLASS(D, MX8, 1, 3), MX_CLASS(D, MX4, 0, 4), MX_CLASS(D, MX4, 1, 4)
-#define MX_KERNELS(D, norms, table)                                                                             \
+#define MX_KERNELS(D, norms, grads, table)                                                                      \
     MxKernels {                                                                                                 \
-        norms, (int)(sizeof(norms) / sizeof(norms[0])), &launch_quantize_any<D>, &launch_dequantize<D>, table,  \
+        {norms, (int)(sizeof(norms) / sizeof(norms[0]))}, {grads, (int)(sizeof(grads) / sizeof(grads[0]))},     \
+            &launch_norm_join<D>, &launch_quantize_any<D>, &launch_dequantize<D>, table,  \
             (int)(sizeof(table) / sizeof(table[0])), &lin_launch_join<D, false>, &lin_launch_join<D, true>      \
     }
 

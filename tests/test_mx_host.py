@@ -23,7 +23,7 @@ def call(function, defaults):
 
 norm = call(lib.pgemm_rms_norm, dict(M=6, N=300, X=FAKE, ldx=300, R=FAKE, ldr=300, w=FAKE, eps=1e-6, H=FAKE, ldh=300, Y=FAKE,
                                      ldy=300, out=2, Q=FAKE, ldq=512, S=FAKE, lds=16, form=0, dtype=2))
-norm_grad = call(lib.pgemm_rms_norm_backward, dict(M=6, N=300, dY=FAKE, lddy=300, H=FAKE, ldh=300, w=FAKE, eps=1e-6, dH=FAKE,
+norm_grad = call(lib.pgemm_rms_norm_backward, dict(M=600, N=300, dY=FAKE, lddy=300, H=FAKE, ldh=300, w=FAKE, eps=1e-6, dH=FAKE,
                                                    lddh=300, dX=FAKE, lddx=300, dw=FAKE, grad=2, dtype=2, ws=FAKE, n=1 << 40))
 quantize = call(lib.pgemm_mx_quantize, dict(M=6, K=300, X=FAKE, ldx=300, order=1, dtype=2, Q=FAKE, ldq=512, S=FAKE, lds=16,
                                             form=0))
@@ -84,7 +84,9 @@ def test_empty_calls_launch_nothing():
 
 def test_workspaces():
     assert lib.pgemm_rms_norm_backward_workspace(0, 64, 2) == 0
-    assert lib.pgemm_rms_norm_backward_workspace(1, 64, 2) == 256
+    assert lib.pgemm_rms_norm_backward_workspace(1, 64, 2) == 0  # few rows: no sums to join
+    assert lib.pgemm_rms_norm_backward_workspace(1, 1 << 20, 2) == 4 << 20  # a row too long for the registers keeps them there
+    assert lib.pgemm_rms_norm_backward_workspace(4096, 4096, 2) % 16384 == 0
     assert lib.pgemm_rms_norm_backward_workspace(5, 4, 3) == DTYPE
     for f in (lib.pgemm_mx_linear_workspace, lib.pgemm_mx_gated_workspace):
         assert f(1, 1, 1, 0) >= 0 and f(1, 1, 1, 2) == INVALID and f(-1, 1, 1, 0) == INVALID and f(1, 1 << 21, 1, 1) == LARGE
