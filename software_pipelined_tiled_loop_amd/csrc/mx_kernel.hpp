@@ -538,33 +538,75 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
 
 // ---- few rows -----------------------------------------------------------------------------------
 
-// One token to a few dozen: bound by the weights' bytes.  The waves of a workgroup
-// share its outputs (16 FM rows, 16 FN columns) and deal out the rows' units of 256
-// entries in turn.  A wave takes its operands straight from memory to registers,
-// as the 16 x 16 x 128 instruction wants them: of lane l = 16 g + r, row r, the
-// unit's step j (128 entries) of the weights chunk 4 j + g, of MX8 activations the
-// pieces g and 4 + g of the step's 128 bytes, and the scale byte 4 j + g.  U units are under way: one is
-// fetched anew as soon as it has been multiplied.  At the end the waves' sums are
-// added in LDS, in the order of the waves.
-template <int D, int F, int FM_, int FN_, int NW_, int U_, bool GATED_>
+// One token to a few dozen: bound by the weights' bytes.  As linear_few: the waves of
+// a workgroup share its outputs (16 FM rows, 16 FNP columns) and deal out the rows'
+// units of 256 entries in turn; each has a ring of its own in LDS, which only it fills
+// and reads, so nothing in the loop waits for another wave.  (Straight from memory to
+// registers, neighbouring lanes hold different rows: four times the accesses to the
+// cache, 14 us for 16 by 4096 x 16384 in 4 bits however much was under way.)
+// The 16 x 16 x 128 instruction's lane 16 q + r takes of a unit's step (128 entries) block q of
+// row r, of MX8 activations the 16-byte pieces q and 4 + q, and the scale of block q.
+template <int D, int F, int FM_, int FN_, int NW_, int S_, bool GATED_>
 struct MxFewCfg {
-    static constexpr int Dt = D, Fmt = F, FM = FM_, FNP = FN_, NW = NW_, U = U_;
+    static constexpr int Dt = D, Fmt = F, FM = FM_, FNP = FN_, NW = NW_, S = S_;
     static constexpr bool GATED = GATED_;
     static constexpr int NP = GATED ? 2 : 1, FN = FNP * NP, NCOLP = 16 * FNP;
-    static constexpr int BM = 16 * FM, NT = 64 * NW, XCH = F == MX8 ? 2 : 1;
-    static constexpr int UA = F == MX8 ? 256 : 128, UB = 128;  // bytes of a unit's row
-    static constexpr int LDS = NW * FM * FN * 1024;
-    static_assert(LDS <= 163840, "sums");
+    static constexpr int BM = 16 * FM, NT = 64 * NW, XT = F == MX8 ? 2 : 1;  // XT: tiles of 128-byte rows of the activations
+    static constexpr int A_TILE = BM * 128, B_TILE = NCOLP * 128;
+    static constexpr int LPA = A_TILE / 1024, LPB = B_TILE / 1024;           // pieces
+    static constexpr int SPA = (BM + 31) / 32, SPB = (NCOLP + 31) / 32;      // pieces of scales, 32 rows each
+    static constexpr int AT_B = XT * A_TILE, AT_S = AT_B + NP * B_TILE;
+    static constexpr int STAGE = (AT_S + (SPA + NP * SPB) * 256 + 1023) / 1024 * 1024, RING = S * STAGE, LDS = NW * RING;
+    static constexpr int LPS = XT * LPA + NP * LPB + SPA + NP * SPB;
+    static_assert(LDS <= 163840 && S >= 2 && LPS * (S - 2) <= 63 && FM * FN * 1024 <= RING, "ring");
 };
+
+// As dma16, of four bytes a lane.
+__device__ __forceinline__ void dma4(const i32x4& rsrc, uint32_t voff, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "s"(lds_base)
+                 : "memory", "m0");
+}
+
 template <class C>
-struct MxUnit {
-    i32x4 a[C::FM][2][C::XCH], b[C::FN][2];
-    i32x2 sa[C::FM], sb[C::FN];
-};
+__device__ __forceinline__ void mx_few_multiply(f32x4 (&acc)[C::FM][C::FN], const char PGEMM_LDS* st, int lane) {
+    const int r = lane & 15, q = lane >> 4;
+    const auto scale = [&](int piece, int row, int ks) -> int {
+        return *(const uint8_t PGEMM_LDS*)(st + C::AT_S + piece * 256 + row * 8 + ks * 4 + q);
+    };
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        i32x4 b[C::FN];
+        int sb[C::FN];
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            const int p = j / C::FNP, row = 16 * (j % C::FNP) + r;
+            b[j] = *(const i32x4 PGEMM_LDS*)(st + C::AT_B + p * C::B_TILE + a_off<8>(row, ks * 4 + q));
+            sb[j] = scale(C::SPA + p * C::SPB, row, ks);
+        }
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+            const int row = 16 * i + r;
+            i32x8 x;
+            if constexpr (C::Fmt == MX8) {
+                const char PGEMM_LDS* t = st + ks * C::A_TILE;
+                x = two_chunks(*(const i32x4 PGEMM_LDS*)(t + a_off<8>(row, q)), *(const i32x4 PGEMM_LDS*)(t + a_off<8>(row, 4 + q)));
+            } else {
+                x = two_chunks(*(const i32x4 PGEMM_LDS*)(st + a_off<8>(row, ks * 4 + q)), i32x4{0, 0, 0, 0});
+            }
+            const int sx = scale(0, row, ks);
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    two_chunks(b[j], i32x4{0, 0, 0, 0}), x, acc[i][j], 4, C::Fmt == MX8 ? 0 : 4, 0, sb[j], 0, sx);
+        }
+    }
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
-    __shared__ __attribute__((aligned(16))) char smem_raw[C::LDS];
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS];
     const int per_split = g.tiles_m * g.tiles_n;
     const WgTiles w = wg_tiles_of(per_split * g.splits, (int)blockIdx.x, (int)gridDim.x);
     if (w.count == 0) return;
@@ -577,24 +619,35 @@ __global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
     const int tn = __builtin_amdgcn_readfirstlane(L / g.tiles_m), tm = __builtin_amdgcn_readfirstlane(L - tn * g.tiles_m);
     const int m0 = tm * C::BM, n0 = tn * C::NCOLP;
     const int rows_left = g.e.M - m0, cols_left = g.e.N - n0;
-    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char PGEMM_LDS* ring = (char PGEMM_LDS*)smem_raw + wave * C::RING;
+    const uint32_t lds0 = (uint32_t)(size_t)ring;
 
-    uint32_t va[C::FM], vsa[C::FM], vb[C::FNP], vsb[C::FNP];
+    // Each lane's offsets in a unit: 16 bytes of a row of codes, four of a row of scales.
+    uint32_t va[C::LPA], vb[C::LPB], vsa[C::SPA], vsb[C::SPB];
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-        const int row = 16 * i + r;
-        va[i] = row < rows_left ? (uint32_t)(row * (int)g.lda + q * 16) : OOB;
-        vsa[i] = row < rows_left ? (uint32_t)(row * (int)g.lsa) : OOB;
+    for (int p = 0; p < C::LPA; ++p) {
+        int row, kc;
+        a_inv<8>(p * 1024 + lane * 16, row, kc);
+        va[p] = row < rows_left ? (uint32_t)(row * (int)g.lda + kc * 16) : OOB;
     }
 #pragma unroll
-    for (int j = 0; j < C::FNP; ++j) {
-        const int row = 16 * j + r;
-        vb[j] = row < cols_left ? (uint32_t)(row * (int)g.ldb + q * 16) : OOB;
-        vsb[j] = row < cols_left ? (uint32_t)(row * (int)g.lsb) : OOB;
+    for (int p = 0; p < C::LPB; ++p) {
+        int row, kc;
+        a_inv<8>(p * 1024 + lane * 16, row, kc);
+        vb[p] = row < cols_left ? (uint32_t)(row * (int)g.ldb + kc * 16) : OOB;
     }
-    const char* a = (const char*)g.A + m0 * g.lda;
-    const char* sa = (const char*)g.SA + m0 * g.lsa;
+#pragma unroll
+    for (int p = 0; p < C::SPA; ++p) {
+        const int row = p * 32 + (lane >> 1);
+        vsa[p] = row < C::BM && row < rows_left ? (uint32_t)(row * (int)g.lsa + (lane & 1) * 4) : OOB;
+    }
+#pragma unroll
+    for (int p = 0; p < C::SPB; ++p) {
+        const int row = p * 32 + (lane >> 1);
+        vsb[p] = row < C::NCOLP && row < cols_left ? (uint32_t)(row * (int)g.lsb + (lane & 1) * 4) : OOB;
+    }
     f32x4 acc[C::FM][C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
@@ -603,75 +656,57 @@ __global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
 
     const int total = g.filled / 256;
     const int t0 = (int)((int64_t)total * split / g.splits), t1 = (int)((int64_t)total * (split + 1) / g.splits);
-    // The wave's stretch of them, in a row, so that a line of scales serves several; unit t, zeros past the last one.
-    const int first = t0 + (t1 - t0) * wave / C::NW, end = t0 + (t1 - t0) * (wave + 1) / C::NW;
-    const auto fetch = [&](MxUnit<C>& u, int t) {
-        const auto rsrc = [&](const char* p) {
-            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, t < end ? 0x80000000u : 0u, 0x00020000);
-        };
-        const auto get = [](const __amdgpu_buffer_rsrc_t& s, uint32_t v) {
-            return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(s, v, 0, 0));
-        };
-        const auto get2 = [](const __amdgpu_buffer_rsrc_t& s, uint32_t v) {
-            return __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(s, v, 0, 0));
+    // Loads unit t into stage st; past the last one every lane reads zeros.
+    const auto issue = [&](int t, int st) {
+        const int range = t < t1 ? (int)0x80000000u : 0;
+        const uint32_t at = lds0 + (uint32_t)(st * C::STAGE);
+        const auto rows = [&](const char* base, int64_t by) {
+            i32x4 r = make_rsrc_sgpr(base + by * t);
+            r[2] = range;
+            return r;
         };
 #pragma unroll
         for (int p = 0; p < C::NP; ++p) {
-            const __amdgpu_buffer_rsrc_t rb = rsrc((const char*)g.B[p] + n0 * g.ldb + (int64_t)t * C::UB);
-            const __amdgpu_buffer_rsrc_t rs = rsrc((const char*)g.SB[p] + n0 * g.lsb + (int64_t)t * 8);
+            const i32x4 rb = rows((const char*)g.B[p] + n0 * g.ldb, 128);
 #pragma unroll
-            for (int j = 0; j < C::FNP; ++j) {
+            for (int x = 0; x < C::LPB; ++x) dma16(rb, vb[x], at + C::AT_B + p * C::B_TILE + x * 1024u);
+            const i32x4 rs = rows((const char*)g.SB[p] + n0 * g.lsb, 8);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) u.b[p * C::FNP + j][k] = get(rb, vb[j] + 64 * k);
-                u.sb[p * C::FNP + j] = get2(rs, vsb[j]);
-            }
+            for (int x = 0; x < C::SPB; ++x) dma4(rs, vsb[x], at + C::AT_S + (C::SPA + p * C::SPB + x) * 256u);
         }
-        const __amdgpu_buffer_rsrc_t ra = rsrc(a + (int64_t)t * C::UA), rs = rsrc(sa + (int64_t)t * 8);
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
+        for (int h = 0; h < C::XT; ++h) {
+            const i32x4 ra = rows((const char*)g.A + m0 * g.lda + h * 128, C::XT * 128);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int c = 0; c < C::XCH; ++c) u.a[i][k][c] = get(ra, va[i] + 64 * (k * C::XCH + c));
-            u.sa[i] = get2(rs, vsa[i]);
+            for (int x = 0; x < C::LPA; ++x) dma16(ra, va[x], at + h * C::A_TILE + x * 1024u);
         }
+        const i32x4 rs = rows((const char*)g.SA + m0 * g.lsa, 8);
+#pragma unroll
+        for (int x = 0; x < C::SPA; ++x) dma4(rs, vsa[x], at + C::AT_S + x * 256u);
     };
-    const auto multiply = [&](const MxUnit<C>& u) {
+    int t = t0 + wave;
+    if (t < t1) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int i = 0; i < C::FM; ++i) {
-                const i32x8 x = two_chunks(u.a[i][k][0], C::XCH == 2 ? u.a[i][k][C::XCH - 1] : i32x4{0, 0, 0, 0});
-                const int sx = (int)((uint32_t)u.sa[i][k] >> (8 * q));
-#pragma unroll
-                for (int j = 0; j < C::FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        two_chunks(u.b[j][k], i32x4{0, 0, 0, 0}), x, acc[i][j], 4, C::Fmt == MX8 ? 0 : 4, 0,
-                        (int)((uint32_t)u.sb[j][k] >> (8 * q)), 0, sx);
-            }
-    };
-    if (first < end) {
-        MxUnit<C> u[C::U];
-#pragma unroll
-        for (int i = 0; i < C::U; ++i) fetch(u[i], first + i);
-        for (int t = first + C::U; t < end; t += C::U) {
-#pragma unroll
-            for (int i = 0; i < C::U; ++i) {
-                multiply(u[i]);
-                fetch(u[i], t + i);
-            }
+        for (int p = 0; p < C::S - 1; ++p) issue(t + p * C::NW, p);
+        int st = 0;
+        for (; t < t1; t += C::NW) {
+            // the oldest unit has landed, and the stage before it has been read
+            lgkm_drain();
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(C::LPS * (C::S - 2)) : "memory");
+            issue(t + (C::S - 1) * C::NW, st == 0 ? C::S - 1 : st - 1);
+            mx_few_multiply<C>(acc, ring + st * C::STAGE, lane);
+            st = st + 1 == C::S ? 0 : st + 1;
         }
-#pragma unroll
-        for (int i = 0; i < C::U; ++i) multiply(u[i]);
     }
+    __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing LDS
+    asm volatile("" ::: "memory");
 
-    // The waves' sums.
-    char PGEMM_LDS* own = (char PGEMM_LDS*)smem_raw + wave * (C::FM * C::FN * 1024);
+    // The waves' sums, each in its own ring.
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) *(f32x4 PGEMM_LDS*)(own + ((i * C::FN + j) * 64 + lane) * 16) = acc[i][j];
-    __syncthreads();
+        for (int j = 0; j < C::FN; ++j) *(f32x4 PGEMM_LDS*)(ring + ((i * C::FN + j) * 64 + lane) * 16) = acc[i][j];
+    lgkm_barrier();
     constexpr int GPR = C::NCOLP / 8, GROUPS = C::BM * GPR;  // groups of eight columns
     for (int x = (int)threadIdx.x; x < GROUPS; x += C::NT) {
         const int row = x / GPR, c8 = x % GPR;
@@ -684,8 +719,7 @@ __global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
             const char PGEMM_LDS* at = (const char PGEMM_LDS*)smem_raw + (block * 64 + (row & 15) + 32 * (c8 & 1)) * 16;
 #pragma unroll
             for (int v = 0; v < C::NW; ++v)
-                s[p] += join8(*(const f32x4 PGEMM_LDS*)(at + v * (C::FM * C::FN * 1024)),
-                              *(const f32x4 PGEMM_LDS*)(at + v * (C::FM * C::FN * 1024) + 256));
+                s[p] += join8(*(const f32x4 PGEMM_LDS*)(at + v * C::RING), *(const f32x4 PGEMM_LDS*)(at + v * C::RING + 256));
         }
         if (g.part) {
             float* o = g.part + ((int64_t)split * C::NP * g.e.M + m0 + row) * g.np8 + n0 + 8 * c8;

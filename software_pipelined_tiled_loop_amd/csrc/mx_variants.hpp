@@ -4,7 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "linear_variants.hpp"
-#include "mx_kernel.hpp"
+#include "mx_large.hpp"
 #include "norm_kernel.hpp"
 
 namespace pgemm {
@@ -81,6 +81,10 @@ hipError_t launch_mx_tile(const MxArgs& a, int grid, hipStream_t s) {
     return lin_launch<MxArgs>(&mx_tile<C>, a, dim3(grid), C::NT, s);
 }
 template <class C>
+hipError_t launch_mx_large(const MxArgs& a, int grid, hipStream_t s) {
+    return lin_launch<MxArgs>(&mx_large<C>, a, dim3(grid), C::NT, s);
+}
+template <class C>
 hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
     return lin_launch<MxArgs>(&mx_few<C>, a, dim3(grid), C::NT, s);
 }
@@ -101,13 +105,20 @@ hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
             163840 / MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN)::LDS,                                        \
             &launch_mx_tile<MX_TILE_CFG(D, F, GATED, BM, BN, S, WGM, WGN)>                                      \
     }
-#define MX_FEW(D, F, GATED, FM, FN, NW, U)                                                                      \
+#define MX_LARGE(D, F, GATED)                                                                                   \
     MxVariant {                                                                                                 \
-        F, GATED, 16 * FM, 16 * FN, 256, 64 * NW, NW, 2, &launch_mx_few<MxFewCfg<D, F, FM, FN, NW, U, GATED != 0>> \
+        F, GATED, 256, GATED ? 128 : 256, F == MX8 ? 128 : 256, 256, 0, 1, &launch_mx_large<MxLargeCfg<D, F, GATED != 0>> \
+    }
+#define MX_FEW_CFG(D, F, GATED, FM, FN, NW, S) MxFewCfg<D, F, FM, FN, NW, S, GATED != 0>
+#define MX_FEW(D, F, GATED, FM, FN, NW, S)                                                                      \
+    MxVariant {                                                                                                 \
+        F, GATED, 16 * FM, 16 * FN, 256, 64 * NW, NW, 163840 / MX_FEW_CFG(D, F, GATED, FM, FN, NW, S)::LDS,     \
+            &launch_mx_few<MX_FEW_CFG(D, F, GATED, FM, FN, NW, S)>                                              \
     }
 #define MX_CLASS(D, F, GATED, DEEP)                                                                             \
-    MX_TILE(D, F, GATED, 256, 256, (F == MX8 ? 3 : 4), 2, 2), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2),        \
-        MX_FEW(D, F, GATED, 1, 1, 8, 2), MX_FEW(D, F, GATED, 2, 1, 8, 2), MX_FEW(D, F, GATED, 4, 1, 8, 2)
+    MX_LARGE(D, F, GATED), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2), MX_FEW(D, F, GATED, 1, 1, 4, 3),         \
+        MX_FEW(D, F, GATED, 1, 2, 4, 3), MX_FEW(D, F, GATED, 1, 4, 2, 3), MX_FEW(D, F, GATED, 2, 1, 4, 3),      \
+        MX_FEW(D, F, GATED, 2, 2, 4, 2), MX_FEW(D, F, GATED, 3, 2, 2, 3)
 #define MX_VARIANTS(D) MX_CLASS(D, MX8, 0, 3), MX_CLASS(D, MX8, 1, 3), MX_CLASS(D, MX4, 0, 4), MX_CLASS(D, MX4, 1, 4)
 #define MX_KERNELS(D, norms, grads, table)                                                                      \
     MxKernels {                                                                                                 \
