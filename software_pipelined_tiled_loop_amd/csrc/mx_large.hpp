@@ -41,24 +41,31 @@ struct MxLargeCfg {
     static constexpr int AT_B = 2 * UNIT, AT_S = 4 * UNIT;
     static constexpr int SB = 32, G = SB * 32 / BK;       // bytes of a row in a group of scales; its periods
     static constexpr int S_STAGE = 512 * SB, TOTAL = AT_S + 2 * S_STAGE;
-    static constexpr int LDS = AT_S;                      // what the epilogue uses
     static constexpr int PB = 8 / TURNS;                  // the wave's pieces of the weights a period
     static constexpr int PIECES = 8 + PB;                 // of codes a period
     static constexpr int WAIT_X = PIECES, WAIT_Y = PIECES / 2 + 4;
     static_assert(TOTAL == 163840 && FN == 8, "all of a CU's LDS");
 };
 
-// Codes of a unit: chunk kc of a row.  MX4 fragments read chunks 2 q + ks (lanes that
-// are served together differ by two chunks), MX8 ones q and 4 + q.
-template <int F>
-PGEMM_HD constexpr int mx_swz16(int line) { return F == MX8 ? (line & 7) << 1 : (line & 1) | (line & 6) << 1; }
-template <int F>
-PGEMM_HD constexpr int mx_off16(int row, int kc) {
-    return (row >> 1 << 8) + ((((row & 1) * 8 + kc) ^ mx_swz16<F>(row >> 1)) << 4);
+// Of two blocks' 32 weights' rows the even block's are 0 .. 3, 8 .. 11, 16 .., the odd one's four further on: a lane's
+// results, four rows of a block, then join to eight columns of the output.
+PGEMM_HD constexpr int mx_row_b(int r) { return 8 * (r >> 2) + (r & 3); }
+
+// Codes of a unit: chunk kc of a row.  The LDS serves sixteen lanes at a time, eight rows of one parity at two of the
+// chunks: MX4 fragments read chunks 2 q + ks, MX8 ones q and 4 + q.  The eight rows' 256-byte lines, four
+// bits of them for the weights' rows as they are dealt, are told apart by three bits.
+template <int F, bool B>
+PGEMM_HD constexpr int mx_swz16(int line) {
+    const int l = B ? (line & 1) | (line >> 2 & 3) << 1 : line & 7;
+    return F == MX8 ? l << 1 : (l & 1) | (l & 6) << 1;
 }
-template <int F>
+template <int F, bool B>
+PGEMM_HD constexpr int mx_off16(int row, int kc) {
+    return (row >> 1 << 8) + ((((row & 1) * 8 + kc) ^ mx_swz16<F, B>(row >> 1)) << 4);
+}
+template <int F, bool B>
 PGEMM_HD void mx_inv16(int off, int& row, int& kc) {
-    const int line = off >> 8, u = ((off >> 4) & 15) ^ mx_swz16<F>(line);
+    const int line = off >> 8, u = ((off >> 4) & 15) ^ mx_swz16<F, B>(line);
     row = 2 * line + (u >> 3);
     kc = u & 7;
 }
@@ -88,114 +95,121 @@ __device__ __forceinline__ void mx_mfma16(f32x4& acc, const i32x4 (&x)[2], const
 
 // What a period's loads and reads go by.
 struct MxLargeAt {
-    const char PGEMM_LDS* a;        // units of the period's rows, and of the next period's
-    const char PGEMM_LDS* a_next;
-    const char PGEMM_LDS* b_next;   // the next period's weights
-    const char PGEMM_LDS* s;        // scales of the period and of the next one, at their places in the group
-    const char PGEMM_LDS* s_next;
+    uint32_t a[2], a_next[2];       // LDS: each lane's first row of the period's unit, and of the next period's (by step or piece)
+    uint32_t b_next[2];             // of the next period's weights
+    uint32_t sa, sa_next, sb_next;  // of their scales
     uint32_t la1, la2, lb;          // LDS places of the wave's pieces: next period's rows, the one after, and its weights
     uint32_t k1, k2, kb;            // bytes in the rows
 };
 
+template <class T>
+__device__ __forceinline__ T mx_lds(uint32_t at) { return *(const T PGEMM_LDS*)at; }
+
 template <class C>
 struct MxLarge {
-    i32x4 ra, rb;
+    i32x4 ra, rb;                   // rows from kBack bytes before them on (see piece)
     uint32_t va[8], vb[8];
-    int lane, wm0, wn0;
     MxLargeState<C> f;
+    static constexpr uint32_t kBack = 4096;
 
-    // Fragment reads.  Lane 16 q + r: row r.
+    // Fragment reads: row block I / 2 of a block, step or piece I % 2.
     template <int BUF, int I>
-    __device__ __forceinline__ void read_a(const char PGEMM_LDS* unit, int block) {  // I: row block * 2 + step or piece
-        const int r = lane & 15, q = lane >> 4, row = wm0 + 32 * block + 16 * (I / 2) + r;
-        f.a[BUF][I / 2][I % 2] = *(const i32x4 PGEMM_LDS*)(unit + mx_off16<C::Fmt>(row, C::Fmt == MX8 ? 4 * (I % 2) + q : 2 * q + I % 2));
+    __device__ __forceinline__ void read_a(const uint32_t (&unit)[2], int block) {
+        f.a[BUF][I / 2][I % 2] = mx_lds<i32x4>(unit[I % 2] + (32 * block + 16 * (I / 2)) * 128);
     }
-    __device__ __forceinline__ int scale(const char PGEMM_LDS* s, int row) const {
-        const int q = lane >> 4;
-        if constexpr (C::Fmt == MX8) return *(const uint8_t PGEMM_LDS*)(s + row * C::SB + q);
-        else return *(const unsigned short PGEMM_LDS*)(s + row * C::SB + 2 * q);
+    static __device__ __forceinline__ int scale(uint32_t at) {
+        if constexpr (C::Fmt == MX8) return mx_lds<uint8_t>(at);
+        else return mx_lds<unsigned short>(at);
     }
     template <int BUF, int I>
-    __device__ __forceinline__ void read_sa(const char PGEMM_LDS* s, int block) {
-        f.sa[BUF][I] = scale(s, wm0 + 32 * block + 16 * I + (lane & 15));
-    }
+    __device__ __forceinline__ void read_sa(uint32_t at, int block) { f.sa[BUF][I] = scale(at + (32 * block + 16 * I) * C::SB); }
+    // Row of the weights' block J that lane 0 of a half row reads; lane r is mx_row_b(r) rows on.
     template <int J>
-    __device__ __forceinline__ int row_b() const { return J / C::FNP * C::BNP + wn0 + 16 * (J % C::FNP) + (lane & 15); }
-    // TURN: which half of the unit's line (MX8)
-    template <int J, int KSTEP, int TURN>
-    __device__ __forceinline__ void read_b(const char PGEMM_LDS* unit) {
-        const int q = lane >> 4;
-        f.b[J][KSTEP] = *(const i32x4 PGEMM_LDS*)(unit + mx_off16<C::Fmt>(row_b<J>(), C::Fmt == MX8 ? 4 * TURN + q : 2 * q + KSTEP));
-    }
+    static constexpr int row_b = J / C::FNP * C::BNP + 32 * (J % C::FNP / 2) + 4 * (J % 2);
+    // WHICH: the step, or the half of the unit's line (MX8)
+    template <int J, int KSTEP, int WHICH>
+    __device__ __forceinline__ void read_b(const uint32_t (&unit)[2]) { f.b[J][KSTEP] = mx_lds<i32x4>(unit[WHICH] + row_b<J> * 128); }
     template <int J>
-    __device__ __forceinline__ void read_sb(const char PGEMM_LDS* s) { f.sb[J] = scale(s, 256 + row_b<J>()); }
+    __device__ __forceinline__ void read_sb(uint32_t at) { f.sb[J] = scale(at + row_b<J> * C::SB); }
 
-    // Pieces: of rows, X of the 2 of a block; of the weights.  M0 first, the load an instruction later.
-    template <int BLOCK, int X>
-    __device__ __forceinline__ void place_a(uint32_t at) const {
-        asm volatile("s_add_u32 m0, %0, %1" : : "s"(at), "n"(BLOCK * 4096 + X * 1024) : "m0", "scc");
+    // Pieces of 1 KiB: LDS at M0 plus the instruction's offset, which the memory's address takes too (so va and vb
+    // are that much less, and the rows' address kBack bytes, which they have more).
+    // M0 is set for all pieces in a row of 4 KiB, an instruction before the first load.
+    template <int OFF>
+    static __device__ __forceinline__ void load(uint32_t v, const i32x4& r, uint32_t k) {
+        asm volatile("buffer_load_dwordx4 %0, %1, %2 offen offset:%3 lds" : : "v"(v), "s"(r), "s"(k), "n"(OFF) : "memory");
     }
-    template <int BLOCK, int X>
-    __device__ __forceinline__ void load_a(uint32_t k) const {
-        asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" : : "v"(va[2 * BLOCK + X]), "s"(ra), "s"(k) : "memory");
+    template <int ADD>
+    static __device__ __forceinline__ void place(uint32_t at) {
+        asm volatile("s_add_u32 m0, %0, %1" : : "s"(at), "n"(ADD) : "m0", "scc");
     }
-    template <int Q>
-    __device__ __forceinline__ void place_b(uint32_t at) const {
-        asm volatile("s_add_u32 m0, %0, %1" : : "s"(at), "n"(Q * 1024) : "m0", "scc");
-    }
-    template <int Q>
-    __device__ __forceinline__ void load_b(uint32_t k) const {
-        asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" : : "v"(vb[Q]), "s"(rb), "s"(k) : "memory");
-    }
-
+    static constexpr int H = C::PB / 2;  // pieces of weights in a row
     // Piece P of the PIECES of a period, in their order (TURN: the period's place among those of a unit of weights).
     //   0, 1 rows of block 3 (next period)   2, 3 of block 0 (the one after)   weights, first half
     //   weights, second half                 rows of blocks 1 and 2 (the one after)
+    static constexpr bool placed(int p) { return p < 4 || p >= 4 + C::PB ? p % 2 == 0 : (p - 4) % H == 0; }
     template <int P, int TURN, bool PLACE>
     __device__ __forceinline__ void piece(const MxLargeAt& at) const {
-        constexpr int B0 = C::TURNS == 2 && TURN == 0 ? 4 : 0;
-        if constexpr (P < 2) {
-            if constexpr (PLACE) place_a<3, P>(at.la1);
-            else load_a<3, P>(at.k1);
-        } else if constexpr (P < 4) {
-            if constexpr (PLACE) place_a<0, P - 2>(at.la2);
-            else load_a<0, P - 2>(at.k2);
-        } else if constexpr (P < 4 + C::PB) {
-            if constexpr (PLACE) place_b<B0 + P - 4>(at.lb);
-            else load_b<B0 + P - 4>(at.kb);
+        if constexpr (P < 4 || P >= 4 + C::PB) {
+            constexpr int BLOCK = P < 2 ? 3 : P < 4 ? 0 : 1 + (P - 4 - C::PB) / 2, X = P % 2;
+            if constexpr (PLACE) place<BLOCK * 4096>(P < 2 ? at.la1 : at.la2);
+            else load<X * 1024>(va[2 * BLOCK + X], ra, P < 2 ? at.k1 : at.k2);
         } else {
-            constexpr int X = P - 4 - C::PB;
-            if constexpr (PLACE) place_a<1 + X / 2, X % 2>(at.la2);
-            else load_a<1 + X / 2, X % 2>(at.k2);
+            constexpr int Q = (C::TURNS == 2 && TURN == 0 ? 4 : 0) + P - 4;
+            if constexpr (PLACE) place<Q * 1024>(at.lb);
+            else load<Q % H * 1024>(vb[Q], rb, at.kb);
+        }
+    }
+    // Steps of pieces FIRST to END - 1: each group's M0, then its loads.
+    static constexpr int steps(int first, int end) {
+        int n = 0;
+        for (int p = first; p < end; ++p) n += placed(p) ? 2 : 1;
+        return n;
+    }
+    // The piece of step S, twice, plus one where the step sets M0.
+    static constexpr int step_of(int first, int s) {
+        int p = first;
+        while (true) {
+            if (placed(p)) {
+                if (s == 0) return 2 * p + 1;
+                --s;
+            }
+            if (s == 0) return 2 * p;
+            --s;
+            ++p;
         }
     }
     template <int FIRST, int END, int TURN>
     __device__ __forceinline__ void pieces(const MxLargeAt& at) const {
         if constexpr (FIRST < END) {
-            piece<FIRST, TURN, true>(at);
-            asm volatile("s_nop 0");
+            if constexpr (placed(FIRST)) {
+                piece<FIRST, TURN, true>(at);
+                asm volatile("s_nop 0");
+            }
             piece<FIRST, TURN, false>(at);
             pieces<FIRST + 1, END, TURN>(at);
         }
     }
-
-    // All of a unit of weights; rows of the blocks from FIRST on.
+    // In the prologue: all of a unit of weights; rows of the blocks from FIRST on.
     template <int Q>
     __device__ __forceinline__ void all_b(uint32_t at, uint32_t k) const {
         if constexpr (Q < 8) {
-            place_b<Q>(at);
-            asm volatile("s_nop 0");
-            load_b<Q>(k);
+            if constexpr (Q % H == 0) {
+                place<Q * 1024>(at);
+                asm volatile("s_nop 0");
+            }
+            load<Q % H * 1024>(vb[Q], rb, k);
             all_b<Q + 1>(at, k);
         }
     }
-    template <int FIRST, int END, int X = 0>
+    template <int FIRST, int END>
     __device__ __forceinline__ void rows_a(uint32_t at, uint32_t k) const {
         if constexpr (FIRST < END) {
-            place_a<FIRST, X>(at);
+            place<FIRST * 4096>(at);
             asm volatile("s_nop 0");
-            load_a<FIRST, X>(k);
-            rows_a<FIRST + X, END, (X + 1) % 2>(at, k);
+            load<0>(va[2 * FIRST], ra, k);
+            load<1024>(va[2 * FIRST + 1], ra, k);
+            rows_a<FIRST + 1, END>(at, k);
         }
     }
 
@@ -204,23 +218,30 @@ struct MxLarge {
     // period's weights into the registers that have become free.
     template <int BLOCK, int TURN>
     struct Block {
-        static constexpr int NM = 2 * C::KS * C::FN, NPC = C::PIECES / 4, P0 = BLOCK * NPC;
-        static constexpr int READS = 6, E = READS + 2 * NPC, BUF = BLOCK & 1, NXT = BUF ^ 1;
+        static constexpr int NM = 2 * C::KS * C::FN, P0 = BLOCK * (C::PIECES / 4);
+        static constexpr int READS = 6, STEPS = steps(P0, P0 + C::PIECES / 4), E = READS + STEPS;
+        static constexpr int PAIRS = READS < STEPS ? READS : STEPS, BUF = BLOCK & 1, NXT = BUF ^ 1;
         template <int I>
         static __device__ __forceinline__ void read(MxLarge& m, const MxLargeAt& at) {
-            const char PGEMM_LDS* unit = BLOCK == 3 ? at.a_next : at.a;
-            if constexpr (I < 4) m.template read_a<NXT, I>(unit, (BLOCK + 1) & 3);
-            else m.template read_sa<NXT, I - 4>(BLOCK == 3 ? at.s_next : at.s, (BLOCK + 1) & 3);
+            constexpr int R = (I + 4) % READS;  // scales first: the next block's first MFMA waits for them
+            if constexpr (R < 4) m.template read_a<NXT, R>(BLOCK == 3 ? at.a_next : at.a, (BLOCK + 1) & 3);
+            else m.template read_sa<NXT, R - 4>(BLOCK == 3 ? at.sa_next : at.sa, (BLOCK + 1) & 3);
         }
-        // scales first: the next block's first MFMA waits for them
+        template <int S>
+        static __device__ __forceinline__ void step(const MxLarge& m, const MxLargeAt& at) {
+            constexpr int X = step_of(P0, S);
+            m.template piece<X / 2, TURN, X % 2 != 0>(at);
+        }
+        // (the steps alone, where there are more of them than reads, stand behind different MFMAs)
         template <int J>
         static __device__ __forceinline__ void item(MxLarge& m, const MxLargeAt& at) {
-            if constexpr (J < 2 * READS && J < 4 * NPC) {
-                if constexpr (J % 2 == 0) read<(J / 2 + 4) % READS>(m, at);
-                else m.template piece<P0 + J / 4, TURN, (J / 2) % 2 == 0>(at);
+            if constexpr (J < 2 * PAIRS) {
+                if constexpr (J % 2 == 0) read<J / 2>(m, at);
+                else step<J / 2>(m, at);
+            } else if constexpr (READS > PAIRS) {
+                read<J - PAIRS>(m, at);
             } else {
-                constexpr int X = J - READS;  // no reads left: pieces alone, an MFMA between M0 and the load
-                if constexpr (J < E) m.template piece<P0 + X / 2, TURN, X % 2 == 0>(at);
+                step<J - PAIRS>(m, at);
             }
         }
         template <int J, int END>
@@ -237,8 +258,8 @@ struct MxLarge {
                 mx_mfma16<C, KSTEP>(acc[2 * BLOCK + I][J], m.f.a[BUF][I], m.f.b[J][KSTEP], m.f.sa[BUF][I], m.f.sb[J]);
                 if constexpr (BLOCK == 3) {
                     if constexpr (I == 1) {
-                        m.template read_b<J, KSTEP, (TURN + 1) % C::TURNS>(at.b_next);
-                        if constexpr (KSTEP == C::KS - 1) m.template read_sb<J>(at.s_next);
+                        m.template read_b<J, KSTEP, C::TURNS == 2 ? 1 - TURN : KSTEP>(at.b_next);
+                        if constexpr (KSTEP == C::KS - 1) m.template read_sb<J>(at.sb_next);
                     } else {
                         items<T * E / (NM / 2), (T + 1) * E / (NM / 2)>(m, at);
                     }
@@ -251,12 +272,177 @@ struct MxLarge {
         }
     };
     template <int J = 0>
-    __device__ __forceinline__ void first_b(const char PGEMM_LDS* unit, const char PGEMM_LDS* s) {
+    __device__ __forceinline__ void first_b(const uint32_t (&unit)[2], uint32_t scales) {
         if constexpr (J < C::FN) {
             read_b<J, 0, 0>(unit);
-            if constexpr (C::KS == 2) read_b<J, C::KS - 1, 0>(unit);
-            read_sb<J>(s);
-            first_b<J + 1>(unit, s);
+            if constexpr (C::KS == 2) read_b<J, C::KS - 1, 1>(unit);
+            read_sb<J>(scales);
+            first_b<J + 1>(unit, scales);
+        }
+    }
+};
+
+// The epilogue.  The weights' rows are dealt to the blocks' rows such that a lane has of
+// each pair of blocks eight columns side by side (mx_row_b), 16 bytes of the output.  One
+// wave a SIMD has nothing to hide its instructions behind, so they are few: the output's
+// range ends with its last row, which drops the stores beyond, and a lane's offsets move
+// by rows alone.  (With Epi::put, a general one, it took 6 us a tile besides the stores;
+// through LDS, as lin_epilogue goes, 4.5.)  The accumulators have to be named by constants: each
+// iteration of the short loop picks its own of them.  A group that the edge of
+// the output cuts goes element by element, from LDS, where a loop can index it.
+template <class C>
+struct MxFinish {
+    typedef typename Elem<C::Dt>::type T;
+    static constexpr uint32_t TS = sizeof(T);
+    static constexpr int PAIRS = C::FNP / 2, U = C::GATED ? 2 : 4, HALVES = C::FM / U;  // U groups at once: what the registers hold
+    struct Raw {
+        i32x4 a[TS / 2];
+    };
+    const EpiArgs& e;
+    __amdgpu_buffer_rsrc_t y, r;
+    uint32_t oy, orr;      // bytes of the lane's first group
+    int n0, col, cols, valid_rows;
+    f32x8 b0[PAIRS], b1[C::GATED ? PAIRS : 1];
+    Raw next[U];
+
+    __device__ __forceinline__ MxFinish(const EpiArgs& a, int m0, int n0_, int row, int col_) : e(a), n0(n0_), col(col_) {
+        const int rows = min(e.M - m0, C::BM);
+        cols = e.N - n0;
+        valid_rows = rows - row;
+        const auto whole = [&](const void* p, int64_t ld) {
+            const uint32_t range = (uint32_t)((rows - 1) * (int)ld + min(cols, C::BNP)) * TS;
+            return __builtin_amdgcn_make_buffer_rsrc(p ? (char*)const_cast<void*>(p) + (m0 * ld + n0) * (int64_t)TS : nullptr, (short)0,
+                                                     range, 0x00020000);
+        };
+        y = whole(e.Y[0], e.ldy);
+        r = whole(e.R, e.ldr);
+        oy = (uint32_t)(row * (int)e.ldy + col) * TS;
+        orr = (uint32_t)(row * (int)e.ldr + col) * TS;
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+            b0[p] = bias(0, p);
+            if constexpr (C::GATED) b1[p] = bias(1, p);
+        }
+    }
+    __device__ __forceinline__ bool cut(int p) const { return cols - col - 32 * p < 8; }
+    __device__ __forceinline__ f32x8 bias(int which, int p) const {
+        if (!e.bias[which] || cut(p)) return zero8();
+        return load8<T>(make_rsrc((const T*)e.bias[which] + n0), (uint32_t)(col + 32 * p) * TS);
+    }
+    __device__ __forceinline__ void fetch(int it) {
+        if (!e.R) return;
+        const int p = it / HALVES;
+        const uint32_t o = (orr + (uint32_t)(16 * U * (it % HALVES) * (int)e.ldr + 32 * p) * TS) | (cut(p) ? OOB : 0u);
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+#pragma unroll
+            for (int d = 0; d < (int)TS / 2; ++d)
+                next[q].a[d] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                             r, o + (uint32_t)(16 * q * (int)e.ldr) * TS + 16 * d, 0, 0));
+    }
+    static __device__ __forceinline__ f32x8 value(const Raw& x) {
+        if constexpr (TS == 4) {
+            return join8(__builtin_bit_cast(f32x4, x.a[0]), __builtin_bit_cast(f32x4, x.a[1]));
+        } else {
+            const typename Vec8<T>::type h = __builtin_bit_cast(typename Vec8<T>::type, x.a[0]);
+            f32x8 v;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
+            return v;
+        }
+    }
+    // Element x of the group of v (w) `by` rows on in pair p, where the output's edge cuts it.
+    template <int KIND>
+    __device__ __forceinline__ void one(int by, int p, int x, float v, float w) const {
+        const int c = col + 32 * p + x;
+        if (e.bias[0]) v += (float)((const T*)e.bias[0])[n0 + c];
+        v = act1<KIND>(e.act, v);
+        if constexpr (C::GATED) {
+            if (e.bias[1]) w += (float)((const T*)e.bias[1])[n0 + c];
+            v *= w;
+        }
+        if (e.R) v += load1<T>(r, orr + (uint32_t)(by * (int)e.ldr + 32 * p + x) * TS);
+        store1<T>(y, oy + (uint32_t)(by * (int)e.ldy + 32 * p + x) * TS, v);
+    }
+    static __device__ __forceinline__ f32x8 pair(const f32x4& a, const f32x4& b) {
+        // read where they are used: the compiler copies all 256 to VGPRs at once, and spills
+        const auto from = [](float x) {
+            float v;
+            asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(x));
+            return v;
+        };
+        f32x8 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = from(a[i]);
+            v[4 + i] = from(b[i]);
+        }
+        return v;
+    }
+    template <int KIND>
+    __device__ __forceinline__ void run(f32x4 (&acc)[C::FM][C::FN], char PGEMM_LDS* own) {
+        fetch(0);
+#pragma unroll 1
+        for (int it = 0; it < PAIRS * HALVES; ++it) {
+            f32x8 v[U], w[C::GATED ? U : 1], c0, c1;
+#pragma unroll
+            for (int x = 0; x < PAIRS * HALVES; ++x) {
+                if (x != it) continue;
+                const int xp = x / HALVES, xh = x % HALVES;
+#pragma unroll
+                for (int q = 0; q < U; ++q) {
+                    v[q] = pair(acc[U * xh + q][2 * xp], acc[U * xh + q][2 * xp + 1]);
+                    if constexpr (C::GATED) w[q] = pair(acc[U * xh + q][C::FNP + 2 * xp], acc[U * xh + q][C::FNP + 2 * xp + 1]);
+                }
+                c0 = b0[xp];
+                c1 = b1[C::GATED ? xp : 0];
+            }
+            const int p = it / HALVES, by = 16 * U * (it % HALVES);
+            if (cols_cut(e.N)) {
+#pragma unroll
+                for (int q = 0; q < U; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        *(f32x4 PGEMM_LDS*)(own + (2 * q + h) * 4096) =
+                            f32x4{v[q][4 * h], v[q][4 * h + 1], v[q][4 * h + 2], v[q][4 * h + 3]};
+                        if constexpr (C::GATED)
+                            *(f32x4 PGEMM_LDS*)(own + (2 * U + 2 * q + h) * 4096) =
+                                f32x4{w[q][4 * h], w[q][4 * h + 1], w[q][4 * h + 2], w[q][4 * h + 3]};
+                    }
+            }
+            if (e.bias[0]) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) v[q] += c0;
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) v[q] = act8<KIND>(e.act, v[q]);
+            if constexpr (C::GATED) {
+                if (e.bias[1]) {
+#pragma unroll
+                    for (int q = 0; q < U; ++q) w[q] += c1;
+                }
+#pragma unroll
+                for (int q = 0; q < U; ++q) v[q] *= w[q];
+            }
+            if (e.R) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) v[q] += value(next[q]);
+                if (it + 1 < PAIRS * HALVES) fetch(it + 1);
+            }
+            const uint32_t o = (oy + (uint32_t)(by * (int)e.ldy + 32 * p) * TS) | (cut(p) ? OOB : 0u);
+#pragma unroll
+            for (int q = 0; q < U; ++q) store8<T>(y, o + (uint32_t)(16 * q * (int)e.ldy) * TS, v[q]);
+            if (!cols_cut(e.N)) continue;
+            const int n = cols - col - 32 * p;
+#pragma unroll 1
+            for (int q = 0; q < U; ++q) {
+#pragma unroll 1
+                for (int x = 0; x < (n < 8 && by + 16 * q < valid_rows ? n : 0); ++x) {
+                    const char PGEMM_LDS* at = own + (2 * q + (x >> 2)) * 4096 + 4 * (x & 3);
+                    one<KIND>(by + 16 * q, p, x, *(const float PGEMM_LDS*)at,
+                              C::GATED ? *(const float PGEMM_LDS*)(at + 2 * U * 4096) : 0.0f);
+                }
+            }
         }
     }
 };
@@ -297,26 +483,23 @@ __global__ void __launch_bounds__(C::NT, 1) mx_large(MxArgs g) {
     const int t0 = g0 * C::G, t1 = min(g1 * C::G, total);
     if (t1 > t0) {
         MxLarge<C> m;
-        m.lane = lane;
-        m.wm0 = wm0;
-        m.wn0 = wn0;
         // With the whole contraction in one go the XCDs begin at different places of it (see linear_kernel).
         const int x = blockIdx.x & 7;
         const int begin = g.splits == 1 ? (int)((int64_t)groups * (((x & 6) + 4 * (x & 1)) & 7) >> 3) : g0;
         const int first = begin * C::G;
         const int panel = C::NP == 2 ? wave / 2 : 0;
-        m.ra = make_rsrc_sgpr((const char*)g.A + m0 * g.lda);
-        m.rb = make_rsrc_sgpr((const char*)(panel ? g.B[1] : g.B[0]) + n0 * g.ldb);
+        m.ra = make_rsrc_sgpr((const char*)g.A + m0 * g.lda - MxLarge<C>::kBack);
+        m.rb = make_rsrc_sgpr((const char*)(panel ? g.B[1] : g.B[0]) + n0 * g.ldb - MxLarge<C>::kBack);
         // Rows: of block b the sixteen from a_row + 32 b on; weights: 64 rows from 64 * wave on.
         const int a_row = (wave >> 1) * 128 + (wave & 1) * 16;
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
             int row, kc;
-            mx_inv16<C::Fmt>((a_row + 32 * (p / 2) + 8 * (p % 2)) * 128 + lane * 16, row, kc);
-            m.va[p] = row < rows_left ? (uint32_t)(row * (int)g.lda + kc * 16) : OOB;
-            mx_inv16<C::Fmt>((64 * wave + 8 * p) * 128 + lane * 16, row, kc);
+            mx_inv16<C::Fmt, false>((a_row + 32 * (p / 2) + 8 * (p % 2)) * 128 + lane * 16, row, kc);
+            m.va[p] = row < rows_left ? (uint32_t)(row * (int)g.lda + kc * 16) + MxLarge<C>::kBack - p % 2 * 1024 : OOB;
+            mx_inv16<C::Fmt, true>((64 * wave + 8 * p) * 128 + lane * 16, row, kc);
             row -= panel * C::BNP;
-            m.vb[p] = row < cols_left ? (uint32_t)(row * (int)g.ldb + kc * 16) : OOB;
+            m.vb[p] = row < cols_left ? (uint32_t)(row * (int)g.ldb + kc * 16) + MxLarge<C>::kBack - p % MxLarge<C>::H * 1024 : OOB;
         }
         // Scales: 128 rows a wave, of the activations or of a panel of the weights, two lanes a row.
         const int s_row = wave * 128;
@@ -328,7 +511,8 @@ __global__ void __launch_bounds__(C::NT, 1) mx_large(MxArgs g) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int row = s_first + 32 * q + (lane >> 1);
-            vs[q] = row < s_rows ? (uint32_t)(row * (int)ls + (lane & 1) * 16) : OOB;
+            // (a row's halves swapped in every second eight rows: reads of sixteen rows meet no bank twice)
+            vs[q] = row < s_rows ? (uint32_t)(row * (int)ls + (((lane & 1) ^ (lane >> 4 & 1)) << 4)) : OOB;
         }
         const char* s_base = (of_a ? (const char*)g.SA + m0 * ls : (const char*)(s_panel ? g.SB[1] : g.SB[0]) + n0 * ls);
         const int s_end = (s_rows - 1) * (int)ls + g.filled / 32;  // bytes from there to the end of the last row
@@ -369,47 +553,55 @@ __global__ void __launch_bounds__(C::NT, 1) mx_large(MxArgs g) {
             m.template pieces<0, C::PIECES, C::TURNS - 1>(at);
         }
         wait_barrier<C::WAIT_X>();
-        m.template read_a<0, 0>(smem, 0);
-        m.template read_a<0, 1>(smem, 0);
-        m.template read_a<0, 2>(smem, 0);
-        m.template read_a<0, 3>(smem, 0);
-        m.template read_sa<0, 0>(smem + C::AT_S, 0);
-        m.template read_sa<0, 1>(smem + C::AT_S, 0);
-        m.first_b(smem + C::AT_B, smem + C::AT_S);
+        // Each lane's first row in a unit, at the chunk of each step (piece, half of the line); its first scales.
+        const int r = lane & 15, q = lane >> 4;
+        uint32_t oa[2], ob[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            oa[i] = lds0 + mx_off16<C::Fmt, false>(wm0 + r, C::Fmt == MX8 ? 4 * i + q : 2 * q + i);
+            ob[i] = lds0 + C::AT_B + mx_off16<C::Fmt, true>(wn0 + mx_row_b(r), C::Fmt == MX8 ? 4 * i + q : 2 * q + i);
+        }
+        const uint32_t swap_a = (r >> 3) << 4, swap_b = (r >> 2 & 1) << 4, of_q = C::Fmt == MX8 ? q : 2 * q;
+        const uint32_t osa = lds0 + (wm0 + r) * C::SB + of_q, osb = lds0 + (256 + wn0 + mx_row_b(r)) * C::SB + of_q;
+        const auto scales_a = [&](uint32_t stage, uint32_t place) { return osa + stage + (place ^ swap_a); };
+        const auto scales_b = [&](uint32_t stage, uint32_t place) { return osb + stage + (place ^ swap_b); };
+        m.template read_a<0, 0>(oa, 0);
+        m.template read_a<0, 1>(oa, 0);
+        m.template read_a<0, 2>(oa, 0);
+        m.template read_a<0, 3>(oa, 0);
+        m.template read_sa<0, 0>(scales_a(C::AT_S, 0), 0);
+        m.template read_sa<0, 1>(scales_a(C::AT_S, 0), 0);
+        m.first_b(ob, scales_b(C::AT_S, 0));
 
-        uint32_t ua = 0, ub = 0;     // unit of the period's rows, of its weights
-        uint32_t s_at = C::AT_S;     // its scales
-        int place = 0, row_left = total - first, n = t1 - t0;
-        uint32_t free_scales = ~0u;  // a stage of scales that is free from this period on
+        uint32_t ua = 0, ub = 0;       // unit of the period's rows, of its weights
+        uint32_t stage = C::AT_S;      // its scales' stage, and its place in their group, in bytes of a row
+        uint32_t at_place = 0;
+        int row_left = total - first;
+        uint32_t free_scales = ~0u;    // a stage of scales that is free from this period on
         const auto period = [&](auto turn) {
             constexpr int TURN = decltype(turn)::value;
-            // TURN 1 of a unit of weights loads the first half of the unit two on, its own place; TURN 0 the second of the next.
             MxLargeAt at;
-            const uint32_t s_stage = (s_at - C::AT_S) / C::S_STAGE * C::S_STAGE;
-            --row_left;
-            const bool ends = ++place == C::G || row_left == 0;
-            const uint32_t s_next = ends ? C::AT_S + C::S_STAGE - s_stage : s_at + C::BK / 32;
-            at.a = smem + ua;
-            at.a_next = smem + (C::UNIT - ua);
-            at.s = smem + s_at;
-            at.s_next = smem + s_next;
+            const bool ends = --row_left == 0 || at_place + C::BK / 32 == C::SB;
+            const uint32_t next_stage = ends ? 2 * C::AT_S + C::S_STAGE - stage : stage;
+            const uint32_t next_place = ends ? 0 : at_place + C::BK / 32;
+            const uint32_t ub_next = TURN == C::TURNS - 1 ? C::UNIT - ub : ub;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                at.a[i] = oa[i] + ua;
+                at.a_next[i] = oa[i] + (C::UNIT - ua);
+                at.b_next[i] = ob[i] + ub_next;
+            }
+            at.sa = scales_a(stage, at_place);
+            at.sa_next = scales_a(next_stage, next_place);
+            at.sb_next = scales_b(next_stage, next_place);
             at.la1 = at_a + C::UNIT - ua;
             at.la2 = at_a + ua;
             at.k1 = round(ka + 128);
             at.k2 = round(at.k1 + 128);
-            if constexpr (C::TURNS == 1) {
-                at.b_next = smem + C::AT_B + C::UNIT - ub;
-                at.lb = at_b + ub;
-                at.kb = round_b(round_b(kw + 128) + 128);
-            } else if constexpr (TURN == 0) {
-                at.b_next = smem + C::AT_B + ub;
-                at.lb = at_b + C::UNIT - ub;
-                at.kb = round_b(kw + 128);
-            } else {
-                at.b_next = smem + C::AT_B + C::UNIT - ub;
-                at.lb = at_b + ub;
-                at.kb = round_b(round_b(kw + 128) + 128);
-            }
+            // (of a unit's two periods, MX8, the first loads the rest of the next unit, the second the half of the one after)
+            at.lb = at_b + (C::TURNS == 2 && TURN == 0 ? C::UNIT - ub : ub);
+            at.kb = round_b(kw + 128);
+            if constexpr (TURN == C::TURNS - 1) at.kb = round_b(at.kb + 128);
             wait_barrier<C::WAIT_X>();
             if (free_scales != ~0u) scales(free_scales);
             MxLarge<C>::template Block<0, TURN>::run(m, acc, at);
@@ -417,17 +609,17 @@ __global__ void __launch_bounds__(C::NT, 1) mx_large(MxArgs g) {
             wait_barrier<C::WAIT_Y>();
             MxLarge<C>::template Block<2, TURN>::run(m, acc, at);
             MxLarge<C>::template Block<3, TURN>::run(m, acc, at);
-            free_scales = ends ? s_stage : ~0u;
-            if (ends) place = 0;
-            s_at = s_next;
+            free_scales = ends ? stage - C::AT_S : ~0u;
+            stage = next_stage;
+            at_place = next_place;
             ua = C::UNIT - ua;
             ka = at.k1;
             if constexpr (TURN == C::TURNS - 1) {
-                ub = C::UNIT - ub;
+                ub = ub_next;
                 kw = round_b(kw + 128);
             }
         };
-        for (int t = 0; t < n; t += C::TURNS) {
+        for (int t = t0; t < t1; t += C::TURNS) {
             period(KindC<0>{});
             if constexpr (C::TURNS == 2) period(KindC<1>{});
         }
@@ -444,14 +636,18 @@ __global__ void __launch_bounds__(C::NT, 1) mx_large(MxArgs g) {
             const int row = m0 + wm0 + 16 * i + li;
 #pragma unroll
             for (int j = 0; j < C::FN; ++j) {
-                const int col = n0 + wn0 + 16 * (j % C::FNP) + lg4;
+                const int col = n0 + wn0 + 32 * (j % C::FNP / 2) + 4 * (j % 2) + 2 * lg4;
                 if (row < g.e.M && col < g.np8)
                     *(f32x4*)(base + ((int64_t)(j / C::FNP) * g.e.M + row) * g.np8 + col) = acc[i][j];
             }
         }
         return;
     }
-    lin_epilogue<C>(g.e, m0, n0, 0, smem, acc, wave, lane, wm0, wn0);
+    MxFinish<C> fin(g.e, m0, n0, wm0 + (lane & 15), wn0 + 8 * (lane >> 4));
+    if (cols_cut(g.e.N)) drain_barrier();  // the ring's memory is free
+    with_act(g.e.act.kind, [&](auto kind) {
+        fin.template run<decltype(kind)::value>(acc, smem + (wave * 64 + lane) * 16);  // 16 bytes of each lane, 4 KiB apart
+    });
 }
 
 }  // namespace pgemm
