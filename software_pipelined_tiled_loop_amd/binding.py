@@ -133,8 +133,8 @@ for _f, _a in (
     getattr(_lib, _f).argtypes = _a
     getattr(_lib, _f).restype = _int
 for _f, _a in (("pgemm_rms_norm_backward_workspace", [_i64, _i64, _int]),
-               ("pgemm_mx_linear_workspace", [_i64, _i64, _i64, _int]),
-               ("pgemm_mx_gated_workspace", [_i64, _i64, _i64, _int])):
+               ("pgemm_mx_linear_workspace", [_i64, _i64, _i64, _int, _int]),
+               ("pgemm_mx_gated_workspace", [_i64, _i64, _i64, _int, _int])):
     getattr(_lib, _f).argtypes = _a
     getattr(_lib, _f).restype = _i64
 
@@ -934,7 +934,7 @@ def _describe_mx_linear(XQ, XS, WQ, WS, Y, bias, residual, act):
     ldy = c.rows("Y", 4, Y, (M, N), own, True)
     c.vector("bias", 5, bias, N, own)
     ldr = c.rows("residual", 6, residual, (M, N), own)
-    return c.done(pgemm_mx_linear, pgemm_mx_linear_workspace(M, N, K, form), lambda p: (
+    return c.done(pgemm_mx_linear, pgemm_mx_linear_workspace(M, N, K, form, t), lambda p: (
         M, N, K, p[0], ldxq, p[1], ldxs, form, p[2], ldwq, p[3], ldws, p[5], p[6], ldr, a, p[4], ldy, t))
 
 
@@ -964,7 +964,7 @@ def _describe_mx_gated(XQ, XS, WgQ, WgS, WuQ, WuS, H, bias_g, bias_u, act):
     ldh = c.rows("H", 6, H, (M, N), own, True)
     c.vector("bias_g", 7, bias_g, N, own)
     c.vector("bias_u", 8, bias_u, N, own)
-    return c.done(pgemm_mx_gated, pgemm_mx_gated_workspace(M, N, K, form), lambda p: (
+    return c.done(pgemm_mx_gated, pgemm_mx_gated_workspace(M, N, K, form, t), lambda p: (
         M, N, K, p[0], ldxq, p[1], ldxs, form, p[2], p[4], g[0], p[3], p[5], g[1], p[7], p[8], a, p[6], ldh, t))
 
 

@@ -172,13 +172,38 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, int format, int gated, int dt
     return best;
 }
 
-int64_t product_workspace(int64_t M, int64_t N, int64_t K, int format, int planes) {
+// fp32 outputs of MX8 activations, of more rows than the few-rows kernels take at once: the scaled
+// MFMAs' sums are not fp32's there (MxFewCfg::WIDE), so linear_kernel multiplies the
+// entries' values, which bf16 holds.
+constexpr int64_t kFewRows = 48;
+bool through_values(int64_t M, int format, int dtype) { return format == MX8 && dtype == PGEMM_F32 && M > kFewRows; }
+// Its workspace: the values, the products' sums (where an epilogue follows), the product's own.
+struct Values {
+    int64_t x, w, z, ldz, own, total;
+};
+int64_t values_layout(int64_t M, int64_t N, int64_t K, int planes, Values& l) {
+    const int64_t filled = mx_filled(K);
+    l.own = pgemm_linear_workspace(M, N, filled, PGEMM_BF16);
+    if (l.own < 0) return l.own;
+    l.ldz = round_up(N, 8);
+    l.x = round_up(M * filled * 2, 256);
+    l.w = round_up(N * filled * 2, 256);
+    l.z = round_up(M * l.ldz * 4, 256);
+    return l.total = l.x + l.w + planes * l.z + l.own;
+}
+
+int64_t product_workspace(int64_t M, int64_t N, int64_t K, int format, int dtype, int planes) {
+    if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
     if (format != PGEMM_MX8 && format != PGEMM_MX4) return PGEMM_ERR_INVALID_ARG;
     if (M < 0 || N < 0 || K < 0) return PGEMM_ERR_INVALID_ARG;
-    if (M > kMaxDim || N >= kMaxLd || K >= kMaxLd || ceil_div(M, 64) * ceil_div(N, 64) >= (int64_t)1 << 24)
+    if (M > kMaxDim || N >= kMaxLd || mx_filled(K) >= kMaxLd || ceil_div(M, 64) * ceil_div(N, 64) >= (int64_t)1 << 24)
         return PGEMM_ERR_TOO_LARGE;
     if (M == 0 || N == 0) return 0;
-    const Plan p = plan_product(M, N, K, format, planes == 2, PGEMM_BF16);  // the types have the same kernels
+    if (through_values(M, format, dtype)) {
+        Values l;
+        return values_layout(M, N, K, planes, l);
+    }
+    const Plan p = plan_product(M, N, K, format, planes == 2, dtype);
     return p.v ? round_up(p.part_bytes, 256) : PGEMM_ERR_TOO_LARGE;
 }
 
@@ -191,10 +216,33 @@ struct Product {
     int64_t ldy;
 };
 
+int run_values(int64_t M, int64_t N, int64_t K, const Product& q, const EpiArgs& e, int planes, void* workspace,
+               hipStream_t stream) {
+    Values l;
+    if (values_layout(M, N, K, planes, l) < 0) return PGEMM_ERR_TOO_LARGE;  // found out before, with the workspace
+    const int64_t filled = mx_filled(K);
+    char* ws = (char*)workspace;
+    char *x = ws, *w = ws + l.x, *z = w + l.w, *own = z + planes * l.z;
+    const bool bare = planes == 1 && !e.bias[0] && !e.R && e.act.kind == ACTK_NONE;  // the sums are the output
+    PGEMM_TRY(pgemm_mx_dequantize(M, filled, q.XQ, q.ldxq, q.XS, q.ldxs, PGEMM_MX8, x, filled, PGEMM_BF16, stream));
+    for (int p = 0; p < planes; ++p) {  // one weight after the other, in the same place
+        PGEMM_TRY(pgemm_mx_dequantize(N, filled, q.WQ[p], q.ldwq, q.WS[p], q.ldws, PGEMM_MX4, w, filled, PGEMM_BF16, stream));
+        PGEMM_TRY(pgemm_linear(M, N, filled, x, filled > 0 ? filled : 1, w, filled > 0 ? filled : 1, PGEMM_NK, nullptr, nullptr, 0,
+                               PGEMM_ACT_NONE, nullptr, 0, bare ? q.Y : (void*)(z + p * l.z), bare ? q.ldy : l.ldz, PGEMM_F32,
+                               PGEMM_BF16, own, l.own, stream));
+    }
+    if (bare) return PGEMM_OK;
+    MxRestArgs a;
+    a.Z = (const float*)z;
+    a.plane = l.z / 4;
+    a.ldz = l.ldz;
+    a.e = e;
+    return launched("mx_rest", kernels_for(PGEMM_F32).rest(a, planes == 2, grid_for(ceil_div(N, 1024) * M, 1), stream));
+}
+
 int run_product(int64_t M, int64_t N, int64_t K, const Product& q, int format, int act, int dtype, int planes,
                 void* workspace, int64_t workspace_bytes, hipStream_t stream) {
-    if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
-    const int64_t need = product_workspace(M, N, K, format, planes), es = elem_size(dtype);
+    const int64_t need = product_workspace(M, N, K, format, dtype, planes), es = elem_size(dtype);
     if (need < 0) return (int)need;
     if (act < PGEMM_ACT_NONE || act > PGEMM_ACT_GELU_TANH) return PGEMM_ERR_INVALID_ARG;
     PGEMM_TRY(check_blocks(q.XQ, q.ldxq, q.XS, q.ldxs, N > 0 ? M : 0, K, format));
@@ -228,6 +276,7 @@ int run_product(int64_t M, int64_t N, int64_t K, const Product& q, int format, i
     a.e.M = (int)M;
     a.e.N = (int)N;
     a.e.out_f32 = dtype == PGEMM_F32;
+    if (through_values(M, format, dtype)) return run_values(M, N, K, q, a.e, planes, workspace, stream);
     const Plan p = plan_product(M, N, K, format, planes == 2, dtype);
     a.tiles_m = (int)p.tiles_m;
     a.tiles_n = (int)p.tiles_n;
@@ -396,11 +445,11 @@ int pgemm_mx_dequantize(int64_t rows, int64_t K, const void* Q, int64_t ldq, con
     return launched("mx_dequantize", kernels_for(dtype).dequantize(a, format, grid, (hipStream_t)stream));
 }
 
-int64_t pgemm_mx_linear_workspace(int64_t M, int64_t N, int64_t K, int x_format) {
-    return product_workspace(M, N, K, x_format, 1);
+int64_t pgemm_mx_linear_workspace(int64_t M, int64_t N, int64_t K, int x_format, int dtype) {
+    return product_workspace(M, N, K, x_format, dtype, 1);
 }
-int64_t pgemm_mx_gated_workspace(int64_t M, int64_t N, int64_t K, int x_format) {
-    return product_workspace(M, N, K, x_format, 2);
+int64_t pgemm_mx_gated_workspace(int64_t M, int64_t N, int64_t K, int x_format, int dtype) {
+    return product_workspace(M, N, K, x_format, dtype, 2);
 }
 
 int pgemm_mx_linear(int64_t M, int64_t N, int64_t K, const void* XQ, int64_t ldxq, const void* XS, int64_t ldxs,

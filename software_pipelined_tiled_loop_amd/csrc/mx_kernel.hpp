@@ -550,6 +550,9 @@ template <int D, int F, int FM_, int FN_, int NW_, int S_, bool GATED_>
 struct MxFewCfg {
     static constexpr int Dt = D, Fmt = F, FM = FM_, FNP = FN_, NW = NW_, S = S_;
     static constexpr bool GATED = GATED_;
+    // Of MX8 operands the scaled MFMAs keep 13 bits below a group's largest product: under a
+    // 16-bit output's rounding, but not an fp32 one's, which takes bf16 MFMAs of the entries' values.
+    static constexpr bool WIDE = F == MX8 && D == DT_F32;
     static constexpr int NP = GATED ? 2 : 1, FN = FNP * NP, NCOLP = 16 * FNP;
     static constexpr int BM = 16 * FM, NT = 64 * NW, XT = F == MX8 ? 2 : 1;  // XT: tiles of 128-byte rows of the activations
     static constexpr int A_TILE = BM * 128, B_TILE = NCOLP * 128;
@@ -567,6 +570,52 @@ __device__ __forceinline__ void dma4(const i32x4& rsrc, uint32_t voff, uint32_t 
                  :
                  : "v"(voff), "s"(rsrc), "s"(lds_base)
                  : "memory", "m0");
+}
+
+// Eight entries' values in bf16, exactly where they are 2^-133 or more.
+template <int F>
+__device__ __forceinline__ bf16x8 mx_bf16(int lo, int hi, uint32_t byte) {
+    const f32x8 v = mx_values<F>(i32x2{lo, hi}, byte);
+    bf16x8 h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (__bf16)v[i];
+    return h;
+}
+// The same on bf16 MFMAs: of four blocks each lane takes its own one, eight entries a step.
+template <class C>
+__device__ __forceinline__ void mx_few_multiply_wide(f32x4 (&acc)[C::FM][C::FN], const char PGEMM_LDS* st, int lane) {
+    const int r = lane & 15, q = lane >> 4;
+    const auto scale = [&](int piece, int row, int ks) -> uint32_t {
+        return *(const uint8_t PGEMM_LDS*)(st + C::AT_S + piece * 256 + row * 8 + ks * 4 + q);
+    };
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        bf16x8 b[C::FN][4];
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            const int p = j / C::FNP, row = 16 * (j % C::FNP) + r;
+            const i32x4 c = *(const i32x4 PGEMM_LDS*)(st + C::AT_B + p * C::B_TILE + a_off<8>(row, ks * 4 + q));
+            const uint32_t byte = scale(C::SPA + p * C::SPB, row, ks);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) b[j][t] = mx_bf16<MX4>(c[t], 0, byte);
+        }
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+            const int row = 16 * i + r;
+            const uint32_t byte = scale(0, row, ks);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const i32x4 c = *(const i32x4 PGEMM_LDS*)(st + ks * C::A_TILE + a_off<8>(row, 2 * q + h));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const bf16x8 x = mx_bf16<MX8>(c[2 * t], c[2 * t + 1], byte);
+#pragma unroll
+                    for (int j = 0; j < C::FN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][2 * h + t], x, acc[i][j], 0, 0, 0);
+                }
+            }
+        }
+    }
 }
 
 template <class C>
@@ -694,7 +743,8 @@ __global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
             lgkm_drain();
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(C::LPS * (C::S - 2)) : "memory");
             issue(t + (C::S - 1) * C::NW, st == 0 ? C::S - 1 : st - 1);
-            mx_few_multiply<C>(acc, ring + st * C::STAGE, lane);
+            if constexpr (C::WIDE) mx_few_multiply_wide<C>(acc, ring + st * C::STAGE, lane);
+            else mx_few_multiply<C>(acc, ring + st * C::STAGE, lane);
             st = st + 1 == C::S ? 0 : st + 1;
         }
     }
@@ -739,6 +789,41 @@ __global__ void __launch_bounds__(C::NT) mx_few(MxArgs g) {
 #pragma unroll
                 for (int z = 0; z < 7; ++z)
                     if (z < ep.valid(0)) ep.template put1<KIND>(0, z, s[0][z], s[C::NP - 1][z]);
+            }
+        });
+    }
+}
+
+// ---- fp32 outputs of many rows of MX8 ----------------------------------------------------------------
+
+// The epilogue of products that linear_kernel has formed of the entries' values in bf16
+// (fp32, [plane][M][ldz]): four columns a thread.  Bound by memory.
+struct MxRestArgs {
+    const float* Z;
+    int64_t plane, ldz;
+    EpiArgs e;
+};
+template <bool GATED>
+__global__ void __launch_bounds__(256) mx_rest(MxRestArgs g) {
+    const int strips = (g.e.N + 1023) / 1024;
+    for (int64_t b = blockIdx.x; b < (int64_t)strips * g.e.M; b += gridDim.x) {
+        const int64_t m = b / strips;
+        const int n0 = (int)(b - m * strips) * 1024 + 4 * (int)threadIdx.x;
+        with_act(g.e.act.kind, [&](auto kind) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = n0 + i;
+                if (n >= g.e.N) break;
+                float z = g.Z[m * g.ldz + n];
+                if (g.e.bias[0]) z += ((const float*)g.e.bias[0])[n];
+                z = act1<decltype(kind)::value>(g.e.act, z);
+                if constexpr (GATED) {
+                    float u = g.Z[g.plane + m * g.ldz + n];
+                    if (g.e.bias[1]) u += ((const float*)g.e.bias[1])[n];
+                    z *= u;
+                }
+                if (g.e.R) z += ((const float*)g.e.R)[m * g.e.ldr + n];
+                ((float*)g.e.Y[0])[m * g.e.ldy + n] = z;
             }
         });
     }

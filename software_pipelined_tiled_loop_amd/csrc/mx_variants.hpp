@@ -40,6 +40,7 @@ struct MxKernels {
     const MxVariant* v;
     int n;
     LinLaunch join, join_gated;
+    hipError_t (*rest)(const MxRestArgs&, bool gated, int grid, hipStream_t);
 };
 
 template <int D, int TPR, int CH>
@@ -75,6 +76,10 @@ template <int D>
 hipError_t launch_dequantize(const MxCopyArgs& a, int format, int grid, hipStream_t s) {
     return format == MX8 ? lin_launch<MxCopyArgs>(&mx_dequantize_rows<D, MX8>, a, dim3(grid), 256, s)
                          : lin_launch<MxCopyArgs>(&mx_dequantize_rows<D, MX4>, a, dim3(grid), 256, s);
+}
+inline hipError_t launch_mx_rest(const MxRestArgs& a, bool gated, int grid, hipStream_t s) {
+    return gated ? lin_launch<MxRestArgs>(&mx_rest<true>, a, dim3(grid), 256, s)
+                 : lin_launch<MxRestArgs>(&mx_rest<false>, a, dim3(grid), 256, s);
 }
 template <class C>
 hipError_t launch_mx_tile(const MxArgs& a, int grid, hipStream_t s) {
@@ -115,16 +120,20 @@ hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
         F, GATED, 16 * FM, 16 * FN, 256, 64 * NW, NW, 163840 / MX_FEW_CFG(D, F, GATED, FM, FN, NW, S)::LDS,     \
             &launch_mx_few<MX_FEW_CFG(D, F, GATED, FM, FN, NW, S)>                                              \
     }
+#define MX_FEWS(D, F, GATED)                                                                                    \
+    MX_FEW(D, F, GATED, 1, 1, 4, 3), MX_FEW(D, F, GATED, 1, 2, 4, 3), MX_FEW(D, F, GATED, 1, 4, 2, 3),           \
+        MX_FEW(D, F, GATED, 2, 1, 4, 3), MX_FEW(D, F, GATED, 2, 2, 4, 2), MX_FEW(D, F, GATED, 3, 2, 2, 3)
 #define MX_CLASS(D, F, GATED, DEEP)                                                                             \
-    MX_LARGE(D, F, GATED), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2), MX_FEW(D, F, GATED, 1, 1, 4, 3),         \
-        MX_FEW(D, F, GATED, 1, 2, 4, 3), MX_FEW(D, F, GATED, 1, 4, 2, 3), MX_FEW(D, F, GATED, 2, 1, 4, 3),      \
-        MX_FEW(D, F, GATED, 2, 2, 4, 2), MX_FEW(D, F, GATED, 3, 2, 2, 3)
-#define MX_VARIANTS(D) MX_CLASS(D, MX8, 0, 3), MX_CLASS(D, MX8, 1, 3), MX_CLASS(D, MX4, 0, 4), MX_CLASS(D, MX4, 1, 4)
+    MX_LARGE(D, F, GATED), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2), MX_FEWS(D, F, GATED)
+// (fp32 outputs of MX8 activations: few rows alone, see MxFewCfg::WIDE; more rows go through linear_kernel)
+#define MX_VARIANTS_MX4(D) MX_CLASS(D, MX4, 0, 4), MX_CLASS(D, MX4, 1, 4)
+#define MX_VARIANTS(D) MX_CLASS(D, MX8, 0, 3), MX_CLASS(D, MX8, 1, 3), MX_VARIANTS_MX4(D)
+#define MX_VARIANTS_F32 MX_FEWS(DT_F32, MX8, 0), MX_FEWS(DT_F32, MX8, 1), MX_VARIANTS_MX4(DT_F32)
 #define MX_KERNELS(D, norms, grads, table)                                                                      \
     MxKernels {                                                                                                 \
         {norms, (int)(sizeof(norms) / sizeof(norms[0]))}, {grads, (int)(sizeof(grads) / sizeof(grads[0]))},     \
             &launch_norm_join<D>, &launch_quantize_any<D>, &launch_dequantize<D>, table,  \
-            (int)(sizeof(table) / sizeof(table[0])), &lin_launch_join<D, false>, &lin_launch_join<D, true>      \
+            (int)(sizeof(table) / sizeof(table[0])), &lin_launch_join<D, false>, &lin_launch_join<D, true>, &launch_mx_rest \
     }
 
 // Per type of the values, each in its own translation unit.

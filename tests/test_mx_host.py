@@ -89,7 +89,10 @@ def test_workspaces():
     assert lib.pgemm_rms_norm_backward_workspace(4096, 4096, 2) % 16384 == 0
     assert lib.pgemm_rms_norm_backward_workspace(5, 4, 3) == DTYPE
     for f in (lib.pgemm_mx_linear_workspace, lib.pgemm_mx_gated_workspace):
-        assert f(1, 1, 1, 0) >= 0 and f(1, 1, 1, 2) == INVALID and f(-1, 1, 1, 0) == INVALID and f(1, 1 << 21, 1, 1) == LARGE
+        assert f(1, 1, 1, 0, 2) >= 0 and f(1, 1, 1, 2, 2) == INVALID and f(-1, 1, 1, 0, 2) == INVALID
+        assert f(1, 1 << 21, 1, 1, 2) == LARGE and f(1, 1, 1, 0, 3) == DTYPE
+        # fp32 outputs of many MX8 rows keep the values of both operands
+        assert f(4096, 4096, 4096, 0, 0) >= 2 * 4096 * 4096 * 2 and f(4096, 4096, 4096, 1, 0) < 1 << 20
 
 
 def test_every_declared_function_is_bound():
