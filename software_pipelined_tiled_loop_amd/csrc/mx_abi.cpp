@@ -20,6 +20,7 @@ constexpr int kNumCU = 256;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 int64_t smaller(int64_t a, int64_t b) { return a < b ? a : b; }
+double larger(double a, double b) { return a > b ? a : b; }
 int64_t elem_size(int dtype) { return dtype == PGEMM_F32 ? 4 : 2; }
 bool float_type(int dtype) { return dtype == PGEMM_F32 || dtype == PGEMM_F16 || dtype == PGEMM_BF16; }
 
@@ -125,25 +126,39 @@ struct Plan {
     int64_t tiles_m, tiles_n, splits, np8, part_bytes;
 };
 
-// Estimated microseconds.
+// Estimated microseconds: a launch's fixed part, what each further round of workgroups
+// adds, and the contraction in steps of 256 entries.  A step takes its loads' latency
+// in each round, or the time in which a CU takes its workgroups' bytes (mx_few) or
+// multiplies (mx_tile; mx_large, alone on its CU).  Fitted to these kernels' times at 448 shapes of
+// 1 to 4096 rows, 128 to 18000 columns and 128 to 16384 entries, each with 1 to 8 splits: the choice is
+// within 1.2 % of the best one on average, and within 35 % at the worst.  The sides
+// of it, in us, at 4096 columns of 4096 entries in 4 bits: 64 rows 5.9 by mx_few's tiles
+// of 32 x 32, 13 by mx_tile; 256 rows 14.1 and 13.2; 2048 rows 31.5 by mx_tile,
+// 32.5 by mx_large; 4096 rows 57 and 38.  A split's join costs more than it gives
+// unless there are few workgroups: 512 rows 13.9 in one go, 23 in two splits.
 double est_us(const MxVariant& v, int64_t M, int64_t N, int64_t filled, int64_t splits) {
-    const int64_t wgs = ceil_div(M, v.bm) * ceil_div(N, v.bn) * splits;
+    const double wgs = (double)(ceil_div(M, v.bm) * ceil_div(N, v.bn) * splits);
+    const auto whole = [](double x) { return (double)(int64_t)(x + 0.999999); };
+    const double per_cu = whole(wgs / kNumCU), rounds = whole(wgs / (kNumCU * v.per_cu));
     const int planes = v.gated ? 2 : 1;
-    const double kt = (double)ceil_div(filled / v.bk, splits) * v.bk;  // entries of a workgroup
+    const bool mx8 = v.format == MX8;
     double us;
     if (v.few) {
-        const double bytes = kt * ((M < v.bm ? M : v.bm) * (v.format == MX8 ? 1.0 : 0.5) + v.bn * planes * 0.53);
-        us = 3.0 * ceil_div(wgs, 2 * kNumCU) + (double)ceil_div(wgs, kNumCU) * bytes / 20e3;
+        const double steps = (double)ceil_div(ceil_div(filled / 256, splits), v.few);
+        const double bytes = (double)v.few * (v.bm * (mx8 ? 256 : 128) + planes * v.bn * 128);
+        us = 3.3 + 0.0008 * v.bm * v.bn * planes + 2.2 * (rounds - 1) + steps * larger(0.26 * rounds, per_cu * bytes / 72e3);
+    } else if (v.bm == 128) {
+        const double steps = (double)smaller(2 * ceil_div(ceil_div(filled, 512), splits), filled / 256);
+        us = 6.5 + 5.3 * (rounds - 1) + steps * larger((mx8 ? 0.19 : 0.16) * rounds, (mx8 ? 0.74 : 0.57) * per_cu);
     } else {
-        const bool large = v.bm == 256;
-        const double rate = (v.format == MX8 ? (large ? 2600e6 : 1300e6) : (large ? 5200e6 : 1600e6)) / kNumCU;
-        us = ceil_div(wgs, (int64_t)kNumCU) * (2.0 * v.bm * v.bn * planes * kt / rate + (large ? 17.0 : 6.0));
+        const double steps = (double)smaller(4 * ceil_div(ceil_div(filled, 1024), splits), filled / 256);
+        us = 1.3 + 11.7 * per_cu + (mx8 ? 2.25 : 1.22) * per_cu * steps;
     }
-    if (splits > 1) us += 5.0 + 0.29 * splits + 2.0 * splits * M * N * planes * 4.0 / 4.4e6;
+    if (splits > 1) us += 3.0 + 0.055 * splits + 0.29 * splits * M * N * planes * 4e-6;
     return us;
 }
 
-// From sizes and format alone, so that the workspace functions and the calls agree.
+// From sizes, format and type alone, so that the workspace functions and the calls agree.
 Plan plan_product(int64_t M, int64_t N, int64_t K, int format, int gated, int dtype) {
     const MxKernels k = kernels_for(dtype);
     const int64_t filled = mx_filled(K);
@@ -155,8 +170,8 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, int format, int gated, int dt
         if (v.format != format || v.gated != gated) continue;
         const int64_t tiles = ceil_div(M, v.bm) * ceil_div(N, v.bn);
         if (round_up(tiles, 8) * v.threads >= (int64_t)1 << 32) continue;
-        for (int64_t s = 1; s <= 16; ++s) {
-            if (s > 1 && (s * (v.few ? v.few : 4) * v.bk > filled || tiles * s > 2 * kNumCU)) break;
+        for (int64_t s : {1, 2, 3, 4, 6, 8}) {
+            if (s > 1 && (s * (v.few ? v.few : 2) * v.bk > filled || tiles * s > 4 * kNumCU)) break;
             const double us = est_us(v, M, N, filled, s);
             if (best.v && us >= best_us) continue;
             best_us = us;
@@ -172,10 +187,11 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, int format, int gated, int dt
     return best;
 }
 
-// fp32 outputs of MX8 activations, of more rows than the few-rows kernels take at once: the scaled
-// MFMAs' sums are not fp32's there (MxFewCfg::WIDE), so linear_kernel multiplies the
-// entries' values, which bf16 holds.
-constexpr int64_t kFewRows = 48;
+// fp32 outputs of MX8 activations: the scaled MFMAs' sums are not fp32's there, so mx_few
+// multiplies the entries' values (MxFewCfg::WIDE).  With more rows the values are
+// written out once, in bf16, which holds them, and linear_kernel multiplies them: by
+// 4096 x 4096 128 rows take 18 us in mx_few, 38 that way; 256 rows 34 and 36; 512 rows 65 and 43.
+constexpr int64_t kFewRows = 256;
 bool through_values(int64_t M, int format, int dtype) { return format == MX8 && dtype == PGEMM_F32 && M > kFewRows; }
 // Its workspace: the values, the products' sums (where an epilogue follows), the product's own.
 struct Values {
@@ -192,7 +208,8 @@ int64_t values_layout(int64_t M, int64_t N, int64_t K, int planes, Values& l) {
     return l.total = l.x + l.w + planes * l.z + l.own;
 }
 
-int64_t product_workspace(int64_t M, int64_t N, int64_t K, int format, int dtype, int planes) {
+// `plan`: the choice, where there is one.
+int64_t product_workspace(int64_t M, int64_t N, int64_t K, int format, int dtype, int planes, Plan& plan) {
     if (!float_type(dtype)) return PGEMM_ERR_UNSUPPORTED_DTYPE;
     if (format != PGEMM_MX8 && format != PGEMM_MX4) return PGEMM_ERR_INVALID_ARG;
     if (M < 0 || N < 0 || K < 0) return PGEMM_ERR_INVALID_ARG;
@@ -203,8 +220,8 @@ int64_t product_workspace(int64_t M, int64_t N, int64_t K, int format, int dtype
         Values l;
         return values_layout(M, N, K, planes, l);
     }
-    const Plan p = plan_product(M, N, K, format, planes == 2, dtype);
-    return p.v ? round_up(p.part_bytes, 256) : PGEMM_ERR_TOO_LARGE;
+    plan = plan_product(M, N, K, format, planes == 2, dtype);
+    return plan.v ? round_up(plan.part_bytes, 256) : PGEMM_ERR_TOO_LARGE;
 }
 
 struct Product {
@@ -242,7 +259,8 @@ int run_values(int64_t M, int64_t N, int64_t K, const Product& q, const EpiArgs&
 
 int run_product(int64_t M, int64_t N, int64_t K, const Product& q, int format, int act, int dtype, int planes,
                 void* workspace, int64_t workspace_bytes, hipStream_t stream) {
-    const int64_t need = product_workspace(M, N, K, format, dtype, planes), es = elem_size(dtype);
+    Plan p;
+    const int64_t need = product_workspace(M, N, K, format, dtype, planes, p), es = elem_size(dtype);
     if (need < 0) return (int)need;
     if (act < PGEMM_ACT_NONE || act > PGEMM_ACT_GELU_TANH) return PGEMM_ERR_INVALID_ARG;
     PGEMM_TRY(check_blocks(q.XQ, q.ldxq, q.XS, q.ldxs, N > 0 ? M : 0, K, format));
@@ -277,7 +295,6 @@ int run_product(int64_t M, int64_t N, int64_t K, const Product& q, int format, i
     a.e.N = (int)N;
     a.e.out_f32 = dtype == PGEMM_F32;
     if (through_values(M, format, dtype)) return run_values(M, N, K, q, a.e, planes, workspace, stream);
-    const Plan p = plan_product(M, N, K, format, planes == 2, dtype);
     a.tiles_m = (int)p.tiles_m;
     a.tiles_n = (int)p.tiles_n;
     a.group_m = 4;
@@ -446,10 +463,12 @@ int pgemm_mx_dequantize(int64_t rows, int64_t K, const void* Q, int64_t ldq, con
 }
 
 int64_t pgemm_mx_linear_workspace(int64_t M, int64_t N, int64_t K, int x_format, int dtype) {
-    return product_workspace(M, N, K, x_format, dtype, 1);
+    Plan p;
+    return product_workspace(M, N, K, x_format, dtype, 1, p);
 }
 int64_t pgemm_mx_gated_workspace(int64_t M, int64_t N, int64_t K, int x_format, int dtype) {
-    return product_workspace(M, N, K, x_format, dtype, 2);
+    Plan p;
+    return product_workspace(M, N, K, x_format, dtype, 2, p);
 }
 
 int pgemm_mx_linear(int64_t M, int64_t N, int64_t K, const void* XQ, int64_t ldxq, const void* XS, int64_t ldxs,

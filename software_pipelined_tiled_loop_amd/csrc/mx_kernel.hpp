@@ -559,7 +559,7 @@ struct MxFewCfg {
     static constexpr int LPA = A_TILE / 1024, LPB = B_TILE / 1024;           // pieces
     static constexpr int SPA = (BM + 31) / 32, SPB = (NCOLP + 31) / 32;      // pieces of scales, 32 rows each
     static constexpr int AT_B = XT * A_TILE, AT_S = AT_B + NP * B_TILE;
-    static constexpr int STAGE = (AT_S + (SPA + NP * SPB) * 256 + 1023) / 1024 * 1024, RING = S * STAGE, LDS = NW * RING;
+    static constexpr int STAGE = AT_S + (SPA + NP * SPB) * 256, RING = S * STAGE, LDS = NW * RING;
     static constexpr int LPS = XT * LPA + NP * LPB + SPA + NP * SPB;
     static_assert(LDS <= 163840 && S >= 2 && LPS * (S - 2) <= 63 && FM * FN * 1024 <= RING, "ring");
 };
