@@ -129,11 +129,12 @@ struct Plan {
 // Estimated microseconds: a launch's fixed part, what each further round of workgroups
 // adds, and the contraction in steps of 256 entries.  A step takes its loads' latency
 // in each round, or the time in which a CU takes its workgroups' bytes (mx_few) or
-// multiplies (mx_tile; mx_large, alone on its CU).  Fitted to these kernels' times at 448 shapes of
-// 1 to 4096 rows, 128 to 18000 columns and 128 to 16384 entries, each with 1 to 8 splits: the choice is
-// within 1.2 % of the best one on average, and within 35 % at the worst.  The sides
-// of it, in us, at 4096 columns of 4096 entries in 4 bits: 64 rows 5.9 by mx_few's tiles
-// of 32 x 32, 13 by mx_tile; 256 rows 14.1 and 13.2; 2048 rows 31.5 by mx_tile,
+// multiplies (mx_tile; mx_large, alone on its CU).  Fitted to these kernels' times, with weights that
+// come from memory, at 580 shapes of 1 to 4096 rows, 128 to 28672 columns and 128 to 16384
+// entries, each with 1 to 8 splits: the choice is within 1.5 % of the best one on average
+// for each format and product, and within 40 % at the worst.  The sides
+// of it, in us, at 4096 columns of 4096 entries in 4 bits, weights in the cache: 64 rows 6.2 by mx_few's
+// tiles of 32 x 32, 13 by mx_tile; 256 rows 14.1 and 13.2; 2048 rows 31.5 by mx_tile,
 // 32.5 by mx_large; 4096 rows 57 and 38.  A split's join costs more than it gives
 // unless there are few workgroups: 512 rows 13.9 in one go, 23 in two splits.
 double est_us(const MxVariant& v, int64_t M, int64_t N, int64_t filled, int64_t splits) {
@@ -146,15 +147,15 @@ double est_us(const MxVariant& v, int64_t M, int64_t N, int64_t filled, int64_t 
     if (v.few) {
         const double steps = (double)ceil_div(ceil_div(filled / 256, splits), v.few);
         const double bytes = (double)v.few * (v.bm * (mx8 ? 256 : 128) + planes * v.bn * 128);
-        us = 3.3 + 0.0008 * v.bm * v.bn * planes + 2.2 * (rounds - 1) + steps * larger(0.26 * rounds, per_cu * bytes / 72e3);
+        us = 3.2 + 0.00075 * v.bm * v.bn * planes + 2.7 * (rounds - 1) + steps * larger(0.115 * rounds, per_cu * bytes / 42.8e3);
     } else if (v.bm == 128) {
         const double steps = (double)smaller(2 * ceil_div(ceil_div(filled, 512), splits), filled / 256);
-        us = 6.5 + 5.3 * (rounds - 1) + steps * larger((mx8 ? 0.19 : 0.16) * rounds, (mx8 ? 0.74 : 0.57) * per_cu);
+        us = 6.6 + 3.1 * (rounds - 1) + (mx8 ? 0.91 : 0.73) * per_cu * steps;
     } else {
         const double steps = (double)smaller(4 * ceil_div(ceil_div(filled, 1024), splits), filled / 256);
-        us = 1.3 + 11.7 * per_cu + (mx8 ? 2.25 : 1.22) * per_cu * steps;
+        us = 3.6 + 8.0 * per_cu + (mx8 ? 2.26 : 1.29) * per_cu * steps;
     }
-    if (splits > 1) us += 3.0 + 0.055 * splits + 0.29 * splits * M * N * planes * 4e-6;
+    if (splits > 1) us += 5.2 + 0.08 * splits + 0.32 * splits * M * N * planes * 4e-6;
     return us;
 }
 

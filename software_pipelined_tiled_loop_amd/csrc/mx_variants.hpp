@@ -120,13 +120,13 @@ hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
         F, GATED, 16 * FM, 16 * FN, 256, 64 * NW, NW, 163840 / MX_FEW_CFG(D, F, GATED, FM, FN, NW, S)::LDS,     \
             &launch_mx_few<MX_FEW_CFG(D, F, GATED, FM, FN, NW, S)>                                              \
     }
-// (fp32 outputs of MX8 are bound by making the values, and have the tiles with enough waves:
+// (fp32 outputs of MX8 are bound by making the values, and have no tiles of more rows:
 // 256 rows of 4096 x 4096 34 us with tiles of 32 x 32 in two waves, 51 with 64 x 32)
 #define MX_FEWS_WIDE(D, F, GATED)                                                                               \
-    MX_FEW(D, F, GATED, 1, 1, 4, 2), MX_FEW(D, F, GATED, 1, 2, 4, 2), MX_FEW(D, F, GATED, 2, 2, 4, 2),           \
-        MX_FEW(D, F, GATED, 2, 2, 2, 3)
+    MX_FEW(D, F, GATED, 1, 1, 4, 3), MX_FEW(D, F, GATED, 1, 2, 4, 3), MX_FEW(D, F, GATED, 2, 2, 2, 3)
 #define MX_FEWS(D, F, GATED)                                                                                    \
-    MX_FEWS_WIDE(D, F, GATED), MX_FEW(D, F, GATED, 2, 1, 4, 2), MX_FEW(D, F, GATED, 4, 2, 2, 2)
+    MX_FEWS_WIDE(D, F, GATED), MX_FEW(D, F, GATED, 1, 4, 2, 3), MX_FEW(D, F, GATED, 3, 2, 2, 3),                 \
+        MX_FEW(D, F, GATED, 4, 2, 2, 2)
 #define MX_CLASS(D, F, GATED, DEEP)                                                                             \
     MX_LARGE(D, F, GATED), MX_TILE(D, F, GATED, 128, 128, DEEP, 2, 2), MX_FEWS(D, F, GATED)
 // (fp32 outputs of MX8 activations: few rows alone, see MxFewCfg::WIDE; more rows go through linear_kernel)
