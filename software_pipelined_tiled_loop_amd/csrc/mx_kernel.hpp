@@ -99,17 +99,19 @@ struct MxScales {
 };
 
 // A scaled MFMA with the accumulators in AGPRs, from inline asm (as mfma_lone):
-// weights times activations, byte KS (0 or 1) of each side's scales.
+// weights times activations, byte KS (0 or 1) of each side's scales.  The compiler may
+// put the scales' filling up to 32 bits right before it, so it brings its own two wait
+// states, which pass while the MFMA before it runs.
 template <class C, int KS>
 __device__ __forceinline__ void mx_mfma(f32x16& acc, const i32x4 (&x)[C::XCH], const i32x4& w, int sx, int sw) {
     if constexpr (C::Fmt == MX8) {
         const i32x8 xx = two_chunks(x[0], x[1]);
-        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4"
+        asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4"
                      : "+a"(acc)
                      : "v"(w), "v"(xx), "v"(sw), "v"(sx), "n"(KS));
     } else {
         asm volatile(
-            "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+            "s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
             : "+a"(acc)
             : "v"(w), "v"(x[0]), "v"(sw), "v"(sx), "n"(KS));
     }
