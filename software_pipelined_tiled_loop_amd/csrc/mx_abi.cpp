@@ -361,7 +361,10 @@ int pgemm_rms_norm(int64_t M, int64_t N, const void* X, int64_t ldx, const void*
     a.y_f32 = out_dtype == PGEMM_F32;
     a.format = format;
     const NormVariant<NormArgs>& v = norm_variant(kernels_for(dtype).norm, a.filled);
-    return launched("rms_norm", v.launch(a, grid_for(M, v.threads < 256 ? 256 / v.threads : 1), (hipStream_t)stream));
+    // at most eight workgroups a CU, which go on to further rows: 4096 x 4096 in bf16 takes 22.5 us with 2048
+    // workgroups, 24.2 with one a row
+    const int64_t grid = smaller(grid_for(M, v.threads < 256 ? 256 / v.threads : 1), 8 * kNumCU);
+    return launched("rms_norm", v.launch(a, (int)grid, (hipStream_t)stream));
 }
 
 int pgemm_rms_norm_backward(int64_t M, int64_t N, const void* dY, int64_t lddy, const void* H, int64_t ldh,

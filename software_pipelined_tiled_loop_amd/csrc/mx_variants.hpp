@@ -96,8 +96,8 @@ hipError_t launch_mx_few(const MxArgs& a, int grid, hipStream_t s) {
 
 #define NORM_VARIANT(D, TPR, CH) NormVariant<NormArgs>{TPR, CH, &launch_norm<D, TPR, CH>}
 #define NORM_VARIANTS(D)                                                                                  \
-    NORM_VARIANT(D, 64, 1), NORM_VARIANT(D, 64, 2), NORM_VARIANT(D, 256, 1), NORM_VARIANT(D, 256, 2),     \
-        NORM_VARIANT(D, 1024, 1), NORM_VARIANT(D, 1024, 2), NormVariant<NormArgs>{1024, 0, &launch_norm_long<D>}
+    NORM_VARIANT(D, 64, 1), NORM_VARIANT(D, 64, 2), NORM_VARIANT(D, 256, 1), NORM_VARIANT(D, 512, 1),     \
+        NORM_VARIANT(D, 512, 2), NORM_VARIANT(D, 1024, 2), NormVariant<NormArgs>{1024, 0, &launch_norm_long<D>}
 #define NORM_GRAD_VARIANT(D, TPR, CH) NormVariant<NormGradArgs>{TPR, CH, &launch_norm_grad<D, TPR, CH>}
 #define NORM_GRAD_VARIANTS(D)                                                                             \
     NORM_GRAD_VARIANT(D, 64, 1), NORM_GRAD_VARIANT(D, 128, 1), NORM_GRAD_VARIANT(D, 256, 1),              \
