@@ -441,7 +441,7 @@ int pgemm_mx_quantize(int64_t rows, int64_t K, const void* X, int64_t ldx, int x
     a.K = (int)K;
     a.filled = (int)mx_filled(K);
     const bool columns = x_order == PGEMM_KN;
-    const int grid = columns ? grid_for(ceil_div(rows, 256) * (a.filled / 256), 1) : share_rows(a, a.filled / 8);
+    const int grid = columns ? grid_for(ceil_div(rows, kColumnRows) * (a.filled / 256), 1) : share_rows(a, a.filled / 8);
     return launched("mx_quantize", kernels_for(dtype).quantize(a, format, columns, grid, (hipStream_t)stream));
 }
 

@@ -222,40 +222,44 @@ __global__ void __launch_bounds__(256) mx_dequantize_rows(MxCopyArgs g) {
     }
 }
 
+constexpr int kEach = 2, kColumnRows = 64 * kEach;  // rows of a thread, of a workgroup
 template <class T>
-struct __attribute__((packed, aligned(sizeof(T)))) Packed4 {
-    T v[4];
+struct __attribute__((packed, aligned(sizeof(T)))) PackedRows {
+    T v[kEach];
 };
-// Rows that are columns in memory (a weight stored K x N).  A workgroup has 256
-// rows by 256 entries: a wave the rows' blocks of 32, a thread four rows' block,
-// loaded in 32 stretches of four elements that lie side by side over the lanes.
-// Codes and scales go through LDS, so that rows are written in whole lines.
+// Rows that are columns in memory (a weight stored K x N).  A workgroup has 128
+// rows by 256 entries: a wave the rows' blocks of 32, a thread two rows' block,
+// loaded in 32 stretches of two elements that lie side by side over the lanes.
+// Codes and scales go through LDS, so that rows are written in whole lines.  Bound by
+// memory: 16384 x 4096 of bf16 to 4 bits takes 31.8 us (5.3 TB/s, in the shared cache
+// partly), to 8 bits 35.6; four rows a thread, whose registers leave a CU one
+// workgroup, which loads and computes in turns, 53.
 template <int D, int F>
 __global__ void __launch_bounds__(512) mx_quantize_columns(MxCopyArgs g) {
     typedef typename Elem<D>::type T;
     constexpr int CB = F == MX8 ? 32 : 16, RB = 8 * CB, CHUNKS = RB / 16;  // bytes of a block's codes, of a row's; its chunks
-    __shared__ __attribute__((aligned(16))) char codes[256 * RB];
-    __shared__ __attribute__((aligned(8))) uint8_t scales[256 * 8];
+    __shared__ __attribute__((aligned(16))) char codes[kColumnRows * RB];
+    __shared__ __attribute__((aligned(8))) uint8_t scales[kColumnRows * 8];
     const int lane = (int)threadIdx.x & 63, blk = (int)threadIdx.x >> 6;
-    const int64_t strips = ((int64_t)g.rows + 255) / 256, total = strips * (g.filled / 256);
+    const int64_t strips = ((int64_t)g.rows + kColumnRows - 1) / kColumnRows, total = strips * (g.filled / 256);
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
-        const int64_t row0 = b % strips * 256;
+        const int64_t row0 = b % strips * kColumnRows;
         const int k0 = (int)(b / strips) * 256, kb = k0 + 32 * blk;
-        const int64_t row = row0 + 4 * lane;
-        const int valid = (int)(g.rows - row < 4 ? g.rows - row : 4);
+        const int64_t row = row0 + kEach * lane;
+        const int valid = (int)(g.rows - row < kEach ? g.rows - row : kEach);
         const T* x = (const T*)g.X + (int64_t)kb * g.ldx + row;
-        Packed4<T> raw[32];
-        if (row0 + 256 <= g.rows && kb + 32 <= g.K) {  // all of the workgroup's rows: no branch between the loads
+        PackedRows<T> raw[32];
+        if (row0 + kColumnRows <= g.rows && kb + 32 <= g.K) {  // all of the workgroup's rows: no branch between the loads
 #pragma unroll
-            for (int j = 0; j < 32; ++j) raw[j] = *(const Packed4<T>*)(x + j * g.ldx);
+            for (int j = 0; j < 32; ++j) raw[j] = *(const PackedRows<T>*)(x + j * g.ldx);
         } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) raw[j].v[e] = kb + j < g.K && e < valid ? x[j * g.ldx + e] : (T)0.0f;
+                for (int e = 0; e < kEach; ++e) raw[j].v[e] = kb + j < g.K && e < valid ? x[j * g.ldx + e] : (T)0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kEach; ++e) {
             f32x8 v[4];
             uint32_t most = 0;
 #pragma unroll
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(512) mx_quantize_columns(MxCopyArgs g) {
             i32x2 c[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[j] = mx_codes<F>(v[j], byte);
-            const int r = 4 * lane + e;
+            const int r = kEach * lane + e;
             // chunks of a row XOR-swizzled by the lane against bank conflicts
             const auto put = [&](int chunk, i32x4 q) { *(i32x4*)(codes + r * RB + ((chunk ^ (lane & 7)) << 4)) = q; };
             if constexpr (F == MX8) {
@@ -279,13 +283,13 @@ __global__ void __launch_bounds__(512) mx_quantize_columns(MxCopyArgs g) {
         }
         __syncthreads();
         const int64_t left = g.rows - row0;
-        for (int i = (int)threadIdx.x; i < 256 * CHUNKS; i += 512) {
+        for (int i = (int)threadIdx.x; i < kColumnRows * CHUNKS; i += 512) {
             const int r = i / CHUNKS, chunk = i % CHUNKS;
             if (r < left)
                 *(i32x4*)((char*)g.Q + (row0 + r) * g.ldq + (int64_t)k0 * CB / 32 + chunk * 16) =
-                    *(const i32x4*)(codes + r * RB + ((chunk ^ ((r >> 2) & 7)) << 4));
+                    *(const i32x4*)(codes + r * RB + ((chunk ^ ((r / kEach) & 7)) << 4));
         }
-        if (threadIdx.x < 256 && (int)threadIdx.x < left) {
+        if (threadIdx.x < kColumnRows && (int)threadIdx.x < left) {
             // (rows of scales are 4-byte aligned)
             int* s = (int*)((uint8_t*)g.S + (row0 + threadIdx.x) * g.lds + k0 / 32);
             s[0] = *(const int*)(scales + threadIdx.x * 8);
