@@ -9,6 +9,14 @@
 // are four consecutive columns of a row.  Its operands, of lane l: row l % 32;
 // e2m1: the 16 bytes of block l / 32 of the step's two; e4m3: the 16-byte pieces
 // l / 32 and 2 + l / 32 of the step's 64 bytes; and the scale of block l / 32.
+// (The 32 x 32 ones need half as many reads of LDS for a product as the 16 x 16 ones, of
+// which mx_large has its own way.)
+//
+// mx_tile has 128 x 128 outputs, two workgroups a CU, and is for grids too small for
+// mx_large's tiles.  Of 4096 columns and entries it takes in 4 bits 11.7 us for 256 rows, 15.3 for
+// 512, 17.6 for 1024 and 31.9 for 2048 (2157 TFLOP/s); with MX8 activations 17.4 for
+// 512, 20.4 and 34.8 for the last two.  Up to one round of the CUs the time is the K loop's
+// latency, 0.3 us for 128 entries with weights from the cache, 0.4 with weights from memory.
 #pragma once
 
 #include "mx_format.hpp"
@@ -59,7 +67,7 @@ PGEMM_HD void mx_inv(int off, int& row, int& kc) {
 
 // Scales go to LDS for 512 entries at a time, 16 bytes of a row, in a ring of their
 // own: four bytes a row with every 128 entries made as many requests to the cache as
-// the codes (4096^3 in 4 bits 46 us instead of @).
+// the codes.
 constexpr int kScaleGroup = 512;
 
 // F: the activations' format.  Tiles of BM rows by BN weights' rows (gated: half of
@@ -543,7 +551,10 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
 // One token to a few dozen: bound by the weights' bytes.  As linear_few: the waves of
 // a workgroup share its outputs (16 FM rows, 16 FNP columns) and deal out the rows'
 // units of 256 entries in turn; each has a ring of its own in LDS, which only it fills
-// and reads, so nothing in the loop waits for another wave.  (Straight from memory to
+// and reads, so nothing in the loop waits for another wave.  16 rows by 4096 x 16384 in 4 bits take
+// 9.2 us (36 MB of weights: 3.9 TB/s), 33 by a pair of 8190 x 4001 13.4; one token by 4096 x 4096 5.6 (the launch
+// 2.5 of it).  Three stages, since with weights from memory two take up to 1.4 times as long (one row by
+// 4096 x 16384 10.8 and 15.4); a fourth gives nothing.  (Straight from memory to
 // registers, neighbouring lanes hold different rows: four times the accesses to the
 // cache, 14 us for 16 by 4096 x 16384 in 4 bits however much was under way.)
 // The 16 x 16 x 128 instruction's lane 16 q + r takes of a unit's step (128 entries) block q of

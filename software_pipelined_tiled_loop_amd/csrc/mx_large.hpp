@@ -21,6 +21,9 @@
 // Block b reads block b + 1's fragments, block 3 those of the next period's block 0 and
 // its weights, each behind the last MFMA that needs what was in its registers.  (In 8
 // bits the weights' 128 bytes of a row last two periods, a quarter at a time.)
+//
+// 4096^3 in 4 bits takes 40.4 us (3400 TFLOP/s), 8192^3 241 (4560); with MX8 activations 52 and
+// 347 (3170).  Of a tile's 40 us some 10 are its first loads and its epilogue.
 #pragma once
 
 #include "mx_kernel.hpp"

@@ -211,7 +211,7 @@ struct NormGradArgs {
 // A block of `rows` rows, as many at once as its threads hold; its columns' sums of
 // dy h s stay in registers.  The next rows are under way while one is summed: TPR
 // threads of one row at a time, and eight rows a block, took 49 us for 4096 x 4096
-// in bf16 with dh.
+// in bf16 with dh, this takes 38 (134 MB: 3.5 TB/s) and its join 4.6.
 constexpr int kNormGradThreads = 1024;
 
 template <int D, int TPR, int CH>
