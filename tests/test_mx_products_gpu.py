@@ -190,6 +190,74 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
 
 
+def test_far_rows_of_large_tiles():
+    """The large tiles' own epilogue, output and residual beyond 2^32 bytes, at the output's odd edges."""
+    M, N, K, far = 4600, 3507, 300, 1 << 20
+    g = gen(9)
+    X, _ = stored(g, M, K, "mx4")
+    W, _ = stored(g, N, K, "mx4", K ** -0.5)
+    near = torch.randn(M, N, generator=g, device="cuda").bfloat16()
+    space = torch.full((M * far // 2,), 9.0, dtype=torch.bfloat16, device="cuda")
+    R, Y = (space.as_strided((M, N), (far // 2, 1), at) for at in (5, 8200))
+    R.copy_(near)
+    want = pg.mx_linear(X, W, torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), residual=near, act="silu")
+    assert torch.equal(pg.mx_linear(X, W, Y, residual=R, act="silu"), want)
+    assert torch.equal(R, near)
+    assert bool((space.as_strided((M, 8200 - 5 - N), (far // 2, 1), 5 + N) == 9).all())
+    assert bool((space.as_strided((M, far // 2 - 8200 - N), (far // 2, 1), 8200 + N) == 9).all())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("M,N", [(5, 700), (3, 5000), (2, 20001)])
+def test_norms_in_place(M, N, dtype):
+    """h over x or over the residual, dx over dh: the same results."""
+    t, g = TYPES[dtype], gen(N)
+    x, r, dy, dh = (torch.randn(M, N, generator=g, device="cuda").to(t) for _ in range(4))
+    w = torch.randn(N, generator=g, device="cuda").to(t)
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    pg.rms_norm(x, w, y, residual=r, H=h)
+    for k in range(2):
+        a = [x.clone(), r.clone()]
+        again = torch.empty_like(y)
+        pg.rms_norm(a[0], w, again, residual=a[1], H=a[k])
+        assert torch.equal(again, y) and torch.equal(a[k], h)
+    dx, dw = pg.rms_norm_backward(dy, h, w, dH=dh, dX=torch.empty_like(x), dweight=torch.empty_like(w))
+    over = dh.clone()
+    dw2 = torch.empty_like(w)
+    pg.rms_norm_backward(dy, h, w, dH=over, dX=over, dweight=dw2)
+    assert torch.equal(over, dx) and torch.equal(dw2, dw)
+
+
+def test_norm_gradient_against_differences():
+    """The backward pass against central differences of the forward pass: they differ by what the 64-bit forms say (the
+    differences' own cubic term) and by the roundings of both passes, as bounded there."""
+    g = gen(11)
+    M, N, step, t = 4, 65, 2.0 ** -6, torch.float32
+    h, dy, w = (torch.randn(*s, generator=g, device="cuda") for s in ((M, N), (M, N), (N,)))
+    dx, dw = pg.rms_norm_backward(dy, h, w, dX=torch.empty_like(h), dweight=torch.empty_like(w))
+    (wx, ex), (ww, ew) = ref.norm_backward(dy, h, w, None, 1e-6)
+    (wx, ex), (ww, ew) = ref.round_out(wx, ex, t), ref.round_out(ww, ew, t)
+    d64 = dy.double().cpu()
+
+    def loss(h_, w_):
+        """(of the operator, of the 64-bit form, how far apart they may be)"""
+        y = pg.rms_norm(h_, w_, torch.empty_like(h_)).double().cpu()
+        v, e = ref.round_out(*ref.norm(h_, None, w_, 1e-6)[1], t)
+        return (y * d64).sum(), (v * d64).sum(), (e * d64.abs()).sum()
+    for _ in range(12):
+        vh, vw = torch.randn(M, N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+        for up, down, v, got, want, e in ((loss(h + step * vh, w), loss(h - step * vh, w), vh, dx, wx, ex),
+                                          (loss(h, w + step * vw), loss(h, w - step * vw), vw, dw, ww, ew)):
+            v = v.double().cpu()
+            difference, plain = (up[0] - down[0]) / (2 * step), (up[1] - down[1]) / (2 * step)
+            cubic = plain - (want * v).sum()
+            bound = (up[2] + down[2]) / (2 * step) + (e * v.abs()).sum()
+            # (h +- step v is rounded, the same way in both forms: half the difference's slope errs by 2^-24 of |h| or |w|)
+            rounding = 2.0 ** -24 * (want.abs() * ((h if v.dim() == 2 else w).double().cpu().abs() + step * v.abs())).sum() / step
+            assert abs(difference - cubic - (got.double().cpu() * v).sum()) <= bound + 4 * rounding
+            assert abs(cubic) < 0.1 * (want.abs() * v.abs()).sum()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("form", ["mx8", "mx4"])
 @pytest.mark.parametrize("M", [1, 33, 300])
