@@ -171,8 +171,9 @@ __device__ __forceinline__ MxPlace mx_place(const MxCopyArgs& g, int64_t b) {
     return MxPlace{(lot << (8 - g.shift)) + ((int)threadIdx.x >> g.shift), (stretch * (kRun << g.shift) + t) * 8, 8 << g.shift};
 }
 
-// Rows whose entries lie side by side: a lane has eight of them, four lanes a block.
-// Bound by memory.
+// Rows whose entries lie side by side: a lane has eight of them, four lanes a block, and two
+// such groups under way.  Bound by memory: 16384 x 4096 of bf16 to 4 bits takes 27 us
+// (6.3 TB/s, in the shared cache partly), to 8 bits 30, of fp32 to 4 bits 48.
 template <int D, int F>
 __global__ void __launch_bounds__(256) mx_quantize_rows(MxCopyArgs g) {
     typedef typename Elem<D>::type T;
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(256) mx_quantize_rows(MxCopyArgs g) {
     }
 }
 
+// The same way back.  16384 x 4096 to bf16 takes 36 us from 4 bits (4.7 TB/s) and from 8: the writes bound it.
 template <int D, int F>
 __global__ void __launch_bounds__(256) mx_dequantize_rows(MxCopyArgs g) {
     typedef typename Elem<D>::type T;

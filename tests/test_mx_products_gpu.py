@@ -190,6 +190,22 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("form", ["mx8", "mx4"])
+@pytest.mark.parametrize("M,N", [(2, 7), (300, 130), (2304, 2297)])
+def test_no_entries(M, N, form, dtype):
+    """K = 0 on every way: bias, activation and residual alone."""
+    t, g = TYPES[dtype], gen(M)
+    X, W = pg.mx_empty(M, 0, form, "cuda"), pg.mx_empty(N, 0, "mx4", "cuda")
+    b, u = (torch.randn(N, generator=g, device="cuda").to(t) for _ in range(2))
+    R = torch.randn(M, N, generator=g, device="cuda").to(t)
+    assert torch.equal(pg.mx_linear(X, W, torch.full_like(R, 9)), torch.zeros_like(R))
+    assert torch.equal(pg.mx_linear(X, W, torch.full_like(R, 9), bias=b, residual=R, act="relu"),
+                       (b.float().clamp_min(0) + R.float()).to(t))
+    assert torch.equal(pg.mx_gated(X, W, W, torch.full_like(R, 9), bias_g=b, bias_u=u, act="relu"),
+                       (b.float().clamp_min(0) * u.float()).to(t).expand(M, N))
+
+
 def test_far_rows_of_large_tiles():
     """The large tiles' own epilogue, output and residual beyond 2^32 bytes, at the output's odd edges."""
     M, N, K, far = 4600, 3507, 300, 1 << 20
