@@ -193,7 +193,9 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, int format, int gated, int dt
 // written out once, in bf16, which holds them, and linear_kernel multiplies them: by
 // 4096 x 4096 128 rows take 18 us in mx_few, 38 that way; 256 rows 34 and 36; 512 rows 65 and 43.
 constexpr int64_t kFewRows = 256;
-bool through_values(int64_t M, int format, int dtype) { return format == MX8 && dtype == PGEMM_F32 && M > kFewRows; }
+bool through_values(int64_t M, int64_t K, int format, int dtype) {
+    return format == MX8 && dtype == PGEMM_F32 && M > kFewRows && K > 0;
+}
 // Its workspace: the values, the products' sums (where an epilogue follows), the product's own.
 struct Values {
     int64_t x, w, z, ldz, own, total;
@@ -203,6 +205,7 @@ int64_t values_layout(int64_t M, int64_t N, int64_t K, int planes, Values& l) {
     l.own = pgemm_linear_workspace(M, N, filled, PGEMM_BF16);
     if (l.own < 0) return l.own;
     l.ldz = round_up(N, 8);
+    if (l.ldz >= kMaxLd) return PGEMM_ERR_TOO_LARGE;
     l.x = round_up(M * filled * 2, 256);
     l.w = round_up(N * filled * 2, 256);
     l.z = round_up(M * l.ldz * 4, 256);
@@ -217,7 +220,7 @@ int64_t product_workspace(int64_t M, int64_t N, int64_t K, int format, int dtype
     if (M > kMaxDim || N >= kMaxLd || mx_filled(K) >= kMaxLd || ceil_div(M, 64) * ceil_div(N, 64) >= (int64_t)1 << 24)
         return PGEMM_ERR_TOO_LARGE;
     if (M == 0 || N == 0) return 0;
-    if (through_values(M, format, dtype)) {
+    if (through_values(M, K, format, dtype)) {
         Values l;
         return values_layout(M, N, K, planes, l);
     }
@@ -295,7 +298,7 @@ int run_product(int64_t M, int64_t N, int64_t K, const Product& q, int format, i
     a.e.M = (int)M;
     a.e.N = (int)N;
     a.e.out_f32 = dtype == PGEMM_F32;
-    if (through_values(M, format, dtype)) return run_values(M, N, K, q, a.e, planes, workspace, stream);
+    if (through_values(M, K, format, dtype)) return run_values(M, N, K, q, a.e, planes, workspace, stream);
     a.tiles_m = (int)p.tiles_m;
     a.tiles_n = (int)p.tiles_n;
     a.group_m = 4;

@@ -91,6 +91,7 @@ def test_workspaces():
     for f in (lib.pgemm_mx_linear_workspace, lib.pgemm_mx_gated_workspace):
         assert f(1, 1, 1, 0, 2) >= 0 and f(1, 1, 1, 2, 2) == INVALID and f(-1, 1, 1, 0, 2) == INVALID
         assert f(1, 1 << 21, 1, 1, 2) == LARGE and f(1, 1, 1, 0, 3) == DTYPE
+        assert f(300, (1 << 21) - 1, 1, 0, 0) == LARGE and f(300, (1 << 21) - 8, 1, 0, 0) > 0
         # fp32 outputs of many MX8 rows keep the values of both operands
         assert f(4096, 4096, 4096, 0, 0) >= 2 * 4096 * 4096 * 2 and f(4096, 4096, 4096, 1, 0) < 1 << 20
 
