@@ -87,15 +87,17 @@ const NormVariant<Args>& norm_variant(const NormTable<Args>& t, int64_t filled) 
     return t.v[i];
 }
 
-// Blocks of rows of the backward pass, one a CU; their sums are joined afterwards.
+// Blocks of rows of the backward pass, two a CU (one where a row takes all of a workgroup's 1024 threads);
+// their sums are joined afterwards.
 struct NormBlocks {
     int64_t rows, blocks, np8;
 };
 NormBlocks norm_blocks(int64_t M, int64_t N, const NormVariant<NormGradArgs>& v) {
     NormBlocks b;
-    const int64_t at_once = v.groups ? kNormGradThreads / v.threads : 1, steps = ceil_div(M, at_once);
+    const bool wide = v.threads == 1024;
+    const int64_t at_once = wide ? 1 : 512 / v.threads, steps = ceil_div(M, at_once), most = wide ? kNumCU : 2 * kNumCU;
     // up to four steps stay in one block, which writes the sums itself
-    b.rows = (steps <= 4 ? steps : ceil_div(steps, kNumCU)) * at_once;
+    b.rows = (steps <= 4 ? steps : ceil_div(steps, most)) * at_once;
     if (b.rows == 0) b.rows = at_once;
     b.blocks = ceil_div(M, b.rows);
     b.np8 = round_up(N, 8);

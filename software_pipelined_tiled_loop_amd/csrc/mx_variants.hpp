@@ -49,11 +49,11 @@ hipError_t launch_norm(const NormArgs& a, int grid, hipStream_t s) {
 }
 template <int D, int TPR, int CH>
 hipError_t launch_norm_grad(const NormGradArgs& a, int grid, hipStream_t s) {
-    return lin_launch<NormGradArgs>(&rms_norm_grad<D, TPR, CH>, a, dim3(grid), kNormGradThreads, s);
+    return lin_launch<NormGradArgs>(&rms_norm_grad<D, TPR, CH>, a, dim3(grid), norm_grad_threads<TPR>, s);
 }
 template <int D>
 hipError_t launch_norm_join(const NormSumArgs& a, int grid, hipStream_t s) {
-    return lin_launch<NormSumArgs>(&rms_norm_join<D>, a, dim3(grid), 256, s);
+    return lin_launch<NormSumArgs>(&rms_norm_join<D>, a, dim3(grid), 1024, s);
 }
 template <int D>
 hipError_t launch_norm_long(const NormArgs& a, int grid, hipStream_t s) {

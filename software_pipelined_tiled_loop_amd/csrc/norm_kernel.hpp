@@ -209,15 +209,17 @@ struct NormGradArgs {
 };
 
 // A block of `rows` rows, as many at once as its threads hold; its columns' sums of
-// dy h s stay in registers.  The next rows are under way while one is summed: TPR
-// threads of one row at a time, and eight rows a block, took 49 us for 4096 x 4096
-// in bf16 with dh, this takes 38 (134 MB: 3.5 TB/s) and its join 4.6.
-constexpr int kNormGradThreads = 1024;
+// dy h s stay in registers.  The next rows are under way while one is summed.  Two
+// workgroups of 512 threads a CU cover each other's barriers: 4096 x 4096 in bf16 with dh takes
+// 25.8 us (134 MB, 5.2 TB/s, in the shared cache partly), 30.2 by one of 1024 threads, 35.9 by
+// one of 512, 28.7 by four; 49 without the next rows under way, in blocks of eight rows.
+template <int TPR>
+constexpr int norm_grad_threads = TPR < 512 ? 512 : TPR;
 
 template <int D, int TPR, int CH>
-__global__ void __launch_bounds__(kNormGradThreads) rms_norm_grad(NormGradArgs g) {
+__global__ void __launch_bounds__(norm_grad_threads<TPR>) rms_norm_grad(NormGradArgs g) {
     typedef typename Elem<D>::type T;
-    constexpr int NT = kNormGradThreads, RPW = NT / TPR;
+    constexpr int NT = norm_grad_threads<TPR>, RPW = NT / TPR;
     __shared__ float red[2][RPW][32];
     __shared__ f32x8 join[RPW > 1 ? NT : 1];
     const int t = (int)threadIdx.x % TPR, mine = (int)threadIdx.x / TPR;
@@ -338,29 +340,29 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_long(NormGradArgs g) {
     }
 }
 
-// The blocks' sums in a fixed order: sixteen interleaved runs of blocks, then the
-// runs.  Sixteen columns a workgroup, so that few columns spread over the CUs too.
+// The blocks' sums in a fixed order: 64 interleaved runs of blocks, then the
+// runs.  512 blocks of 4096 columns take 4.9 us, most of it the launch.  Sixteen columns a workgroup, so that few columns spread over the CUs too.
 struct NormSumArgs {
     const float* sums;  // [blocks][np8]
     void* out;
     int blocks, np8, N, out_f32;
 };
 template <int D>
-__global__ void __launch_bounds__(256) rms_norm_join(NormSumArgs g) {
+__global__ void __launch_bounds__(1024) rms_norm_join(NormSumArgs g) {
     typedef typename Elem<D>::type T;
-    __shared__ float red[16][16];
+    __shared__ float red[64][16];
     const int c = (int)threadIdx.x & 15, run = (int)threadIdx.x >> 4;
     for (int64_t n0 = (int64_t)blockIdx.x * 16; n0 < g.N; n0 += (int64_t)gridDim.x * 16) {
         const int64_t n = n0 + c;
         float x = 0.0f;
         if (n < g.N) {
 #pragma unroll 8
-            for (int b = run; b < g.blocks; b += 16) x += g.sums[(int64_t)b * g.np8 + n];
+            for (int b = run; b < g.blocks; b += 64) x += g.sums[(int64_t)b * g.np8 + n];
         }
         red[run][c] = x;
         __syncthreads();
         if (run == 0 && n < g.N) {
-            for (int k = 1; k < 16; ++k) x += red[k][c];
+            for (int k = 1; k < 64; ++k) x += red[k][c];
             if (g.out_f32) ((float*)g.out)[n] = x;
             else ((T*)g.out)[n] = (T)x;
         }
