@@ -99,6 +99,25 @@ def test_scales_over_their_range(M, N, K, form):
         at_once(pg.mx_linear(X, W, torch.empty(M, N, dtype=t, device="cuda")), *ref.round_out(z, e, t), str(t))
 
 
+@pytest.mark.parametrize("form", ["mx8", "mx4"])
+@pytest.mark.parametrize("M", [5, 300, 2304])
+def test_the_smallest_entries(M, form):
+    """Entries below 2^-126, down to 2^-133, with weights that bring the products back: nothing is taken for zero."""
+    g, N, K = gen(12), 2297 if M > 300 else 70, 512
+    X, W = pg.mx_empty(M, K, form, "cuda"), pg.mx_empty(N, K, "mx4", "cuda")
+    codes = torch.randint(0, 256, X[0].shape, generator=g, device="cuda")
+    X[0].copy_(torch.where(codes % 128 == 127, torch.zeros_like(codes), codes) if form == "mx8" else codes)  # no NaN
+    X[1].copy_(torch.randint(3, 9, X[1].shape, generator=g, device="cuda"))
+    W[0].copy_(torch.randint(0, 256, W[0].shape, generator=g, device="cuda"))
+    W[1].copy_(torch.randint(220, 224, W[1].shape, generator=g, device="cuda"))
+    x, w = ref.values(*X, form).cuda(), ref.values(*W, "mx4").cuda()
+    for t in (torch.float32, torch.bfloat16):
+        z, e = ref.product(x, w, form, t)
+        at_once(pg.mx_linear(X, W, torch.empty(M, N, dtype=t, device="cuda")), *ref.round_out(z, e, t), str(t))
+    back = pg.mx_dequantize(X, torch.empty(M, K, device="cuda"))
+    assert torch.equal(back.double(), x)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", PLACES)
 def test_streams_graphs_and_repeats(M, N, K, dtype):
