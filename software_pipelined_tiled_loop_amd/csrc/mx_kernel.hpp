@@ -94,6 +94,27 @@ struct MxCfg {
     static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0 && NW % 4 == 0, "a wave's pieces lie in one operand");
     static_assert(S_INSTR * NW * 64 == BM + BN && BM % (64 * S_INSTR) == 0 && BNP % (64 * S_INSTR) == 0, "scale pieces");
     static_assert(LDS <= 163840 && S >= 2 && LPS * (S - 2) <= 63, "ring");
+    // Behind the ready edge of a group's last K tile the group after next is issued, and first read behind that of the
+    // next group's last one: two edges later or more (a row's last group may be two K tiles), by when 2 LPS pieces have followed.
+    static_assert(LPS * (S - 2) <= 2 * LPS, "scales are covered by the edge before their first read");
+};
+
+// Where the scales lie, as a wave goes along its K tiles, two of them at a time: half a
+// group of scales, and a row ends with a pair.
+template <class C>
+struct MxTileWalk {
+    uint32_t scale = C::AT_S;  // of the next pair's first K tile, in LDS (places in a group are 0 and 8)
+    uint32_t stage = C::AT_S;  // the pair's scales' stage
+    int row_left;              // pairs to the row's end
+    bool half = false, ends = false;  // the next pair is its group's second; the pair is its group's last one
+    PGEMM_HD explicit MxTileWalk(int pairs) : row_left(pairs) {}
+    // Behind the pair's first K tile; where `ends`, the stage is free behind the second one's ready edge.
+    PGEMM_HD void pair() {
+        stage = scale & ~15u;
+        ends = --row_left == 0 || half;
+        half = !ends;
+        scale = ends ? (uint32_t)(2 * C::AT_S + C::S_STAGE) - stage : stage + 8;
+    }
 };
 
 template <class C>
@@ -484,9 +505,9 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
         MxFrags<C> f[2];
         MxScales<C> sc[2];
         mx_first<C>(smem, smem + C::AT_S, wm0, wn0, lane, f[0], sc[0]);
-        // Stages as bytes from the ring's beginning; the scales of the next K tile.
-        uint32_t cur = 0, prev = LASTST, scale = C::AT_S;
-        int row_left = (total - first) / 2, odd = 0;
+        // Stages as bytes from the ring's beginning.
+        uint32_t cur = 0, prev = LASTST;
+        MxTileWalk<C> walk((total - first) / 2);
         const auto tile = [&](const MxScales<C>& us, MxScales<C>& next, uint32_t next_scale, uint32_t free_scales) {
             const uint32_t nxt = cur == LASTST ? 0 : cur + C::STAGE;
             MxAt at;
@@ -509,16 +530,10 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
             prev = cur;
             cur = nxt;
         };
-        // K tiles come in pairs, half a group of scales; a row ends with a pair.
         for (int t = t0; t < t1; t += 2) {
-            tile(sc[0], sc[1], scale + 4, 0);
-            const uint32_t stage = scale & ~15u;  // (places in a group are 0 and 8)
-            odd ^= 1;
-            const bool ends = --row_left == 0 || odd == 0;
-            const uint32_t other = (uint32_t)(2 * C::AT_S + C::S_STAGE) - stage;
-            odd = ends ? 0 : 1;
-            scale = ends ? other : stage + 8;
-            tile(sc[1], sc[0], scale, ends ? at_s + (stage - C::AT_S) : 0);
+            tile(sc[0], sc[1], walk.scale + 4, 0);
+            walk.pair();
+            tile(sc[1], sc[0], walk.scale, walk.ends ? at_s + (walk.stage - C::AT_S) : 0);
         }
         __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing LDS
     }

@@ -22,6 +22,13 @@
 // its weights, each behind the last MFMA that needs what was in its registers.  (In 8
 // bits the weights' 128 bytes of a row last two periods, a quarter at a time.)
 //
+// Loads arrive in the order in which they were issued, so an edge's vmcnt says which of
+// them it leaves under way: X the pieces of the period before it (WAIT_X), Y this period's and the
+// last four of the one before (WAIT_Y).  A group of scales is loaded behind edge X of the first period
+// of the group before it and read from block 3 of that group's last period on.  Edge X of
+// any later period covers it; where that group is a single period, which in 4 bits
+// a row's last one may be, edge Y of the same period has to (MxLargeWalk::wait_y).
+//
 // 4096^3 in 4 bits takes 40.4 us (3400 TFLOP/s), 8192^3 241 (4560); with MX8 activations 52 and
 // 347 (3170).  Of a tile's 40 us some 10 are its first loads and its epilogue.
 #pragma once
@@ -46,8 +53,37 @@ struct MxLargeCfg {
     static constexpr int S_STAGE = 512 * SB, TOTAL = AT_S + 2 * S_STAGE;
     static constexpr int PB = 8 / TURNS;                  // the wave's pieces of the weights a period
     static constexpr int PIECES = 8 + PB;                 // of codes a period
-    static constexpr int WAIT_X = PIECES, WAIT_Y = PIECES / 2 + 4;
+    // Loads that the edges leave under way: see above.  Y_SCALES covers scales issued behind the edge X before it.
+    static constexpr int WAIT_X = PIECES, WAIT_Y = PIECES / 2 + 4, WAIT_Y_SCALES = PIECES / 2;
+    static constexpr bool SINGLE = BK == kMxGroup;        // a row's last group of scales may be a single period
     static_assert(TOTAL == 163840 && FN == 8, "all of a CU's LDS");
+    static_assert(WAIT_X <= PIECES && WAIT_Y_SCALES <= PIECES / 2, "scales are covered by the edge before their first read");
+};
+
+// Where the scales of the periods lie, and when a group of them is loaded: a wave's way
+// along its periods, a row's last group perhaps cut.
+template <class C>
+struct MxLargeWalk {
+    uint32_t stage = C::AT_S, place = 0;    // of this period's scales: in LDS, and in their group, in bytes of a row
+    uint32_t next_stage = 0, next_place = 0;
+    uint32_t free = ~0u;                    // a stage that is free from this period on: the next group is loaded into it
+    int row_left;                           // periods to the row's end
+    bool ends = false;                      // the period is its group's last one
+    PGEMM_HD explicit MxLargeWalk(int left) : row_left(left) {}
+    PGEMM_HD void enter() {
+        ends = --row_left == 0 || place + C::BK / 32 == C::SB;
+        next_stage = ends ? 2 * C::AT_S + C::S_STAGE - stage : stage;
+        next_place = ends ? 0 : place + C::BK / 32;
+    }
+    PGEMM_HD bool loads() const { return free != ~0u; }
+    // Block 3 reads the scales that were loaded behind this period's own edge X.
+    PGEMM_HD bool reads_at_once() const { return C::SINGLE && ends && loads(); }
+    PGEMM_HD int wait_y() const { return reads_at_once() ? C::WAIT_Y_SCALES : C::WAIT_Y; }
+    PGEMM_HD void leave() {
+        free = ends ? stage - C::AT_S : ~0u;
+        stage = next_stage;
+        place = next_place;
+    }
 };
 
 // Of two blocks' 32 weights' rows the even block's are 0 .. 3, 8 .. 11, 16 .., the odd one's four further on: a lane's
@@ -151,14 +187,16 @@ struct MxLarge {
     //   0, 1 rows of block 3 (next period)   2, 3 of block 0 (the one after)   weights, first half
     //   weights, second half                 rows of blocks 1 and 2 (the one after)
     static constexpr bool placed(int p) { return p < 4 || p >= 4 + C::PB ? p % 2 == 0 : (p - 4) % H == 0; }
+    static constexpr int block_of(int p) { return p < 2 ? 3 : p < 4 ? 0 : p < 4 + C::PB ? -1 : 1 + (p - 4 - C::PB) / 2; }
+    static constexpr int weights_of(int p, int turn) { return (C::TURNS == 2 && turn == 0 ? 4 : 0) + p - 4; }
     template <int P, int TURN, bool PLACE>
     __device__ __forceinline__ void piece(const MxLargeAt& at) const {
-        if constexpr (P < 4 || P >= 4 + C::PB) {
-            constexpr int BLOCK = P < 2 ? 3 : P < 4 ? 0 : 1 + (P - 4 - C::PB) / 2, X = P % 2;
+        if constexpr (block_of(P) >= 0) {
+            constexpr int BLOCK = block_of(P), X = P % 2;
             if constexpr (PLACE) place<BLOCK * 4096>(P < 2 ? at.la1 : at.la2);
             else load<X * 1024>(va[2 * BLOCK + X], ra, P < 2 ? at.k1 : at.k2);
         } else {
-            constexpr int Q = (C::TURNS == 2 && TURN == 0 ? 4 : 0) + P - 4;
+            constexpr int Q = weights_of(P, TURN);
             if constexpr (PLACE) place<Q * 1024>(at.lb);
             else load<Q % H * 1024>(vb[Q], rb, at.kb);
         }
@@ -577,16 +615,11 @@ __global__ void __launch_bounds__(C::NT, 1) mx_large(MxArgs g) {
         m.first_b(ob, scales_b(C::AT_S, 0));
 
         uint32_t ua = 0, ub = 0;       // unit of the period's rows, of its weights
-        uint32_t stage = C::AT_S;      // its scales' stage, and its place in their group, in bytes of a row
-        uint32_t at_place = 0;
-        int row_left = total - first;
-        uint32_t free_scales = ~0u;    // a stage of scales that is free from this period on
+        MxLargeWalk<C> walk(total - first);
         const auto period = [&](auto turn) {
             constexpr int TURN = decltype(turn)::value;
             MxLargeAt at;
-            const bool ends = --row_left == 0 || at_place + C::BK / 32 == C::SB;
-            const uint32_t next_stage = ends ? 2 * C::AT_S + C::S_STAGE - stage : stage;
-            const uint32_t next_place = ends ? 0 : at_place + C::BK / 32;
+            walk.enter();
             const uint32_t ub_next = TURN == C::TURNS - 1 ? C::UNIT - ub : ub;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -594,9 +627,9 @@ __global__ void __launch_bounds__(C::NT, 1) mx_large(MxArgs g) {
                 at.a_next[i] = oa[i] + (C::UNIT - ua);
                 at.b_next[i] = ob[i] + ub_next;
             }
-            at.sa = scales_a(stage, at_place);
-            at.sa_next = scales_a(next_stage, next_place);
-            at.sb_next = scales_b(next_stage, next_place);
+            at.sa = scales_a(walk.stage, walk.place);
+            at.sa_next = scales_a(walk.next_stage, walk.next_place);
+            at.sb_next = scales_b(walk.next_stage, walk.next_place);
             at.la1 = at_a + C::UNIT - ua;
             at.la2 = at_a + ua;
             at.k1 = round(ka + 128);
@@ -606,15 +639,14 @@ __global__ void __launch_bounds__(C::NT, 1) mx_large(MxArgs g) {
             at.kb = round_b(kw + 128);
             if constexpr (TURN == C::TURNS - 1) at.kb = round_b(at.kb + 128);
             wait_barrier<C::WAIT_X>();
-            if (free_scales != ~0u) scales(free_scales);
+            if (walk.loads()) scales(walk.free);
             MxLarge<C>::template Block<0, TURN>::run(m, acc, at);
             MxLarge<C>::template Block<1, TURN>::run(m, acc, at);
-            wait_barrier<C::WAIT_Y>();
+            if (walk.wait_y() == C::WAIT_Y) wait_barrier<C::WAIT_Y>();
+            else wait_barrier<C::WAIT_Y_SCALES>();
             MxLarge<C>::template Block<2, TURN>::run(m, acc, at);
             MxLarge<C>::template Block<3, TURN>::run(m, acc, at);
-            free_scales = ends ? stage - C::AT_S : ~0u;
-            stage = next_stage;
-            at_place = next_place;
+            walk.leave();
             ua = C::UNIT - ua;
             ka = at.k1;
             if constexpr (TURN == C::TURNS - 1) {
