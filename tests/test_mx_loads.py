@@ -8,7 +8,7 @@ import subprocess
 
 import pytest
 
-from mx_cut_shapes import CUT
+from mx_cut_shapes import CUT, FEW, FEW_SPLIT, LARGE, LARGE_SPLIT, TILE, TILE_SPLIT
 from mx_planner import mx_planner  # noqa: F401
 from software_pipelined_tiled_loop_amd import binding as lib
 
@@ -44,3 +44,14 @@ def test_cut_groups_take_the_large_tiles(mx_planner):  # noqa: F811
     for q, (index, splits, _) in zip(queries, plans):
         v = variants[q[0], index]
         assert v["bm"] == 256 and splits == 1 and -(-q[5] // 256) % 4 == 1 and q[5] > 2048, (q, v, splits)
+
+
+def test_places_take_a_kernel_of_each_kind(mx_planner):  # noqa: F811
+    """The sizes at which rows of blocks lie apart, and at which calls are repeated."""
+    for shape, rows, whole in ((FEW, range(16, 65), True), (FEW_SPLIT, range(16, 65), False), (TILE, (128,), True),
+                               (TILE_SPLIT, (128, 256), False), (LARGE, (256,), True), (LARGE_SPLIT, (256,), False)):
+        queries = [(d, f, g) + shape for d in (lib.PGEMM_F16, lib.PGEMM_BF16) for f in (0, 1) for g in (0, 1)]
+        variants, plans = mx_planner(queries)
+        for q, (index, splits, _) in zip(queries, plans):
+            assert variants[q[0], index]["bm"] in rows and (splits == 1) == whole, (q, variants[q[0], index], splits)
+            assert shape != TILE_SPLIT or q[2] or variants[q[0], index]["bm"] == 128
