@@ -532,7 +532,8 @@ int pgemm_gated_backward(int64_t M, int64_t N, int64_t K, const void* dH, int64_
  * behind the last one: ceil(K / 256) * 256 codes (half as many bytes in MX4) and
  * ceil(K / 256) * 8 scales.  Code rows are 16-byte aligned, scale rows 4-byte
  * aligned (pointers and the leading dimensions ldq and lds, in bytes).  Blocks that
- * were not written by mx_quantize or rms_norm have to hold zero codes there too.
+ * were not written by mx_quantize or rms_norm have to hold zero codes there too, and scales
+ * other than 255 (NaN).
  *
  * The products take activations X in either format and weights in MX4, stored
  * W[N][K] (row n holds the weights of output column n); products and scales are
@@ -544,7 +545,8 @@ int pgemm_gated_backward(int64_t M, int64_t N, int64_t K, const void* dH, int64_
  *
  * The norm adds, squares and sums in fp32 and rounds each output once, from fp32;
  * rows whose sum of squares leaves fp32's range come out as the formula gives it
- * with an infinite sum.  MX outputs are taken from the unrounded y.
+ * with an infinite sum, and squares below that range count as zero (which shows where
+ * eps is no larger).  MX outputs are taken from the unrounded y.
  *
  * Nothing depends on the order in which workgroups run: repeated calls give the
  * same bits.  Calls enqueue kernels on `stream`, allocate nothing and can be
@@ -556,7 +558,8 @@ int pgemm_gated_backward(int64_t M, int64_t N, int64_t K, const void* dH, int64_
  * small, a missing or misaligned pointer, an unknown order, activation, format or
  * output type, an eps that is negative or not finite, a workspace too small);
  * TOO_LARGE (rows above 2^31 - 256, a row length or leading dimension of 2^21 or more,
- * a product of 2^36 outputs or more); HIP for a rejected launch. */
+ * a product of 2^24 blocks of 64 x 64 outputs or more, with cut blocks counted whole);
+ * HIP for a rejected launch. */
 enum pgemm_mx { PGEMM_MX8 = 0, PGEMM_MX4 = 1 };
 
 /* Bytes of workspace, or a negative pgemm_status. */
@@ -600,7 +603,9 @@ int pgemm_mx_gated(int64_t M, int64_t N, int64_t K, const void* XQ, int64_t ldxq
                    void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ABI version: major*10000 + minor*100 + patch (a library convention, not
- * from the pages). */
+ * from the pages).  1.1 has the feed-forward operators.  The norm and the
+ * microscaled operators came later and did not raise it: a program that may meet
+ * an older library looks for the symbol pgemm_rms_norm. */
 int pgemm_version(void);
 
 #ifdef __cplusplus

@@ -193,7 +193,8 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, int format, int gated, int dt
 // fp32 outputs of MX8 activations: the scaled MFMAs' sums are not fp32's there, so mx_few
 // multiplies the entries' values (MxFewCfg::WIDE).  With more rows the values are
 // written out once, in bf16, which holds them, and linear_kernel multiplies them: by
-// 4096 x 4096 128 rows take 18 us in mx_few, 38 that way; 256 rows 34 and 36; 512 rows 65 and 43.
+// 4096 x 4096 128 rows take 18 us in mx_few, 38 that way; 256 rows 34 and 36; 512 rows 65 and 42.  Of those 42 the values
+// take 15, the product 22 and its join 6; of 4096 rows' 114 the values 25.
 constexpr int64_t kFewRows = 256;
 bool through_values(int64_t M, int64_t K, int format, int dtype) {
     return format == MX8 && dtype == PGEMM_F32 && M > kFewRows && K > 0;

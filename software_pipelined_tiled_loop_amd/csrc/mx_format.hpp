@@ -33,7 +33,7 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t bits) {
     const uint32_t e = (bits + up) >> 23;
     return bits >= 0x7f800000u ? 255u : e > down ? e - down : 0u;
 }
-// 2^-e, exactly: e + 127 is at most 252 where the entries are finite.
+// 2^-e, exactly: where the entries are finite e + 127 is at most 247 (e4m3) and 253 (e2m1).
 __device__ __forceinline__ float mx_inverse(uint32_t byte) {
     return byte == 255u ? 0.0f : __builtin_bit_cast(float, (254u - byte) << 23);
 }

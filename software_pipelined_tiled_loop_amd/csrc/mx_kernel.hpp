@@ -567,8 +567,8 @@ __global__ void __launch_bounds__(C::NT, C::MINW) mx_tile(MxArgs g) {
 // a workgroup share its outputs (16 FM rows, 16 FNP columns) and deal out the rows'
 // units of 256 entries in turn; each has a ring of its own in LDS, which only it fills
 // and reads, so nothing in the loop waits for another wave.  16 rows by 4096 x 16384 in 4 bits take
-// 9.2 us (36 MB of weights: 3.9 TB/s), 33 by a pair of 8190 x 4001 13.4; one token by 4096 x 4096 5.6 (the launch
-// 2.5 of it).  Three stages, since with weights from memory two take up to 1.4 times as long (one row by
+// 9.2 us with weights from the shared cache (36 MB: 3.9 TB/s) and 11.7 from memory, 33 by a pair of 8190 x 4001
+// 13.4 and 15.4; one token by 4096 x 4096 5.6 (the launch 2.5 of it), by a pair of 8192 x 4096 8.1 and 10.5.  Three stages, since with weights from memory two take up to 1.4 times as long (one row by
 // 4096 x 16384 10.8 and 15.4); a fourth gives nothing.  (Straight from memory to
 // registers, neighbouring lanes hold different rows: four times the accesses to the
 // cache, 14 us for 16 by 4096 x 16384 in 4 bits however much was under way.)

@@ -1,11 +1,13 @@
 // mx_large.hpp -- the microscaled products' kernel for large outputs: tiles of
 // 256 x 256, four waves of 128 x 128, one workgroup a CU.
 //
-// What bounds it is power: scaled MFMAs on 4-bit operands are so cheap that moving
-// the operands costs the part as much, and its clock falls to 1.4 to 1.9 GHz.  So
-//   * 16 x 16 x 128 MFMAs: alone, on random data, 8370 TFLOP/s in 4 bits where
-//     32 x 32 x 64 ones leave the clock lower and reach 7690 (8-bit activations: 4830
-//     and 4570);
+// Scaled MFMAs on 4-bit operands are so cheap that feeding them costs as much, in clocks and
+// in power.  A tile of 4096 entries takes 69400 clocks in 4 bits, 58200 of them in the K loop,
+// where its MFMAs alone take 36400 (8-bit activations: 101500, 90300 and 67100); and on random data the clock
+// is 1.9 to 2.2 GHz (by the card) where zeros, in as many clocks, run at 2.39.  So
+//   * 16 x 16 x 128 MFMAs: alone, on random data, 8290 TFLOP/s in 4 bits at 2.27 GHz where
+//     32 x 32 x 64 ones lower the clock to 1.91 and reach 7490 (8-bit activations:
+//     4860 and 4490);
 //   * codes come in whole 128-byte lines of a row (64 bytes of a row fetch the line
 //     twice), scales 32 bytes of a row at a time, in a ring of their own;
 //   * each code is read once from LDS by each wave that multiplies it.
@@ -29,8 +31,9 @@
 // any later period covers it; where that group is a single period, which in 4 bits
 // a row's last one may be, edge Y of the same period has to (MxLargeWalk::wait_y).
 //
-// 4096^3 in 4 bits takes 40.4 us (3400 TFLOP/s), 8192^3 241 (4560); with MX8 activations 52 and
-// 347 (3170).  Of a tile's 40 us some 10 are its first loads and its epilogue.
+// A call of 4096^3 in 4 bits takes 41 to 42 us (3350 TFLOP/s), 44 with operands that come from memory, of
+// 8192^3 238 (4620) and 247; with MX8 activations 51 and 55, 350 (3140) and 360.  Of a tile's
+// clocks 11000 are its epilogue.
 #pragma once
 
 #include "mx_kernel.hpp"
